@@ -58,6 +58,7 @@ extern "C" {
 /* element types */
 #define MDS_F32 0
 #define MDS_BF16 1
+#define MDS_E4M3 2 /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest value 448, no infinities */
 
 /* sticky status bits (workspace word 0) */
 #define MDS_STATUS_BAD_ANCHOR 1u      /* an anchor token was outside [0, V); token 0 was used */
@@ -65,6 +66,9 @@ extern "C" {
 /* bit 4u is reserved (unused) */
 #define MDS_STATUS_BAD_INDEX 8u       /* an indexed call met a state slot >= n_slots or a cache row outside
                                          [0, n_cache_rows); that row was treated as padding */
+
+#define MDS_STATUS_BAD_PAGE 16u       /* a page id or slot outside the cache: page 0 was read, the row was not written */
+#define MDS_STATUS_NO_PAGES 32u       /* mds_kv_page_tables could not place a request's tokens */
 
 /* sampling salts: the draft salt is the pages' draft-noise salt (1 << 30) */
 #define MDS_SALT_DRAFT (1u << 30)
@@ -488,6 +492,178 @@ int mds_verify_slot_offsets(int b, size_t* counter_offset, size_t* key_offset);
  * bits of a word matter, so 2^23 words cover every possible variate.
  */
 int mds_debug_gumbel(int n, const uint32_t* words, float* gumbel, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The serving operators around the loop: the paged key/value cache (page
+ * tables, append, attention) that the scoring of the K + 1 tokens of every
+ * request runs over, and an LM head from an 8-bit matrix. Conventions as
+ * above; the stream must belong to the current device, and no array may be
+ * written by another stream meanwhile.
+ *
+ * A cache of n_pages pages holds the keys (and one more the values) of
+ * page_size tokens a page, page_size a power of two in [16, 1024]: element
+ * (page, i, head, d) of a page array at page*page_stride + i*slot_stride +
+ * head*head_stride + d, in elements, the array 16-byte aligned and the strides
+ * whole multiples of 16 bytes (else MDS_ERR_UNSUPPORTED). Slot
+ * page*page_size + i names token i of a page. A state slot's block table row
+ * [max_pages] lists its pages in order of position; position p of the request
+ * is token p % page_size of page block_table[s][p / page_size].
+ */
+
+/*
+ * mds_kv_page_tables - pages, positions and slots of the next new tokens of a
+ * batch, from the requests' lengths on the device.
+ *
+ * Batch row b uses state slot s = idx_map[b] (b when idx_map is NULL; then
+ * n_slots >= B); s < 0 is padding. Its context is
+ *   ctx = kv_len[s] + (advance ? advance[b] + advance_add : 0)
+ * tokens (the last verification's num_accepted with advance_add = 1: the
+ * accepted drafts and the anchor), and it gets n = chunk_len[b] >= 0 new ones.
+ * chunk_len[b] < 0 releases the request: its pages go to the end of the free
+ * list in batch order, before any page is taken.
+ * In batch order each request takes max(0, ceil((ctx + n) / page_size) -
+ * pages_held[s]) pages from the end of the free list. A request is refused
+ * (MDS_STATUS_NO_PAGES) when its pages do not fit max_pages or its tokens do
+ * not fit max_tokens, and when the pages it and the requests before it ask
+ * for are more than the list has (a later request that asks for none is not).
+ *
+ * Written (host-known sizes, so the call can be captured):
+ *   block_table     int32 [n_slots, max_pages]: the new entries of rows s only
+ *   query_start     int32 [B + 1]: prefix sums of n (0 for padding and
+ *                   released rows; refused ones keep their rows), at most max_tokens
+ *   seq_lens        int32 [B]: ctx + n; 0 for padding, released and refused rows
+ *   positions       int64 [max_tokens]: ctx + i of each token; 0 behind the last
+ *   slot_map        int64 [max_tokens]: each token's slot; -1 for refused
+ *                   requests and behind the last token
+ *   kv_len_out      int32 [n_slots]: ctx of the batch's slots (0 when released)
+ *   pages_held_out  int32 [n_slots]: their pages
+ *   free_list       int32 [n_pages]: the released pages, from entry free_count[0] on
+ *   free_count_out  int32 [1]
+ * kv_len_out, pages_held_out and free_count_out may be their inputs (a serving
+ * loop's state); entries of slots outside the batch are left as they are. The
+ * other outputs must not overlap anything. Counts out of range (pages_held
+ * outside [0, max_pages], free_count outside [0, n_pages], ctx outside
+ * [0, 2^31)) are clamped, and released pages past n_pages dropped, with
+ * MDS_STATUS_BAD_INDEX. A slot named by two rows, or >= n_slots, makes all
+ * those rows padding, with MDS_STATUS_BAD_INDEX.
+ *   status          device uint32 or NULL: MDS_STATUS_* bits are OR-ed in
+ * Limits: B <= 65535, n_slots <= 2^17, max_pages*page_size <= 2^30, max_tokens <= 2^24.
+ * One launch for up to 4096 tokens, two above.
+ */
+int mds_kv_page_tables(int B, int n_slots, int max_pages, int page_size, int n_pages, int max_tokens,
+                       const int32_t* idx_map, const int32_t* kv_len, const int32_t* advance, int advance_add,
+                       const int32_t* chunk_len, int32_t* block_table, const int32_t* pages_held,
+                       int32_t* free_list, const int32_t* free_count, int32_t* query_start, int32_t* seq_lens,
+                       int64_t* positions, int64_t* slot_map, int32_t* kv_len_out, int32_t* pages_held_out,
+                       int32_t* free_count_out, uint32_t* status, void* stream);
+
+/*
+ * mds_kv_append - writes the keys and values of T tokens into the cache.
+ *   k, v          bf16 [T, Hkv, D], element (t, h, d) at t*token_stride +
+ *                 h*head_stride + d; 16-byte aligned, strides multiples of 8;
+ *                 D a multiple of 16, at most 1024
+ *   k_pages, v_pages  MDS_BF16 (copied) or MDS_E4M3: the float32 quotient by
+ *                 k_scale[h] / v_scale[h], clamped to +-448 and rounded to
+ *                 nearest even (NaN stays NaN); strides in elements
+ *   slot_map      int64 [T]: the token's slot; < 0 skips the row, a slot past
+ *                 the cache is skipped with MDS_STATUS_BAD_PAGE. Two rows with
+ *                 one slot leave either's values.
+ *   k_scale, v_scale  float [Hkv], required for MDS_E4M3
+ *   status        device uint32 or NULL
+ * One launch; nothing but the named slots is written.
+ */
+int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_token_stride, int64_t v_head_stride, void* k_pages, void* v_pages, int cache_dtype,
+                  int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
+                  int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
+                  int64_t v_pages_head_stride, const int64_t* slot_map, const float* k_scale, const float* v_scale,
+                  uint32_t* status, void* stream);
+
+/*
+ * mds_paged_attention - attention of every request's new tokens over its cache
+ * (the new tokens' own keys and values included: append them first).
+ *
+ * Request b's tokens are rows query_start[b] .. query_start[b + 1] - 1 of q;
+ * with n of them, token i stands at position P = seq_lens[b] - n + i and sees
+ * the keys j < seq_lens[b] with j <= P if causal (1) and j > P - window if
+ * window > 0. For query head h, key head h / (Hq / Hkv):
+ *   x_j = scale * q . k_j (* k_scale),  lse = log sum_j exp(x_j),
+ *   out = sum_j exp(x_j - lse) v_j (* v_scale)
+ * A token that sees no key (also: a padding request's) gets out = 0 and
+ * lse = -inf. Sums and the softmax are float32, the probabilities rounded to
+ * bf16 for the second product, out rounded to bf16.
+ *
+ *   q             bf16 [T, Hq, D] (strides as k in mds_kv_append), D 64 or 128
+ *                 (else MDS_ERR_UNSUPPORTED), Hq a multiple of Hkv
+ *   block_table   int32 [n_slots, max_pages]; idx_map int32 [B] or NULL as for
+ *                 mds_kv_page_tables (a slot < 0 or >= n_slots has no keys)
+ *   query_start   int32 [B + 1], from 0, not decreasing, at most T
+ *   seq_lens      int32 [B]
+ *   max_q_len     no request has more new tokens (a host bound: what is
+ *                 past it is not computed, MDS_STATUS_BAD_INDEX)
+ *   max_seq_len   no sequence is longer, as a guess: it steers how the work is
+ *                 cut; results do not depend on it beyond float32 rounding
+ *   scale         > 0 (1 / sqrt(D))
+ *   k_scale, v_scale  float [Hkv], > 0, or NULL (1): MDS_E4M3 caches
+ *   out           bf16 [T, Hq, D] as q; rows behind query_start[B] are not written
+ *   lse           float [T, Hq] contiguous, or NULL
+ *   workspace     >= mds_paged_attention_workspace_bytes(...), 256-byte
+ *                 aligned; its first word is a sticky status word (zero it
+ *                 once); the rest needs no clearing
+ * Keys past max_pages*page_size are not seen (MDS_STATUS_BAD_INDEX); a page id
+ * outside [0, n_pages) reads page 0 (MDS_STATUS_BAD_PAGE). Cache slots behind
+ * a sequence's end and keys that no token of a request sees are never read.
+ * Two launches when the keys are split over work-groups, else one; equal
+ * inputs give equal bits.
+ */
+int mds_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len,
+                                        int window, size_t* out_bytes);
+int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
+                        int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
+                        int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
+                        int64_t v_pages_head_stride, const int32_t* block_table, int n_slots, int max_pages,
+                        const int32_t* idx_map, const int32_t* query_start, const int32_t* seq_lens, int max_q_len,
+                        int64_t max_seq_len, float scale, int causal, int window, const float* k_scale,
+                        const float* v_scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The LM head from an 8-bit matrix: lm_head [V, H] in MDS_E4M3 with one
+ * float32 scale for each block of 128 rows by 128 columns, scales
+ * [ceil(V / 128), H / 128] contiguous (weight = code * scale), H a multiple of
+ * 128, 128 <= H <= 65536, 2 <= V < 2^24.
+ *
+ * Tiled order: code (v, c) at ((v / 16) * (H / 128) + c / 128) * 2048 +
+ * ((c % 128) / 16) * 256 + (v % 16) * 16 + c % 16 of an array of
+ * 16 * ceil(V / 16) * H bytes (mds_lm_head_fp8_tiled_bytes); rows past V zero.
+ * mds_tile_lm_head_fp8 makes it from row-major codes [V, H] (a checkpoint that
+ * has block scales already); mds_quantize_lm_head_fp8 from a bf16 matrix [V, H]:
+ * scale = max(largest magnitude of the block, 2^-100) / 448, code = the
+ * float32 quotient by it, rounded to nearest even. Both: 16-byte aligned,
+ * not overlapping, one launch.
+ */
+int mds_lm_head_fp8_tiled_bytes(int V, int H, size_t* out_bytes);
+int mds_tile_lm_head_fp8(int V, int H, const void* codes, void* tiled, size_t tiled_bytes, void* stream);
+int mds_quantize_lm_head_fp8(int V, int H, const void* lm_head, void* tiled, size_t tiled_bytes, float* scales,
+                             void* stream);
+
+/*
+ * mds_lm_head_fp8 - mds_draft_lm_head with the 8-bit matrix: logits of B*K
+ * rows (the draft model's K steps, or the target's K + 1 rows a request).
+ * Each hidden row is quantised in blocks of 128 columns as the matrix is
+ * (scale = max(amax, 2^-100) / 448, code = float32 quotient, nearest even), and
+ *   out[b, k, v] = sum over blocks of sx * sw * (sum of code products),
+ * the products exact, all sums float32. A row with a NaN or infinity gives NaN
+ * logits. Arguments as for mds_draft_lm_head, with 1 <= K <= 64; lm_head in
+ * the tiled order, 16-byte aligned; workspace of
+ * mds_lm_head_fp8_workspace_bytes(B, K, V, H), 256-byte aligned, without state.
+ * Two launches; the matrix is read once for up to 224 rows.
+ */
+int mds_lm_head_fp8_workspace_bytes(int B, int K, int V, int H, size_t* out_bytes);
+int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidden_row_stride, const void* lm_head,
+                    const float* scales, void* out, int out_dtype, int64_t out_req_stride, int64_t out_step_stride,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

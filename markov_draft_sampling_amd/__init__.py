@@ -20,11 +20,13 @@ __all__ = [
     "new_workspace", "workspace_status", "verify_slot_offsets", "markov_w2_tiled_bytes", "tile_markov_w2",
     "markov_draft_loop", "markov_draft_loop_noalloc", "markov_draft_loop_timed", "rejection_verify",
     "debug_noise", "debug_gumbel", "debug_top_p", "STATUS_BAD_ANCHOR", "STATUS_BAD_DRAFT", "STATUS_BAD_INDEX", "SALT_DRAFT", "SALT_ACCEPT",
-    "SALT_RESAMPLE",
+    "SALT_RESAMPLE", "E4M3", "STATUS_BAD_PAGE", "STATUS_NO_PAGES", "kv_page_tables", "kv_append",
+    "paged_attention_workspace_bytes", "paged_attention", "lm_head_fp8_tiled_bytes", "tile_lm_head_fp8",
+    "quantize_lm_head_fp8", "lm_head_fp8_workspace_bytes", "lm_head_fp8",
 ]
 
-F32, BF16 = 0, 1
-STATUS_BAD_ANCHOR, STATUS_BAD_DRAFT, STATUS_BAD_INDEX = 1, 2, 8
+F32, BF16, E4M3 = 0, 1, 2
+STATUS_BAD_ANCHOR, STATUS_BAD_DRAFT, STATUS_BAD_INDEX, STATUS_BAD_PAGE, STATUS_NO_PAGES = 1, 2, 8, 16, 32
 SALT_DRAFT, SALT_ACCEPT, SALT_RESAMPLE = 1 << 30, 1, 2
 DRAFT_FP64_GUMBEL, DRAFT_W2_TILED = 1, 2
 
@@ -77,6 +79,18 @@ _SIGS = {
     "mds_verify_slot_offsets": ([_c_int, ctypes.POINTER(_c_sz), ctypes.POINTER(_c_sz)], _c_int),
     "mds_markov_draft_loop_noalloc": ([_c_int] * 4 + [_vp, _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                                       _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _vp], _c_int),
+    "mds_kv_page_tables": ([_c_int] * 6 + [_vp, _vp, _vp, _c_int] + [_vp] * 14, _c_int),
+    "mds_kv_append": ([_c_int] * 3 + [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3
+                      + [_c_i64] * 6 + [_vp] * 5, _c_int),
+    "mds_paged_attention_workspace_bytes": ([_c_int] * 6 + [_c_i64, _c_int, ctypes.POINTER(_c_sz)], _c_int),
+    "mds_paged_attention": ([_c_int] * 5 + [_vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3 + [_c_i64] * 6
+                            + [_vp, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_i64, ctypes.c_float, _c_int, _c_int, _vp,
+                               _vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_sz, _vp], _c_int),
+    "mds_lm_head_fp8_tiled_bytes": ([_c_int, _c_int, ctypes.POINTER(_c_sz)], _c_int),
+    "mds_tile_lm_head_fp8": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp], _c_int),
+    "mds_quantize_lm_head_fp8": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _vp], _c_int),
+    "mds_lm_head_fp8_workspace_bytes": ([_c_int] * 4 + [ctypes.POINTER(_c_sz)], _c_int),
+    "mds_lm_head_fp8": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp, _c_sz, _vp], _c_int),
     "mds_debug_top_p": ([_c_int, _c_int, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_sz, _vp], _c_int),
 }
 
@@ -582,3 +596,18 @@ def debug_top_p(target, temperature, top_p):
                                   _ptr(cut), _ptr(log_z), _ptr(on), _ptr(ws), ws.numel(), _stream(None, target.device)),
            "debug_top_p")
     return tau.to(torch.int64) & 0xFFFFFFFF, cut, log_z, on
+
+
+# the serving operators live in a module of their own, which needs torch when it is imported
+_SERVING = ("kv_page_tables", "kv_append", "paged_attention_workspace_bytes", "paged_attention",
+            "lm_head_fp8_tiled_bytes", "tile_lm_head_fp8", "quantize_lm_head_fp8", "lm_head_fp8_workspace_bytes",
+            "lm_head_fp8")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import _serving
+        fn = getattr(_serving, name)
+        globals()[name] = fn
+        return fn
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

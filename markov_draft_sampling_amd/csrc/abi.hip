@@ -475,6 +475,23 @@ int draft_wave_slabs(int V, int cus, int bt) {
 }
 }  // namespace mds
 
+namespace mds {
+
+int abi_fail(int code, const char* msg) {
+  try {
+    g_last_error = msg;
+  } catch (...) {  // no memory for the message: the code still says what failed
+  }
+  return code;
+}
+
+int abi_ok() {
+  g_last_error.clear();
+  return MDS_OK;
+}
+
+}  // namespace mds
+
 extern "C" {
 
 int mds_abi_version(void) { return MDS_ABI_VERSION; }
