@@ -463,7 +463,7 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
       }
     }
   }
-  if (bad && lane == 0) set_status(a.status, bad);
+  if (bad) set_status(a.status, bad);
 
   // join the four waves, 16 rows at a time: o scaled to the common maximum through LDS, summed by
   // 16 threads a row

@@ -1,0 +1,289 @@
+"""Paged attention on the GPU against the float64 reference within bounds
+derived from its roundings: head layouts, ragged and empty requests, masks
+that leave a row nothing, windows, page sizes, strides, both cache types,
+split and unsplit keys, stale memory behind the sequences."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+import serving_ref as sr
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(ctx, chunk, Hq, Hk, D, P, cache="bf16", causal=True, window=0, pad=3, seed=0, layout="nhd", idx=False,
+          scale=None, poison=True, max_q=None, max_seq=None, qgain=1.5, q_layout="thd"):
+    """Runs the call and the reference; returns (out, lse, reference tuple, tolerance inputs)."""
+    import torch
+    import markov_draft_sampling_amd as mds
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    B = len(ctx)
+    seq = [a + n for a, n in zip(ctx, chunk)]
+    held = [max(1, -(-x // P)) for x in seq]
+    NP = sum(held) + 2
+    pages = rng.permutation(NP - 1) + 1  # page 0 belongs to nobody
+    MP = max(held) + 2
+    n_slots = B + 4 if idx else B
+    slots = rng.permutation(n_slots)[:B] if idx else np.arange(B)
+    table = np.full((n_slots, MP), -123456, np.int32)  # garbage behind the pages
+    at = 0
+    for b in range(B):
+        table[slots[b], :held[b]] = pages[at:at + held[b]]
+        at += held[b]
+    T = sum(chunk)
+    q = (torch.randn((T + pad, Hq, D), generator=g) * qgain).to(torch.bfloat16)
+    kv, dev = [], []
+    for _ in range(2):
+        x = torch.randn((NP, P, Hk, D), generator=g)
+        if cache == "e4m3":
+            x = (x * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+        else:
+            x = x.to(torch.bfloat16)
+        kv.append(x.float())
+        d = x.clone()
+        if poison:  # nothing behind a sequence's end may be read into a result
+            nan = torch.tensor(float("nan")).to(x.dtype)
+            for b in range(B):
+                for p in range(seq[b], held[b] * P):
+                    d.view(torch.uint8 if cache == "e4m3" else x.dtype)[table[slots[b], p // P], p % P] = \
+                        nan.view(torch.uint8) if cache == "e4m3" else nan
+            d.view(torch.uint8 if cache == "e4m3" else x.dtype)[0] = nan.view(torch.uint8) if cache == "e4m3" else nan
+        d = d.cuda()
+        if layout == "hnd":
+            d = d.view(torch.uint8).transpose(1, 2).contiguous().transpose(1, 2).view(d.dtype) if cache == "e4m3" \
+                else d.transpose(1, 2).contiguous().transpose(1, 2)
+        elif layout == "padded":
+            wide = torch.zeros((NP, P, Hk + 1, D + 32), dtype=torch.uint8 if cache == "e4m3" else d.dtype, device="cuda")
+            wide[:, :, :Hk, :D] = d.view(wide.dtype)
+            d = wide.view(d.dtype)[:, :, :Hk, :D]
+        dev.append(d)
+    ks = vs = None
+    if cache == "e4m3":
+        ks = torch.tensor(rng.uniform(0.9, 1.1, Hk) / 60, dtype=torch.float32)
+        vs = torch.tensor(rng.uniform(0.9, 1.1, Hk) / 60, dtype=torch.float32)
+    qs = np.concatenate([[0], np.cumsum(chunk)]).astype(np.int32)
+    qd = q.cuda()
+    out = torch.full((T + pad, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    if q_layout == "htd":
+        qd = qd.transpose(0, 1).contiguous().transpose(0, 1)
+        out = out.transpose(0, 1).contiguous().transpose(0, 1)
+    lse = torch.full((T + pad, Hq), 7.0, device="cuda")
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = dict(scale=scale, causal=causal, window=window, idx_map=t(slots) if idx else None,
+                k_scale=None if ks is None else ks.cuda(), v_scale=None if vs is None else vs.cuda(), lse=lse)
+    mq = max(chunk) if max_q is None else max_q
+    ms = max(seq) if max_seq is None else max_seq
+    print(f"paged attention ctx {list(ctx)[:6]} chunk {list(chunk)[:6]} Hq {Hq} Hk {Hk} D {D} P {P} {cache} "
+          f"causal {causal} window {window}", flush=True)
+    ws = mds.paged_attention(qd, dev[0], dev[1], t(table), t(qs), t(seq), out, mq, ms, **args)
+    torch.cuda.synchronize()
+    assert mds.workspace_status(ws) == 0
+    sc = 1 / math.sqrt(D) if scale is None else scale
+    ref = sr.attention(q, kv[0], kv[1], table, qs, seq, sc, causal, window, slots if idx else None, ks, vs)
+    again = out.clone()
+    mds.paged_attention(qd, dev[0], dev[1], t(table), t(qs), t(seq), out, mq, ms, workspace=ws, **args)
+    assert torch.equal(again, out)  # equal inputs, equal bits
+    o, z = out.cpu(), lse.cpu()
+    assert (o[T:] == 7.0).all() and (z[T:] == 7.0).all()  # rows behind the last token
+    _check(o[:T], z[:T], ref, D, max(seq), T)
+    return o, z
+
+
+def _check(o, z, ref, D, L, T):
+    import torch
+    r, rl, A, S = (x[:T] for x in ref)
+    tol, ltol = sr.attention_tolerance(r, A, S, D, L)
+    err = (o.double() - r).abs()
+    assert (err <= tol).all(), (float((err / tol).max()), torch.nonzero(err > tol)[:4].tolist())
+    none = rl == -math.inf
+    assert (z[none] == -math.inf).all() and (o[none] == 0).all()
+    e = (z.double() - rl).abs()[~none]
+    assert (e <= ltol[~none]).all(), float((e / ltol[~none]).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (8, 2), (6, 2), (5, 1), (16, 16)])
+def test_single_tokens(D, cache, Hq, Hk):
+    _case([0, 1, 15, 16, 31, 32, 33, 200, 511], [1] * 9, Hq, Hk, D, 16, cache)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 3, 4, 8])
+def test_verification_chunks(D, cache, G):
+    _case([0, 5, 30, 100, 333], [8, 8, 8, 8, 8], 2 * G, 2, D, 32, cache, seed=G)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 7), (True, 40), (False, 20),
+                                           (True, 10 ** 6)])
+def test_masks(causal, window):
+    _case([0, 3, 17, 64, 250], [7, 0, 5, 9, 1], 4, 2, 64, 16, causal=causal, window=window, seed=3)
+
+
+@pytest.mark.parametrize("P", [16, 32, 128, 1024])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "padded"])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_pages_and_strides(P, layout, cache):
+    _case([0, 100, 300], [3, 4, 2], 4, 2, 128, P, cache, layout=layout, idx=True, seed=P)
+
+
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+def test_prompt_chunks(D, cache):
+    _case([0, 40, 130], [150, 1, 77], 4, 2, D, 16, cache, seed=9, q_layout="htd")
+
+
+def test_prompt_with_window_and_both_ways():
+    _case([100], [130], 3, 1, 64, 16, window=50, seed=1)
+    _case([100], [130], 3, 1, 128, 16, causal=False, seed=2)
+
+
+def test_split_keys_and_wrong_guess_of_the_longest():
+    # the keys split over work-groups; a guess that is too small or too large changes nothing but rounding
+    for ms in (None, 100, 40000):
+        _case([2000, 900, 10], [2, 1, 3], 4, 1, 128, 16, seed=4, max_seq=ms)
+    _case([3000], [1], 2, 2, 64, 64, "e4m3", seed=5)
+    _case([5000], [2], 1, 1, 64, 16, window=700, seed=5)
+
+
+def test_many_requests_and_empty_ones():
+    rng = np.random.default_rng(0)
+    ctx = rng.integers(0, 60, 130).tolist()
+    chunk = rng.choice([0, 1, 2, 8], 130).tolist()
+    _case(ctx, chunk, 2, 1, 64, 16, seed=6)
+    chunk[77] = 90  # one prompt among them: tiles are found by row offset
+    _case(ctx, chunk, 2, 1, 64, 16, seed=7)
+
+
+def test_requests_without_keys_give_zero():
+    import torch
+    import markov_draft_sampling_amd as mds
+    # seq_lens 0 (refused), shorter than the chunk (its first tokens stand before position 0), a padding slot
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp = torch.randn(6, 16, 1, 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(9, 2, 64, device="cuda").to(torch.bfloat16)
+    out, lse = torch.full_like(q, 3.0), torch.full((9, 2), 3.0, device="cuda")
+    table = t([[1, 2], [3, 4], [5, 0]])
+    ws = mds.paged_attention(q, kp, kp, table, t([0, 3, 6, 9]), t([0, 2, 5]), out, 3, 32, idx_map=t([0, 1, -1]), lse=lse)
+    torch.cuda.synchronize()
+    assert mds.workspace_status(ws) == 0
+    none = torch.tensor([1, 1, 1, 1, 0, 0, 1, 1, 1], dtype=torch.bool)
+    assert (out.cpu()[none] == 0).all() and (lse.cpu()[none] == -math.inf).all()
+    # token 1 of request 1 stands at position 0: it sees one key
+    assert torch.equal(out[4, 0], kp[3, 0, 0]) and torch.isfinite(lse[4:6]).all()
+
+
+def test_out_of_contract_device_data_is_flagged_and_stays_in_bounds():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp = torch.randn(4, 16, 1, 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(4, 1, 64, device="cuda").to(torch.bfloat16)
+
+    def run(table, qs, seq, idx=None, mq=4):
+        out = torch.zeros_like(q)
+        ws = mds.paged_attention(q, kp, kp, t(table), t(qs), t(seq), out, mq, 32, idx_map=idx)
+        torch.cuda.synchronize()
+        return mds.workspace_status(ws), out
+
+    st, out = run([[1, 99]], [0, 2], [20])  # a page outside the cache: page 0 is read
+    st2, out2 = run([[1, 0]], [0, 2], [20])
+    assert st == 16 and st2 == 0 and torch.equal(out, out2)
+    st, out = run([[1, 2]], [0, 1], [1000])  # longer than the table's row
+    assert st == 8 and torch.isfinite(out).all()
+    st, _ = run([[1, 2]], [0, 700], [20])  # tokens past the rows of q
+    assert st & 8
+    st, _ = run([[1, 2], [1, 2]], [0, 3, 1], [20, 20])  # decreasing starts
+    assert st & 8
+    st, out = run([[1, 2]], [0, 2], [20], idx=t([5]))  # a slot past the table
+    assert st == 8 and (out == 0).all()
+    st, _ = run([[1, 2]], [0, 4], [20], mq=1)  # more tokens than max_q_len: flagged when they do not fit its tiles
+    assert st in (0, 8)
+
+
+def test_large_scores_and_a_peak_late_in_the_row():
+    # scores up to some hundreds: the running maximum has to move many times
+    _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
+
+
+def test_offsets_past_32_bits():
+    # pages whose offset passes 2^31 bytes and 2^31 elements: a strided view over a large buffer
+    import torch
+    import markov_draft_sampling_amd as mds
+    P, D, stride = 16, 64, 1 << 30  # elements from page to page
+    big = torch.zeros(4 * stride, dtype=torch.bfloat16, device="cuda")
+    kp = big.as_strided((4, P, 1, D), (stride, D, D, 1))
+    small = torch.randn(4, P, 1, D, device="cuda").to(torch.bfloat16)
+    kp.copy_(small)
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn(2, 2, D, device="cuda").to(torch.bfloat16)
+    outs = []
+    for pages in (kp, small):
+        out = torch.zeros_like(q)
+        mds.paged_attention(q, pages, pages, t([[3, 1, 2, 0]]), t([0, 2]), t([60]), out, 2, 64)
+        outs.append(out)
+    assert torch.equal(*outs)
+    slots = torch.tensor([3 * P + 5, 1], dtype=torch.int64, device="cuda")
+    kv = torch.randn(2, 1, D, device="cuda").to(torch.bfloat16)
+    mds.kv_append(kv, kv, kp, kp.clone(), slots)
+    assert torch.equal(kp[3, 5], kv[0]) and torch.equal(kp[0, 1], kv[1])
+
+
+def test_graph_replays_and_a_side_stream():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    g0 = torch.Generator().manual_seed(1)
+    kp = torch.randn((300, 16, 2, 128), generator=g0).to(torch.bfloat16).cuda()
+    q = torch.randn((16, 8, 128), generator=g0).to(torch.bfloat16).cuda()
+    table = t(np.random.default_rng(0).permutation(300)[:256].reshape(2, 128))
+    qs, seq = t([0, 8, 16]), t([2000, 100])
+    out, lse = torch.zeros_like(q), torch.zeros(16, 8, device="cuda")
+    ws = mds.new_workspace(mds.paged_attention_workspace_bytes(16, 2, 8, 2, 128, 8, 2048))
+    call = lambda o: mds.paged_attention(q, kp, kp, table, qs, seq, o, 8, 2048, lse=lse, workspace=ws)  # noqa: E731
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out)
+    for i in range(5):
+        seq.copy_(t([2000 - 300 * i, 100 + i]))
+        q.copy_(torch.randn((16, 8, 128), generator=g0).to(torch.bfloat16).cuda())
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        want = torch.zeros_like(q)
+        mds.paged_attention(q, kp, kp, table, qs, seq, want, 8, 2048)
+        assert torch.equal(out, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = torch.zeros_like(q)
+    side.wait_stream(torch.cuda.current_stream())
+    mds.paged_attention(q, kp, kp, table, qs, seq, got, 8, 2048, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_refuses_mismatched_tensors():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16, device="cuda")
+    ok = dict(q=q, k=kp, v=kp, table=t([[0, 1]]), qs=t([0, 4]), seq=t([4]), out=torch.zeros_like(q))
+
+    def run(**kw):
+        a = {**ok, **{k: v for k, v in kw.items() if k in ok}}
+        extra = {k: v for k, v in kw.items() if k not in ok}
+        mds.paged_attention(a["q"], a["k"], a["v"], a["table"], a["qs"], a["seq"], a["out"], 4, 4, **extra)
+
+    run()
+    for bad in (dict(q=q.half()), dict(q=q.cpu()), dict(v=kp[:1]), dict(table=t([0, 1])), dict(qs=t([0])),
+                dict(seq=t([4]).long()), dict(out=torch.zeros(4, 4, 32, dtype=torch.bfloat16, device="cuda")),
+                dict(k=kp.half(), v=kp.half()), dict(lse=torch.zeros(3, device="cuda")), dict(idx_map=t([0, 0])),
+                dict(k_scale=torch.ones(2, device="cuda")), dict(scale=-1.0), dict(window=-3),
+                dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(mds.MdsError):
+            run(**bad)
