@@ -4,28 +4,35 @@
 // and the hidden rows quantised on the way in: for each row and 128 columns
 // sx = max(amax, 2^-100) / 448 and qx = e4m3(x / sx), nearest even.
 //
-// Products of codes are exact and summed in float32 by the matrix cores
-// (16x16x128 of 8-bit operands, twice the bf16 rate); each block's sum is
-// scaled once and added to the float32 total.
+// Codes widen to bf16 exactly and their products are summed by the bf16 matrix
+// instruction, whose sums are float32: the 8-bit one, twice as fast, drops low
+// bits of its products before they are added (measured on 16 x 16 x 128 of
+// normal codes: 1.5e-5 of the result's norm off, against 9e-9 here), which
+// a float32 logit shows. Each half block of 64 columns is scaled and added to
+// the float32 total.
 //
-// The call is bound by the matrix: V * H bytes, read once from HBM for up to
-// 256 rows. It is kept in tiles of 16 rows by 128 columns in operand order
-// (fp8_tile_index), so that a wave reads its operands straight into registers
-// as two 1 KB runs and no LDS pass is needed; which 16 columns a lane holds
-// does not matter as long as both operands agree. The quantised hidden rows
-// are written in the same tiles by the quantising kernel and copied chunk by
-// chunk into LDS, three chunks deep, shared by the work-group's eight waves.
+// The matrix is kept in tiles of 16 rows by 128 columns in operand order
+// (fp8_tile_index): a wave reads its operands straight into registers as 1 KB
+// runs, a chunk (128 columns) or more ahead, and widens them there; which
+// columns a lane holds does not matter as long as both operands agree. The
+// quantising kernel writes the hidden rows' codes, widened to bf16, in the
+// same order, chunk by chunk with the rows' scales behind, so that a chunk goes
+// into LDS as one linear copy without registers, shared by the waves.
+//
+// Bound by the matrix's V * H bytes for few rows; at 224 rows by the matrix
+// cores and the LDS reads of the hidden rows, which is why a wave takes 64
+// vocabulary rows (every hidden operand serves four products) and two waves
+// share a vocabulary tile, each with half the hidden rows.
 #include "mds_device.h"
 #include "mds_internal.h"
 
 namespace mds {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxFloor = 0x1p-100f;  // a block of zeros gets a scale it can be divided by
 constexpr int kStagger = 5;  // chunk offset between consecutive work-groups
-constexpr int kUnitScales = 0x7F7F7F7F;  // 2^0 for every operand block of the scaled matrix instruction
 
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
   const int p = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -36,7 +43,17 @@ __device__ __forceinline__ float clamp_e4m3(float y) {
   return y != y ? y : fminf(fmaxf(y, -kE4m3Max), kE4m3Max);
 }
 
+// Two codes of a word to two bf16 (exact: every e4m3 value is one)
+__device__ __forceinline__ uint32_t widen(uint32_t v, bool up) {
+  return up ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true))
+            : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+}
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
+  return __builtin_bit_cast(bf16x8, u32x4{widen(lo, false), widen(lo, true), widen(hi, false), widen(hi, true)});
+}
+
 // Hidden rows: a wave per 16 rows and 128 columns, a lane 32 columns of a row.
+// Column c of row r of a block goes to 1 KB run c / 64 * 2 + c / 8 % 2, lane (c / 16 % 4) * 16 + r of it.
 __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int HB = a.H >> 7, MBt = (a.M + 15) >> 4;
   const int wv = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -46,25 +63,23 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int r = lane >> 2, m = mb * 16 + r, c0 = (lane & 3) * 32;
   const int mt = mb / a.mb, mi = mb - mt * a.mb;
   uint8_t* stage = a.xq + ((size_t)mt * HB + j) * fp8_stage_bytes(a.mb);
-  uint8_t* dst = stage + mi * 2048 + r * 16;
-  float* xs = (float*)(stage + a.mb * 2048) + mi * 16 + r;
-  const int p0 = (lane & 3) * 2;
-  if (m >= a.M) {
-    *(u32x4*)(dst + p0 * 256) = u32x4{0, 0, 0, 0};
-    *(u32x4*)(dst + p0 * 256 + 256) = u32x4{0, 0, 0, 0};
-    if ((lane & 3) == 0) *xs = 0.0f;
-    return;
-  }
-  const uint16_t* src = a.hidden + (long long)m * a.hidden_rs + j * 128 + c0;
+  uint8_t* dst = stage + mi * 4096 + (c0 >> 6) * 2048 + ((c0 >> 4 & 3) * 16 + r) * 16;
+  float* xs = (float*)(stage + a.mb * 4096) + mi * 16 + r;
   float x[32];
+  if (m < a.M) {
+    const uint16_t* src = a.hidden + (long long)m * a.hidden_rs + j * 128 + c0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const u32x4 v = *(const u32x4*)(src + q * 8);
+    for (int q = 0; q < 4; ++q) {
+      const u32x4 v = *(const u32x4*)(src + q * 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[q * 8 + 2 * i] = __uint_as_float(v[i] << 16);
-      x[q * 8 + 2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+      for (int i = 0; i < 4; ++i) {
+        x[q * 8 + 2 * i] = __uint_as_float(v[i] << 16);
+        x[q * 8 + 2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+      }
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
   }
   float am = kAmaxFloor;
 #pragma unroll
@@ -72,13 +87,16 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   am = fmaxf(am, __shfl_xor(am, 1));
   am = fmaxf(am, __shfl_xor(am, 2));
   const float s = am / kE4m3Max;
-  uint32_t w[8];
+  // 16 columns (two runs) from c0, 16 from c0 + 16 (the next 16 lanes of the same runs)
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = quant4(clamp_e4m3(x[4 * i] / s), clamp_e4m3(x[4 * i + 1] / s), clamp_e4m3(x[4 * i + 2] / s),
-                  clamp_e4m3(x[4 * i + 3] / s));
-  *(u32x4*)(dst + p0 * 256) = u32x4{w[0], w[1], w[2], w[3]};
-  *(u32x4*)(dst + p0 * 256 + 256) = u32x4{w[4], w[5], w[6], w[7]};
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float* y = x + q * 16 + e * 8;
+      const uint32_t lo = quant4(clamp_e4m3(y[0] / s), clamp_e4m3(y[1] / s), clamp_e4m3(y[2] / s), clamp_e4m3(y[3] / s));
+      const uint32_t hi = quant4(clamp_e4m3(y[4] / s), clamp_e4m3(y[5] / s), clamp_e4m3(y[6] / s), clamp_e4m3(y[7] / s));
+      *(bf16x8*)(dst + e * 1024 + q * 256) = widen8(lo, hi);
+    }
   if ((lane & 3) == 0) *xs = s;
 }
 
@@ -93,32 +111,33 @@ __device__ __forceinline__ void chunk_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 16 x 16 sums over 128 columns of e4m3 codes
-__device__ __forceinline__ floatx4 product(i32x8 a, i32x8 b) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, kUnitScales,
-                                                          0, kUnitScales);
-}
-
 // 16 bytes a lane straight into LDS
 __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t rs, uint8_t* to, int lane_off, int off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, lane_off, off, 0, 0);
 }
 
-// MB: 16-row blocks of hidden rows; NBW: 16-row vocabulary blocks per wave; eight waves.
-template <int MB, int NBW>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_kernel(LmHeadFp8Args a) {
-  constexpr int NW = 8;
-  constexpr int kStage = fp8_stage_bytes(MB);    // a chunk's hidden rows and their scales
-  constexpr int kCopy = kStage / 1024;           // 1 KB copies of it, dealt to the waves in turn
+// A work-group has MW x VW waves: wave (wm, wv) takes MB 16-row blocks of hidden rows from wm * MB and NBW
+// 16-row blocks of the vocabulary. NST chunks of hidden rows in LDS, R chunks of the matrix in registers.
+template <int MB, int NBW, int MW, int VW, int NST, int R>
+__global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_kernel(
+    LmHeadFp8Args a) {
+  static_assert((NST == 2 || NST == 4) && NST % R == 0 && 8 % NBW == 0, "ring sizes, one scale block a wave");
+  constexpr int NW = MW * VW;
+  constexpr int kStage = fp8_stage_bytes(MB * MW);  // a chunk's hidden rows and their scales
+  constexpr int kCopy = kStage / 1024;              // 1 KB copies of it, dealt to the waves in turn
   constexpr int kQ = (kCopy + NW - 1) / NW;
-  constexpr int kLoads = 2 * NBW + 1;            // a wave's loads of a chunk of the matrix
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kStage], s_x1[kStage], s_x2[kStage];
+  constexpr int kLoads = 2 * NBW + 1;               // a wave's loads of a chunk of the matrix
+  // newer operations than the copies of the next chunk: its loads, and all of the chunks after it
+  constexpr int kNewer = kLoads + (NST - 2) * (kQ + kLoads);
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kStage], s_x1[kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x2[NST > 2 ? kStage : 16], s_x3[NST > 2 ? kStage : 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / VW, wv = w % VW;
   const int lr = lane & 15, lg = lane >> 4;
   const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
-  const int mb0 = blockIdx.y * MB;
-  const int vb0 = (blockIdx.x * NW + w) * NBW;   // first 16-row block of this wave
+  const int mb0 = (blockIdx.y * MW + wm) * MB;
+  const int vb0 = (blockIdx.x * VW + wv) * NBW;  // first 16-row block of this wave
   const int coff = (int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB);
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
 
@@ -136,17 +155,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       copy_1k(xrs, buf + p * 1024, lane * 16, chunk_of(c) * kStage + p * 1024);
     }
   };
-  i32x8 A[3][NBW];
-  float ws[3];
-  auto aload = [&](int slot, int c) {
-    const int j = chunk_of(c);
+  u32x4 raw[R][2][NBW];  // codes of 64 columns each
+  float ws[R];
+  auto load = [&](int slot, int p, int c) {
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb) {
-      const u32x4 a0 = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)j * 2048));
-      const u32x4 a1 = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)j * 2048 + 1024));
-      A[slot][nb] = i32x8{(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
-    }
-    ws[slot] = wsp[j];
+    for (int nb = 0; nb < NBW; ++nb)
+      raw[slot][p][nb] = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)chunk_of(c) * 2048 + p * 1024));
   };
   floatx4 acc[NBW][MB];
 #pragma unroll
@@ -154,71 +168,91 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // chunk c: its hidden rows in LDS buffer c % 3, its matrix tiles in register slot c % 3; the copies and
-  // loads of chunk c + 2 go out at the start of chunk c
-  copy(s_x0, 0);
-  aload(0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  copy(s_x1, min(1, HB - 1));
-  aload(1, min(1, HB - 1));
-  __builtin_amdgcn_sched_barrier(0);
-  chunk_barrier<kQ + 2 * kLoads>();
-  auto chunk = [&](int c, int cc, const uint8_t* cur, uint8_t* nxt) {
-    const int ch = min(c + 2, HB - 1);  // the last chunk is requested again at the end, never used
-    copy(nxt, ch);
-    aload((cc + 2) % 3, ch);
-    __builtin_amdgcn_sched_barrier(0);
-    const float sw = ws[cc];
-    // one row block after the other: its operand reads one block ahead, its scaling one block behind the
-    // products (the order is pinned: left alone the compiler holds every block's products at once)
-    const float* sx = (const float*)(cur + MB * 2048) + lr;
-    auto operand = [&](int mb) {
-      const u32x4 b0 = *(const u32x4*)(cur + mb * 2048 + lane * 16);
-      const u32x4 b1 = *(const u32x4*)(cur + mb * 2048 + 1024 + lane * 16);
-      return i32x8{(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
-    };
-    i32x8 b = operand(0);
-    float s = sx[0], sp = 0.0f;
-    floatx4 z[NBW], zp[NBW];
+  // chunk c: hidden rows in LDS stage c % NST, matrix in register slot c % R. At its start the copies of chunk
+  // c + NST - 1 go out; each half's registers are loaded with chunk c + R once they are widened.
+  auto stage_of = [&](int i) { return i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3; };
 #pragma unroll
-    for (int mb = 0; mb <= MB; ++mb) {
-      i32x8 bn = b;
-      float sn = s;
-      if (mb + 1 < MB) {
-        bn = operand(mb + 1);
-        sn = sx[(mb + 1) * 16];
-      }
-      if (mb < MB) {
-#pragma unroll
-        for (int nb = 0; nb < NBW; ++nb)
-          z[nb] = product(A[cc][nb], b);
-      }
-      if (mb > 0) {
-        const float f = sp * sw;
-#pragma unroll
-        for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      b = bn;
-      sp = s;
-      s = sn;
-#pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
+  for (int i = 0; i < NST - 1; ++i) {
+    copy(stage_of(i), min(i, HB - 1));
+    if (i < R) {
+      load(i, 0, min(i, HB - 1));
+      load(i, 1, min(i, HB - 1));
+      ws[i] = wsp[chunk_of(min(i, HB - 1))];
     }
-    // chunk c + 1's copies have landed: newer are its loads, and chunk c + 2's copies and loads
-    chunk_barrier<kQ + 2 * kLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (R == NST) {
+    load(R - 1, 0, min(R - 1, HB - 1));
+    load(R - 1, 1, min(R - 1, HB - 1));
+    ws[R - 1] = wsp[chunk_of(min(R - 1, HB - 1))];
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  chunk_barrier<kLoads>();
+  auto chunk = [&](int c, int st, int slot) {
+    const uint8_t* cur = stage_of(st) + wm * MB * 4096;
+    const float* sx = (const float*)(stage_of(st) + MB * MW * 4096) + wm * MB * 16 + lr;
+    copy(stage_of((st + NST - 1) % NST), min(c + NST - 1, HB - 1));  // the last chunk again at the end, never used
+    const float sw = ws[slot];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      bf16x8 A[NBW][2];
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb) {
+        const u32x4 x = raw[slot][p][nb];
+        A[nb][0] = widen8(x[0], x[1]);
+        A[nb][1] = widen8(x[2], x[3]);
+      }
+      load(slot, p, min(c + R, HB - 1));
+      if (p == 1) ws[slot] = wsp[chunk_of(min(c + R, HB - 1))];
+      __builtin_amdgcn_sched_barrier(0);
+      // one row block after the other, operand reads one block ahead, scaling one block behind (the order is
+      // pinned: left alone the compiler holds every block's sums at once)
+      const uint8_t* xb = cur + p * 2048 + lane * 16;
+      bf16x8 b0 = *(const bf16x8*)xb, b1 = *(const bf16x8*)(xb + 1024);
+      float s = sx[0], sp = 0.0f;
+      floatx4 z[NBW], zp[NBW];
+#pragma unroll
+      for (int mb = 0; mb <= MB; ++mb) {
+        bf16x8 n0 = b0, n1 = b1;
+        float sn = s;
+        if (mb + 1 < MB) {
+          n0 = *(const bf16x8*)(xb + (mb + 1) * 4096);
+          n1 = *(const bf16x8*)(xb + (mb + 1) * 4096 + 1024);
+          sn = sx[(mb + 1) * 16];
+        }
+        if (mb < MB) {
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb) z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][1], b1, z[nb], 0, 0, 0);
+        }
+        if (mb > 0) {
+          const float f = sp * sw;
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        b0 = n0;
+        b1 = n1;
+        sp = s;
+        s = sn;
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
+      }
+    }
+    chunk_barrier<kNewer>();  // chunk c + 1's copies have landed
   };
   int c = 0;
 #pragma nounroll
-  for (; c + 3 <= HB; c += 3) {
-    chunk(c, 0, s_x0, s_x2);
-    chunk(c + 1, 1, s_x1, s_x0);
-    chunk(c + 2, 2, s_x2, s_x1);
-  }
-  if (c < HB) chunk(c, 0, s_x0, s_x2);
-  if (c + 1 < HB) chunk(c + 1, 1, s_x1, s_x0);
+  for (; c + NST <= HB; c += NST)
+#pragma unroll
+    for (int i = 0; i < NST; ++i) chunk(c + i, i, i % R);
+#pragma unroll
+  for (int i = 0; i + 1 < NST; ++i)
+    if (c + i < HB) chunk(c + i, i, i % R);
   // lane: vocabulary rows 4 lg + (0 .. 3) of its blocks for hidden row lr of each block
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
@@ -318,11 +352,11 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(int V, int H, const u
   }
 }
 
-template <int MB, int NBW>
+template <int MB, int NBW, int MW, int VW, int NST, int R>
 hipError_t launch_mb(const LmHeadFp8Args& a, hipStream_t st) {
   const int VB = (a.V + 15) >> 4, MBt = (a.M + 15) >> 4;
-  const dim3 grid((unsigned)((VB + 8 * NBW - 1) / (8 * NBW)), (unsigned)((MBt + MB - 1) / MB));
-  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW>), grid, dim3(512), 0, st, a);
+  const dim3 grid((unsigned)((VB + VW * NBW - 1) / (VW * NBW)), (unsigned)((MBt + MB * MW - 1) / (MB * MW)));
+  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW, MW, VW, NST, R>), grid, dim3(64 * MW * VW), 0, st, a);
   return hipGetLastError();
 }
 
@@ -334,18 +368,17 @@ hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (a.mb) {
-    case 1: return launch_mb<1, 2>(a, st);
-    case 2: return launch_mb<2, 2>(a, st);
-    case 4: return launch_mb<4, 2>(a, st);
-    case 8: return launch_mb<8, 2>(a, st);
-    case 12: return launch_mb<12, 2>(a, st);
-    default: return launch_mb<14, 2>(a, st);
+    case 1: return launch_mb<1, 1, 1, 4, 4, 4>(a, st);
+    case 2: return launch_mb<2, 1, 1, 4, 4, 4>(a, st);
+    case 4: return launch_mb<4, 2, 1, 4, 4, 4>(a, st);
+    case 7: return launch_mb<7, 4, 1, 4, 2, 1>(a, st);
+    default: return launch_mb<7, 4, 2, 4, 2, 1>(a, st);
   }
 }
 
 int lm_head_fp8_blocks(int M) {
   const int n = (M + 15) >> 4;
-  return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : n <= 12 ? 12 : 14;
+  return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 7 ? 7 : 14;
 }
 
 hipError_t launch_tile_fp8(int V, int H, const uint8_t* codes, uint8_t* tiled, hipStream_t st) {
