@@ -53,7 +53,8 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
 }
 
 // Hidden rows: a wave per 16 rows and 128 columns, a lane 32 columns of a row.
-// Column c of row r of a block goes to 1 KB run c / 64 * 2 + c / 8 % 2, lane (c / 16 % 4) * 16 + r of it.
+// Column c of row r of a block goes to unit c / 64, 1 KB run c / 8 % 2 of it, lane (c / 16 % 4) * 16 + r; both
+// units of a chunk have its scales.
 __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int HB = a.H >> 7, MBt = (a.M + 15) >> 4;
   const int wv = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -62,9 +63,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int mb = wv % MBt, j = wv / MBt;
   const int r = lane >> 2, m = mb * 16 + r, c0 = (lane & 3) * 32;
   const int mt = mb / a.mb, mi = mb - mt * a.mb;
-  uint8_t* stage = a.xq + ((size_t)mt * HB + j) * fp8_stage_bytes(a.mb);
-  uint8_t* dst = stage + mi * 4096 + (c0 >> 6) * 2048 + ((c0 >> 4 & 3) * 16 + r) * 16;
-  float* xs = (float*)(stage + a.mb * 4096) + mi * 16 + r;
+  uint8_t* unit = a.xq + (((size_t)mt * HB + j) * 2 + (c0 >> 6)) * fp8_unit_bytes(a.mb);
+  uint8_t* dst = unit + mi * 2048 + ((c0 >> 4 & 3) * 16 + r) * 16;
+  float* xs = (float*)(unit + a.mb * 2048) + mi * 16 + r;
   float x[32];
   if (m < a.M) {
     const uint16_t* src = a.hidden + (long long)m * a.hidden_rs + j * 128 + c0;
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
       const uint32_t hi = quant4(clamp_e4m3(y[4] / s), clamp_e4m3(y[5] / s), clamp_e4m3(y[6] / s), clamp_e4m3(y[7] / s));
       *(bf16x8*)(dst + e * 1024 + q * 256) = widen8(lo, hi);
     }
-  if ((lane & 3) == 0) *xs = s;
+  if ((lane & 1) == 0) *xs = s;
 }
 
 // Work-group barrier once this wave's copies of the next chunk have landed in
@@ -111,19 +112,128 @@ __device__ __forceinline__ void chunk_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// buffer descriptor of n bytes from p (raw bytes: word 3), kept in scalar registers
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_at(const uint8_t* p, int n) {
+  const uint64_t q = (uint64_t)p;
+  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)q) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(q >> 32)) << 32;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, __builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+__device__ __forceinline__ u32x4 words_at(const uint8_t* p, int n) {
+  const uint64_t q = (uint64_t)p;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)q),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(q >> 32)),
+               (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
+}
 // 16 bytes a lane straight into LDS
 __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t rs, uint8_t* to, int lane_off, int off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, lane_off, off, 0, 0);
 }
+// The same as assembly, for the wide kernel, whose waits are all its own: the compiler cannot tell its many
+// copies apart and would wait for all of them before every LDS read. (m0, the LDS address, has no other use in that
+// kernel.) r: a descriptor's four words.
+template <bool ONCE>
+__device__ __forceinline__ void copy_1k_asm(u32x4 r, const uint8_t* to, int lane_off, int off) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)to;
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
+}
+
+// acc += (sx of the row * sw) * (A times the hidden operands of 64 columns at xb, a block every 2 KB). One row
+// block after the other, operand reads one block ahead, scaling one block behind (the order is pinned: left alone
+// the compiler holds every block's sums at once).
+template <int MB, int NBW>
+__device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* sx, float sw, const bf16x8 (&A)[NBW][2],
+                                                floatx4 (&acc)[NBW][MB]) {
+  bf16x8 b0 = *(const bf16x8*)xb, b1 = *(const bf16x8*)(xb + 1024);
+  float s = sx[0], sp = 0.0f;
+  floatx4 z[NBW], zp[NBW];
+#pragma unroll
+  for (int mb = 0; mb <= MB; ++mb) {
+    bf16x8 n0 = b0, n1 = b1;
+    float sn = s;
+    if (mb + 1 < MB) {
+      n0 = *(const bf16x8*)(xb + (mb + 1) * 2048);
+      n1 = *(const bf16x8*)(xb + (mb + 1) * 2048 + 1024);
+      sn = sx[(mb + 1) * 16];
+    }
+    if (mb < MB) {
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb)
+        z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb) z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][1], b1, z[nb], 0, 0, 0);
+    }
+    if (mb > 0) {
+      const float f = sp * sw;
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    b0 = n0;
+    b1 = n1;
+    sp = s;
+    s = sn;
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
+  }
+}
+
+// lane: vocabulary rows 4 lg + (0 .. 3) of each of its blocks for hidden row lr of each row block
+template <int MB, int NBW>
+__device__ __forceinline__ void store_logits(const LmHeadFp8Args& a, const floatx4 (&acc)[NBW][MB], int mb0, int vb0) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int m = (mb0 + mb) * 16 + lr;
+    if (m >= a.M) continue;
+    const int b = m / a.K, k = m - b * a.K;
+    const long long off = (long long)b * a.out_rs + (long long)k * a.out_ss;
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb) {
+      const int v = (vb0 + nb) * 16 + lg * 4;
+      const floatx4 z = acc[nb][mb];
+      if (a.out_bf16) {
+        uint16_t* o = (uint16_t*)a.out + off + v;
+        uint32_t hh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hh[i] = f32_to_bf16_bits(z[i]);
+        if (a.vec_out && v + 3 < a.V) {
+          *(u32x2*)o = u32x2{hh[0] | (hh[1] << 16), hh[2] | (hh[3] << 16)};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (v + i < a.V) o[i] = (uint16_t)hh[i];
+        }
+      } else {
+        float* o = (float*)a.out + off + v;
+        if (a.vec_out && v + 3 < a.V) {
+          *(f32x4*)o = f32x4{z[0], z[1], z[2], z[3]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (v + i < a.V) o[i] = z[i];
+        }
+      }
+    }
+  }
+}
 
 // A work-group has MW x VW waves: wave (wm, wv) takes MB 16-row blocks of hidden rows from wm * MB and NBW
 // 16-row blocks of the vocabulary. NST chunks of hidden rows in LDS, R chunks of the matrix in registers.
-template <int MB, int NBW, int MW, int VW, int NST, int R>
-__global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_kernel(
+template <int MB, int NBW, int MW, int VW, int NST, int R, int WPE>
+__global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void lm_head_fp8_kernel(
     LmHeadFp8Args a) {
   static_assert((NST == 2 || NST == 4) && NST % R == 0 && 8 % NBW == 0, "ring sizes, one scale block a wave");
   constexpr int NW = MW * VW;
-  constexpr int kStage = fp8_stage_bytes(MB * MW);  // a chunk's hidden rows and their scales
+  constexpr int kUnit = fp8_unit_bytes(MB * MW);    // 64 columns of the hidden rows, and their scales
+  constexpr int kStage = 2 * kUnit;
   constexpr int kCopy = kStage / 1024;              // 1 KB copies of it, dealt to the waves in turn
   constexpr int kQ = (kCopy + NW - 1) / NW;
   constexpr int kLoads = 2 * NBW + 1;               // a wave's loads of a chunk of the matrix
@@ -134,10 +244,10 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2,
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w / VW, wv = w % VW;
-  const int lr = lane & 15, lg = lane >> 4;
+  const int lr = lane & 15;
   const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
   const int mb0 = (blockIdx.y * MW + wm) * MB;
-  const int vb0 = (blockIdx.x * VW + wv) * NBW;  // first 16-row block of this wave
+  const int vb0 = a.vb_first + (blockIdx.x * VW + wv) * NBW;  // first 16-row block of this wave
   const int coff = (int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB);
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
 
@@ -146,8 +256,7 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2,
   for (int nb = 0; nb < NBW; ++nb) wp[nb] = a.w + (size_t)min(vb0 + nb, VB - 1) * HB * 2048 + lane * 16;
   const float* wsp = a.w_scale + (size_t)min(vb0 >> 3, (a.V - 1) >> 7) * HB;
   // copies as buffer loads: the compiler would have the flat form wait for every load in flight
-  const __amdgpu_buffer_rsrc_t xrs = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(a.xq + (size_t)blockIdx.y * HB * kStage), (short)0, HB * kStage, 0x00020000);  // word 3: raw bytes
+  const __amdgpu_buffer_rsrc_t xrs = bytes_at(a.xq + (size_t)blockIdx.y * HB * kStage, HB * kStage);
   auto copy = [&](uint8_t* buf, int c) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
@@ -189,8 +298,8 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2,
   }
   chunk_barrier<kLoads>();
   auto chunk = [&](int c, int st, int slot) {
-    const uint8_t* cur = stage_of(st) + wm * MB * 4096;
-    const float* sx = (const float*)(stage_of(st) + MB * MW * 4096) + wm * MB * 16 + lr;
+    const uint8_t* cur = stage_of(st) + wm * MB * 2048;
+    const float* sx = (const float*)(stage_of(st) + MB * MW * 2048) + wm * MB * 16 + lr;
     copy(stage_of((st + NST - 1) % NST), min(c + NST - 1, HB - 1));  // the last chunk again at the end, never used
     const float sw = ws[slot];
 #pragma unroll
@@ -205,43 +314,7 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2,
       load(slot, p, min(c + R, HB - 1));
       if (p == 1) ws[slot] = wsp[chunk_of(min(c + R, HB - 1))];
       __builtin_amdgcn_sched_barrier(0);
-      // one row block after the other, operand reads one block ahead, scaling one block behind (the order is
-      // pinned: left alone the compiler holds every block's sums at once)
-      const uint8_t* xb = cur + p * 2048 + lane * 16;
-      bf16x8 b0 = *(const bf16x8*)xb, b1 = *(const bf16x8*)(xb + 1024);
-      float s = sx[0], sp = 0.0f;
-      floatx4 z[NBW], zp[NBW];
-#pragma unroll
-      for (int mb = 0; mb <= MB; ++mb) {
-        bf16x8 n0 = b0, n1 = b1;
-        float sn = s;
-        if (mb + 1 < MB) {
-          n0 = *(const bf16x8*)(xb + (mb + 1) * 4096);
-          n1 = *(const bf16x8*)(xb + (mb + 1) * 4096 + 1024);
-          sn = sx[(mb + 1) * 16];
-        }
-        if (mb < MB) {
-#pragma unroll
-          for (int nb = 0; nb < NBW; ++nb)
-            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-          for (int nb = 0; nb < NBW; ++nb) z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][1], b1, z[nb], 0, 0, 0);
-        }
-        if (mb > 0) {
-          const float f = sp * sw;
-#pragma unroll
-          for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        b0 = n0;
-        b1 = n1;
-        sp = s;
-        s = sn;
-#pragma unroll
-        for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
-      }
+      scaled_products<MB, NBW>(cur + p * kUnit + lane * 16, sx, sw, A, acc);
     }
     chunk_barrier<kNewer>();  // chunk c + 1's copies have landed
   };
@@ -253,41 +326,122 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
   for (int i = 0; i + 1 < NST; ++i)
     if (c + i < HB) chunk(c + i, i, i % R);
-  // lane: vocabulary rows 4 lg + (0 .. 3) of its blocks for hidden row lr of each block
+  store_logits<MB, NBW>(a, acc, mb0, vb0);
+}
+
+// Up to 224 hidden rows a tile: eight waves, wave (wm, wv) takes 7 row blocks from 7 wm and 4 vocabulary blocks
+// from 4 wv. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS; the matrix's chunk (32 KB,
+// each run read by two waves) one deep, widened into registers at the chunk's start, after which the next one
+// is copied over it. The vector unit would be the bound, so a chunk's sums are scaled once, not once a half.
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_wide_kernel(LmHeadFp8Args a) {
+  constexpr int MB = 7, NBW = 4;
+  constexpr int kUnit = fp8_unit_bytes(2 * MB);
+  constexpr int kCopy = 2 * kUnit / 1024;
+  constexpr int kQ = (kCopy + 7) / 8;
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[2][2 * kUnit];
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[16 * 2048];
+  __shared__ float s_ws[2][512];  // the two scale blocks' scales, by chunk (H <= 65536)
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w >> 2, wv = w & 3;
+  const int lr = lane & 15;
+  const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
+  const int vt0 = a.vb_first + blockIdx.x * 16;
+  const int coff = __builtin_amdgcn_readfirstlane((int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB));
+  auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
+  for (int i = tid; i < 2 * HB; i += 512) {
+    const int b = i >= HB ? 1 : 0;
+    s_ws[b][i - b * HB] = a.w_scale[(size_t)min((vt0 >> 3) + b, (a.V - 1) >> 7) * HB + i - b * HB];
+  }
+  const u32x4 xrs = words_at(a.xq + (size_t)blockIdx.y * HB * 2 * kUnit, HB * 2 * kUnit);
+  // the tile's rows of the matrix: 16 blocks of HB * 2 KB (those past the last repeat it)
+  const int nblk = __builtin_amdgcn_readfirstlane(min(16, VB - vt0));
+  const u32x4 wrs = words_at(a.w + (size_t)vt0 * HB * 2048, nblk * HB * 2048);
+  auto copy_x = [&](uint8_t* buf, int c) {
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const int m = (mb0 + mb) * 16 + lr;
-    if (m >= a.M) continue;
-    const int b = m / a.K, k = m - b * a.K;
-    const long long off = (long long)b * a.out_rs + (long long)k * a.out_ss;
+    for (int q = 0; q < kQ; ++q) {
+      const int p = min(q * 8 + w, kCopy - 1);
+      copy_1k_asm<false>(xrs, buf + p * 1024, lane * 16, chunk_of(c) * 2 * kUnit + p * 1024);
+    }
+  };
+  auto copy_w = [&](int c) {
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb) {
-      const int v = (vb0 + nb) * 16 + lg * 4;
-      const floatx4 z = acc[nb][mb];
-      if (a.out_bf16) {
-        uint16_t* o = (uint16_t*)a.out + off + v;
-        uint32_t hh[4];
+    for (int q = 0; q < 4; ++q) {
+      const int p = q * 8 + w;  // 1 KB run p of the chunk: half p % 2 of block p / 2
+      copy_1k_asm<true>(wrs, s_w + p * 1024, lane * 16,
+                        min(p >> 1, nblk - 1) * HB * 2048 + chunk_of(c) * 2048 + (p & 1) * 1024);
+    }
+  };
+  floatx4 acc[NBW][MB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) hh[i] = f32_to_bf16_bits(z[i]);
-        if (a.vec_out && v + 3 < a.V) {
-          *(u32x2*)o = u32x2{hh[0] | (hh[1] << 16), hh[2] | (hh[3] << 16)};
-        } else {
+  for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (v + i < a.V) o[i] = (uint16_t)hh[i];
-        }
-      } else {
-        float* o = (float*)a.out + off + v;
-        if (a.vec_out && v + 3 < a.V) {
-          *(f32x4*)o = f32x4{z[0], z[1], z[2], z[3]};
-        } else {
+    for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  copy_x(s_x[0], 0);
+  copy_w(0);
+  chunk_barrier<0>();
+#pragma nounroll
+  for (int c = 0; c < HB; ++c) {
+    const uint8_t* cur = s_x[c & 1];
+    if (c + 1 < HB) copy_x(s_x[(c + 1) & 1], c + 1);
+    bf16x8 A[NBW][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (v + i < a.V) o[i] = z[i];
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const u32x4 x = *(const u32x4*)(s_w + (wv * NBW + nb) * 2048 + p * 1024 + lane * 16);
+        A[nb][2 * p] = widen8(x[0], x[1]);
+        A[nb][2 * p + 1] = widen8(x[2], x[3]);
+      }
+    const float sw = s_ws[wv >> 1][chunk_of(c)];
+    // every wave has read the matrix's chunk: the next one may land on it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (c + 1 < HB) copy_w(c + 1);
+    const uint8_t* xb = cur + wm * MB * 2048 + lane * 16;
+    const float* sx = (const float*)(cur + 2 * MB * 2048) + wm * MB * 16 + lr;
+    auto operand = [&](int mb, int e) { return *(const bf16x8*)(xb + (e >> 1) * kUnit + mb * 2048 + (e & 1) * 1024); };
+    // one row block after the other, operand reads one block ahead, scaling one block behind (the order is
+    // pinned: left alone the compiler holds every block's sums at once)
+    bf16x8 b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = operand(0, e);
+    float s = sx[0], sp = 0.0f;
+    floatx4 z[NBW], zp[NBW];
+#pragma unroll
+    for (int mb = 0; mb <= MB; ++mb) {
+      float sn = s;
+      if (mb < MB) {
+        if (mb + 1 < MB) sn = sx[(mb + 1) * 16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][e], b[e], e ? z[nb] : floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+          if (mb + 1 < MB) b[e] = operand(mb + 1, e);
         }
       }
+      if (mb > 0) {
+        const float f = sp * sw;
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      sp = s;
+      s = sn;
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
     }
+    // the sums are finished here: otherwise they sink past the branches, with all their addends kept alive
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) asm volatile("" : "+v"(acc[nb][mb]));
+    chunk_barrier<0>();  // chunk c + 1 has landed
   }
+  store_logits<MB, NBW>(a, acc, (blockIdx.y * 2 + wm) * MB, vt0 + wv * NBW);
 }
 
 // Row-major codes [V][H] into the tiles, 16 bytes a thread; rows past V are zero.
@@ -352,12 +506,29 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(int V, int H, const u
   }
 }
 
-template <int MB, int NBW, int MW, int VW, int NST, int R>
+template <int MB, int NBW, int MW, int VW, int NST, int R, int WPE>
 hipError_t launch_mb(const LmHeadFp8Args& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, MBt = (a.M + 15) >> 4;
+  const int VB = ((a.V + 15) >> 4) - a.vb_first, MBt = (a.M + 15) >> 4;
   const dim3 grid((unsigned)((VB + VW * NBW - 1) / (VW * NBW)), (unsigned)((MBt + MB * MW - 1) / (MB * MW)));
-  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW, MW, VW, NST, R>), grid, dim3(64 * MW * VW), 0, st, a);
+  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW, MW, VW, NST, R, WPE>), grid, dim3(64 * MW * VW), 0, st, a);
   return hipGetLastError();
+}
+
+// The wide kernel's work-groups fill the device in rounds of one a CU. A last round of few of them would take
+// as long as a full one (90 us at H = 4096): its vocabulary goes to work-groups of 16 vocabulary rows instead
+// (seven waves, two row blocks each; 55 us for the 256 that one round of them holds, 105 us for 640).
+constexpr int kCus = 256, kTailTiles = 16;
+hipError_t launch_wide(LmHeadFp8Args a, hipStream_t st) {
+  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + 13) / 14;
+  int tiles = (VB + 15) / 16;
+  const int rest = tiles % kCus;
+  const bool tail = mt == 1 && tiles > kCus && rest > 0 && rest <= kTailTiles;
+  if (tail) tiles -= rest;
+  hipLaunchKernelGGL(lm_head_fp8_wide_kernel, dim3((unsigned)tiles, (unsigned)mt), dim3(512), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !tail) return e;
+  a.vb_first = tiles * 16;
+  return launch_mb<2, 1, 7, 1, 2, 2, 2>(a, st);
 }
 
 }  // namespace
@@ -368,11 +539,11 @@ hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (a.mb) {
-    case 1: return launch_mb<1, 1, 1, 4, 4, 4>(a, st);
-    case 2: return launch_mb<2, 1, 1, 4, 4, 4>(a, st);
-    case 4: return launch_mb<4, 2, 1, 4, 4, 4>(a, st);
-    case 7: return launch_mb<7, 4, 1, 4, 2, 1>(a, st);
-    default: return launch_mb<7, 4, 2, 4, 2, 1>(a, st);
+    case 1: return launch_mb<1, 1, 1, 4, 4, 4, 2>(a, st);
+    case 2: return launch_mb<2, 1, 1, 4, 4, 4, 2>(a, st);
+    case 4: return launch_mb<4, 2, 1, 4, 4, 4, 2>(a, st);
+    case 7: return launch_mb<7, 4, 1, 4, 2, 1, 2>(a, st);
+    default: return launch_wide(a, st);
   }
 }
 
