@@ -128,7 +128,7 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, uint
   return t;
 }
 
-// Writes 8 (or D / 16) columns of one output row: o / l, scaled, in bf16; a row without keys is zero.
+// Writes 8 (or 4) columns of one output row: o / l, scaled, in bf16; a row without keys is zero.
 template <int NC>
 __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const Tile& t, int r, int h, int d0,
                                           const float (&o)[NC], float m, float l) {
@@ -185,25 +185,48 @@ __device__ __forceinline__ void read_tr8(uint32_t a0, uint32_t a1, uint32_t a2, 
       : "memory");
 }
 
-// D: head dimension; E4M3: 8-bit cache; NB: 16-row blocks of the row tile
-template <int D, bool E4M3, int NB>
-__global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
-  constexpr int ROWS = NB * 16;
-  constexpr int RB = D * (E4M3 ? 1 : 2);       // bytes of a key (or value)
-  constexpr int SPR = RB / 16;                 // 16-byte slots of it
-  constexpr int RPI = 64 / SPR;                // keys per copy instruction (1 KB)
-  constexpr int NI = 32 / RPI;                 // copy instructions for a block's keys (as many for its values)
-  constexpr int kPart = 32 * RB;               // bytes of a block's keys
-  constexpr int kStage = 2 * kPart;
-  constexpr int NST = kStage >= 16384 ? 2 : 4; // blocks in flight per wave
+// 16 bytes a lane straight into LDS at `lds` (uniform) + 16 * lane, from base (uniform) + off. As assembly:
+// every wait for these copies is the kernel's own, and the compiler, which cannot tell the copies in flight
+// apart, would wait for all of them before each LDS read. (m0, the LDS address, has no other use here.)
+__device__ __forceinline__ void copy_1k(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {  // at most N of this wave's copies are still in flight
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// D: head dimension; E4M3: 8-bit cache; NB: 16-row blocks a wave; RG x KG waves: RG groups of rows, KG of keys
+template <int D, bool E4M3, int NB, int RG, int KG>
+struct AttnShape {
+  static constexpr int kRows = NB * 16 * RG;
+  static constexpr int RB = D * (E4M3 ? 1 : 2);  // bytes of a key (or value)
+  static constexpr int kPart = 32 * RB;          // bytes of a block's keys
+  static constexpr int kStage = 2 * kPart;       // a block of 32 keys and values
+  // blocks in flight per key group: what fits 128 KB, four at most
+  static constexpr int NST = KG * kStage * 4 <= 131072 ? 4 : KG * kStage * 3 <= 131072 ? 3 : 2;
+  static constexpr int kRing = KG * kStage * NST;
+  static constexpr int kJoin = RG * KG * 16 * D * 4;  // the waves' o, 16 rows each
+  static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int D, bool E4M3, int NB, int RG, int KG>
+__global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG * KG / 4, RG * KG / 4))) void attn_kernel(
+    PagedAttnArgs a) {
+  using Sh = AttnShape<D, E4M3, NB, RG, KG>;
+  constexpr int ROWS = Sh::kRows, RB = Sh::RB, kPart = Sh::kPart, kStage = Sh::kStage, NST = Sh::NST;
+  constexpr int SPR = RB / 16;                 // 16-byte slots of a key
+  constexpr int RPI = 64 / SPR;                // keys per copy (1 KB)
+  constexpr int NI = 32 / RPI;                 // copies of a block's keys (as many for its values)
+  constexpr int kMine = (2 * NI + RG - 1) / RG;  // of them, a wave's (the RG waves of a key group share a block)
   constexpr int NS = D / 32;                   // 32-wide slices of the first product
   constexpr int ND = D / 16;                   // 16-wide column blocks of the second
-  // one array per block in flight: the copies into one are not taken for writes to another
-  __shared__ __attribute__((aligned(16))) unsigned char s0[4 * kStage], s1[4 * kStage];
-  __shared__ __attribute__((aligned(16))) unsigned char s2[NST > 2 ? 4 * kStage : 16], s3[NST > 2 ? 4 * kStage : 16];
-  __shared__ float s_m[4][ROWS], s_l[4][ROWS];
+  __shared__ __attribute__((aligned(16))) unsigned char s_kv[Sh::kLds];
+  __shared__ float s_m[KG][ROWS], s_l[KG][ROWS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rg = w % RG, kg = w / RG;
   const int lr = lane & 15, lg = lane >> 4;
   const int h = blockIdx.x % (unsigned)a.Hkv;
   const int ct = blockIdx.x / (unsigned)a.Hkv;
@@ -218,14 +241,16 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
   const int c0 = t.base + c * a.chunk;
   const int lo = max(t.lo, c0), hi = c == a.n_chunks - 1 ? t.hi : min(t.hi, c0 + a.chunk);
   const int nblk = hi > lo ? (hi - c0 + 31) >> 5 : 0;
-  const int nmy = nblk > w ? (nblk - w + 3) >> 2 : 0;  // this wave's blocks: w, w + 4, ..
+  const int nit = (nblk + KG - 1) / KG;                 // rounds; key group kg takes blocks kg, kg + KG, ..
+  const int nmy = nblk > kg ? (nblk - kg + KG - 1) / KG : 0;  // of them, its own
 
-  // the rows: row R of the request is head R % G of token R / G; rows past the tile repeat the last
+  // the wave's rows: row R of the request is head R % G of token R / G; rows past the tile repeat the last
+  const int r0 = t.r0 + min(rg * NB * 16, t.rows - 1), r1 = t.r0 + min((rg + 1) * NB * 16, t.rows) - 1;
   bf16x8 Q[NB][NS];
   int mlo[NB], mhi[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int R = t.r0 + min(nb * 16 + lr, t.rows - 1);
+    const int R = min(t.r0 + (rg * NB + nb) * 16 + lr, t.r0 + t.rows - 1);
     const int tok = R / a.G, hq = h * a.G + (R - tok * a.G);
     const uint16_t* qp = a.q + (long long)(t.q0 + tok) * a.q_ts + hq * a.q_hs;
 #pragma unroll
@@ -236,15 +261,15 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
     mlo[nb] = max(klo, lo);
     mhi[nb] = min(khi, hi);
   }
-  // keys that every row sees: blocks inside need no mask
-  int all_lo, all_hi, x0, x1;
-  token_keys(a, t, (t.r0 + t.rows - 1) / a.G, all_lo, x1);
-  token_keys(a, t, t.r0 / a.G, x0, all_hi);
+  // keys that some row of the wave sees, and those that every row sees (blocks inside need no mask)
+  int any_lo, any_hi, all_lo, all_hi;
+  token_keys(a, t, r0 / a.G, any_lo, all_hi);
+  token_keys(a, t, r1 / a.G, all_lo, any_hi);
   all_lo = max(all_lo, lo);
   all_hi = min(all_hi, hi);
   const float sc = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.0f);
 
-  // copies: instruction p of a block fills keys RPI p .. of it; lane l lands in row r = RPI p + l / SPR,
+  // copies: copy p of a block's keys fills keys RPI p .. of it; lane l lands in row r = RPI p + l / SPR,
   // slot l % SPR, which holds the row's slot (l % SPR) ^ swizzle(r)
   auto kswz = [](int r) { return SPR == 16 ? r & 15 : SPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
   auto vswz = [](int r) {
@@ -252,62 +277,63 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
                 : (SPR == 16 ? (r & 7) * 2 : ((r >> 1) & 3) * 2);
   };
   const int lrow = lane / SPR, lslot = lane % SPR;
-  uint32_t ko[NI], vo[NI];
-#pragma unroll
-  for (int p = 0; p < NI; ++p) {
-    const int r = p * RPI + lrow;
-    ko[p] = (uint32_t)((r & 15) * (int)a.k_ts) + (uint32_t)((lslot ^ kswz(r)) * 16);
-    vo[p] = (uint32_t)((r & 15) * (int)a.v_ts) + (uint32_t)((lslot ^ vswz(r)) * 16);
-  }
+  const uint32_t ring = (uint32_t)(uintptr_t)(MDS_LDS const void*)s_kv + kg * NST * kStage;
   const int32_t* trow = a.block_table + (size_t)t.slot * a.max_pages;
   const char* kb_h = (const char*)a.k_pages + h * a.k_hs;
   const char* vb_h = (const char*)a.v_pages + h * a.v_hs;
   const int pmask = (1 << a.page_log2) - 1;
-  // Page ids of the wave's blocks i0 .. i0 + 31: lane 2 (i - i0) + j has the page of half j (16 keys, in one
-  // page) of block i. Keys outside [lo, hi) repeat the nearest one inside: what lies behind a sequence's end
-  // is never read, and their probability is zero.
+  // this wave's copies of a block: number x = rg + RG n, keys for x < NI, values above. Offset of a lane's 16
+  // bytes from the first key of the half block (16 keys, which lie in one page)
+  uint32_t off[kMine];
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int x = rg + RG * n, p = x % NI, r = p * RPI + lrow;
+    const bool v = x >= NI;
+    off[n] = (uint32_t)((r & 15) * (int)(v ? a.v_ts : a.k_ts)) + (uint32_t)((lslot ^ (v ? vswz(r) : kswz(r))) * 16);
+  }
+  // Page ids of the key group's blocks i0 .. i0 + 31: lane 2 (i - i0) + j has the page of half j of block i.
+  // Keys outside [lo, hi) repeat the nearest one inside: what lies behind a sequence's end is never read, and
+  // their probability is zero.
   int pages = 0;
   auto load_pages = [&](int i0) {
-    const int kh = c0 + (w + 4 * (i0 + (lane >> 1))) * 32 + 16 * (lane & 1);
+    const int kh = c0 + (kg + KG * (i0 + (lane >> 1))) * 32 + 16 * (lane & 1);
     pages = trow[min(max(kh, lo), hi - 1) >> a.page_log2];
     if ((unsigned)pages >= (unsigned)a.n_pages) {
       pages = 0;
       bad |= kStatusBadPage;
     }
   };
-  auto copy_one = [&](const char* p, unsigned char* to) {
-    __builtin_amdgcn_global_load_lds((const MDS_GLOBAL void*)p, (MDS_LDS void*)to, 16, 0, 0);
-  };
-  auto copy_block = [&](unsigned char* buf, int i) {
+  auto copy_block = [&](int i, int st) {
     if (i && (i & 31) == 0) load_pages(i);
-    const int k0 = c0 + (w + 4 * i) * 32;
+    const int k0 = c0 + (kg + KG * i) * 32;
+    const bool inside = k0 >= lo && k0 + 32 <= hi;
+    const char* kp[2];
+    const char* vp[2];
+    int kc[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int kh = k0 + 16 * j;
-      const int kc = min(max(kh, lo), hi - 1);
+      kc[j] = min(max(k0 + 16 * j, lo), hi - 1);
       const int pg = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + j);
-      const char* kp = kb_h + pg * a.k_ps + (kc & pmask) * a.k_ts;
-      const char* vp = vb_h + pg * a.v_ps + (kc & pmask) * a.v_ts;
-      unsigned char* to = buf + j * (NI / 2) * 1024;
-      if (k0 >= lo && k0 + 32 <= hi) {
+      kp[j] = kb_h + pg * a.k_ps + (kc[j] & pmask) * a.k_ts;
+      vp[j] = vb_h + pg * a.v_ps + (kc[j] & pmask) * a.v_ts;
+    }
 #pragma unroll
-        for (int p = 0; p < NI / 2; ++p) {
-          copy_one(kp + ko[j * (NI / 2) + p], to + p * 1024);
-          copy_one(vp + vo[j * (NI / 2) + p], to + kPart + p * 1024);
-        }
-      } else {
-#pragma unroll
-        for (int p = 0; p < NI / 2; ++p) {
-          const int q = j * (NI / 2) + p, r = (q * RPI + lrow) & 15;
-          const int d = min(max(kh + r, lo), hi - 1) - kc - r;  // from the row's own place to the key copied
-          copy_one(kp + (uint32_t)((int)ko[q] + d * (int)a.k_ts), to + p * 1024);
-          copy_one(vp + (uint32_t)((int)vo[q] + d * (int)a.v_ts), to + kPart + p * 1024);
-        }
+    for (int n = 0; n < kMine; ++n) {
+      const int x = rg + RG * n;
+      if ((2 * NI) % RG != 0 && x >= 2 * NI) break;
+      const int p = x % NI, j = p >= NI / 2;
+      const bool v = x >= NI;
+      uint32_t o = off[n];
+      if (!inside) {
+        const int r = (p * RPI + lrow) & 15;
+        const int d = min(max(k0 + 16 * j + r, lo), hi - 1) - kc[j] - r;  // from the row's own place to the key copied
+        o = (uint32_t)((int)o + d * (int)(v ? a.v_ts : a.k_ts));
       }
+      copy_1k(v ? vp[j] : kp[j], o, ring + st * kStage + x * 1024);
     }
   };
 
-  // LDS offsets of a lane's column reads of the values, by block of 16 columns
+  // LDS offsets of a lane's reads: key slices of its row, and column reads of the values by block of 16 columns
   uint32_t va[ND];
 #pragma unroll
   for (int db = 0; db < ND; ++db) {
@@ -322,10 +348,12 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
   }
 
   floatx4 O[NB][ND];
-  float m[NB], l[NB];
+  float l[NB];          // the lane's part of the row sum
+  float m[NB], mc[NB];  // running maximum (base 2, scaled), and what is subtracted: it, or 0 before any key
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     m[nb] = -INFINITY;
+    mc[nb] = 0.0f;
     l[nb] = 0.0f;
 #pragma unroll
     for (int d = 0; d < ND; ++d) O[nb][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -335,8 +363,9 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
     return up ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true))
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
   };
-  auto block = [&](const unsigned char* buf, int i) {
-    const int k0 = c0 + (w + 4 * i) * 32;
+  auto block = [&](int st, int i) {
+    const int k0 = c0 + (kg + KG * i) * 32;
+    const unsigned char* buf = s_kv + (kg * NST + st) * kStage;
     floatx4 S[2][NB];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -364,10 +393,6 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
           S[kb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[s], Q[nb][s], S[kb][nb], 0, 0, 0);
     }
     // lane: row lr of each nb, keys k0 + 16 kb + 4 lg + i
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[kb][nb] *= sc;
     if (k0 < all_lo || k0 + 32 > all_hi) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -384,7 +409,7 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const floatx4 x = S[0][nb], y = S[1][nb];
-      top[nb] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+      top[nb] = fmaxf(fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), x[3]), fmaxf(fmaxf(fmaxf(y[0], y[1]), y[2]), y[3])) * sc;
       grow |= top[nb] > m[nb] + kRescale;
     }
     if (__any(grow)) {
@@ -395,6 +420,7 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
         x = fmaxf(x, __shfl_xor(x, 32));
         const float f = x == m[nb] ? 1.0f : __builtin_amdgcn_exp2f(m[nb] - x);
         m[nb] = x;
+        mc[nb] = x == -INFINITY ? 0.0f : x;
         l[nb] *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) O[nb][d] *= f;
@@ -403,16 +429,15 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
     bf16x8 P[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float mm = m[nb] == -INFINITY ? 0.0f : m[nb];  // a row without keys so far: every p is 0
       float p[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(S[e >> 2][nb][e & 3] - mm);
+      for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[e >> 2][nb][e & 3], sc, -mc[nb]));
       l[nb] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
 #pragma unroll
       for (int e = 0; e < 8; ++e) P[nb][e] = (__bf16)p[e];
     }
     // values: lane column d = 16 db + lr, keys 4 lg + (0 .. 3) and 16 + 4 lg + (0 .. 3)
-    const uint32_t vb = (uint32_t)(uintptr_t)(MDS_LDS const void*)buf + kPart;
+    const uint32_t vb = ring + st * kStage + kPart;
 #pragma unroll
     for (int d0 = 0; d0 < ND; d0 += 4) {
       bf16x8 Vf[4];
@@ -434,147 +459,178 @@ __global__ __launch_bounds__(256, 1) void attn_kernel(PagedAttnArgs a) {
     }
   };
 
-  unsigned char* const buf[4] = {s0 + w * kStage, s1 + w * kStage, NST > 2 ? s2 + w * kStage : s0,
-                                 NST > 2 ? s3 + w * kStage : s1};
   if (nmy > 0) load_pages(0);
+  if constexpr (RG == 1) {
+    // a key group is one wave: its ring is its own, no barrier
 #pragma unroll
-  for (int i = 0; i < NST; ++i)
-    if (i < nmy) copy_block(buf[i], i);
+    for (int i = 0; i < NST; ++i)
+      if (i < nmy) copy_block(i, i);
+    int st = 0;
 #pragma nounroll
-  for (int i0 = 0; i0 < nmy; i0 += NST) {
-#pragma unroll
-    for (int j = 0; j < NST; ++j) {
-      const int i = i0 + j;
-      if (i < nmy) {
-        // block i has landed: at most the NST - 1 blocks after it are still in flight
-        constexpr int N = (NST - 1) * 2 * NI;
-        asm volatile("" ::: "memory");
-        if (i + NST <= nmy)
-          __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-        else
-          __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // near the end: all of them
-        asm volatile("" ::: "memory");
-        block(buf[j], i);
-        if (i + NST < nmy) {
-          // the block's LDS reads have returned (their values were used): its place is free
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          copy_block(buf[j], i + NST);
-        }
+    for (int i = 0; i < nmy; ++i) {
+      // block i has landed: at most the NST - 1 blocks after it are still in flight
+      if (i + NST <= nmy)
+        wait_copies<(NST - 1) * 2 * NI>();
+      else
+        wait_copies<0>();  // near the end: all of them
+      block(st, i);
+      if (i + NST < nmy) {
+        // the block's LDS reads have returned (their values were used): its place is free
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy_block(i + NST, st);
       }
+      st = st + 1 == NST ? 0 : st + 1;
+    }
+  } else {
+    // the RG waves of a key group share its blocks: one barrier a round, after which block i is there for all of
+    // them and the place of block i - 1 is free
+    constexpr int kLeast = 2 * NI / RG;  // copies that every wave of the group makes of a block
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i)
+      if (i < nmy) copy_block(i, i);
+    int st = 0;
+#pragma nounroll
+    for (int i = 0; i < nit; ++i) {
+      if (i + NST - 1 <= nmy)
+        wait_copies<(NST - 2) * kLeast>();
+      else
+        wait_copies<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (i + NST - 1 < nmy) copy_block(i + NST - 1, st == 0 ? NST - 1 : st - 1);
+      if (i < nmy) {
+        const int k0 = c0 + (kg + KG * i) * 32;
+        if (k0 < any_hi && k0 + 32 > any_lo) block(st, i);  // else no row of this wave sees a key of it
+      }
+      st = st + 1 == NST ? 0 : st + 1;
     }
   }
   if (bad) set_status(a.status, bad);
 
-  // join the four waves, 16 rows at a time: o scaled to the common maximum through LDS, summed by
-  // 16 threads a row
+  // join the key groups, 16 rows of each row group at a time: o scaled to the common maximum through LDS, summed
+  // by the threads that share a row, 8 columns each
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     l[nb] += __shfl_xor(l[nb], 16);
     l[nb] += __shfl_xor(l[nb], 32);
     if (lg == 0) {
-      s_m[w][nb * 16 + lr] = m[nb];
-      s_l[w][nb * 16 + lr] = l[nb];
+      s_m[kg][(rg * NB + nb) * 16 + lr] = m[nb];
+      s_l[kg][(rg * NB + nb) * 16 + lr] = l[nb];
     }
   }
   __syncthreads();
-  const int orow = tid >> 4, od = (tid & 15) * (D / 16);
+  float* so = (float*)s_kv + (rg * KG) * 16 * D;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    if (nb * 16 >= t.rows) break;
-    const float M = fmaxf(fmaxf(s_m[0][nb * 16 + lr], s_m[1][nb * 16 + lr]),
-                          fmaxf(s_m[2][nb * 16 + lr], s_m[3][nb * 16 + lr]));
+    const int row0 = (rg * NB + nb) * 16;
+    float M = s_m[0][row0 + lr];
+#pragma unroll
+    for (int i = 1; i < KG; ++i) M = fmaxf(M, s_m[i][row0 + lr]);
     const float f = m[nb] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nb] - M);
-    float* so = (float*)(s0 + w * kStage);
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
       const floatx4 x = m[nb] == -INFINITY && !(l[nb] != l[nb]) ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : O[nb][d] * f;
-      *(floatx4*)(so + lr * D + (((4 * d + lg) ^ lr) * 4)) = x;
+      *(floatx4*)(so + kg * 16 * D + lr * D + (((4 * d + lg) ^ lr) * 4)) = x;
     }
     __syncthreads();
-    const int row = nb * 16 + orow;
-    if (row < t.rows) {
-      const float Mr = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
+    for (int it = kg * 64 + lane; it < 16 * (D / 8); it += 64 * KG) {
+      const int rr = it / (D / 8), od = (it % (D / 8)) * 8, row = row0 + rr;
+      if (row >= t.rows) continue;
+      float Mr = s_m[0][row];
+#pragma unroll
+      for (int i = 1; i < KG; ++i) Mr = fmaxf(Mr, s_m[i][row]);
       float L = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < KG; ++i) {
         const float li = s_l[i][row];
         L += s_m[i][row] == -INFINITY && li == li ? 0.0f : li * __builtin_amdgcn_exp2f(s_m[i][row] - Mr);
       }
-      float o[D / 16];
+      float o[8];
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
+      for (int q = 0; q < 2; ++q) {
         floatx4 x = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x += *(const floatx4*)((const float*)(s0 + i * kStage) + orow * D + (((od / 4 + q) ^ orow) * 4));
+        for (int i = 0; i < KG; ++i) x += *(const floatx4*)(so + i * 16 * D + rr * D + (((od / 4 + q) ^ rr) * 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[q * 4 + e] = x[e];
       }
-      if (a.n_chunks == 1 || t.chunks == 1) {
-        store_row<D / 16>(a, t, row, h, od, o, Mr, L);
+      if (t.chunks == 1) {
+        store_row(a, t, row, h, od, o, Mr, L);
       } else {
         const size_t pr = ((size_t)ct * a.Hkv + h) * ROWS + row;
         float* po = a.part_o + pr * D + od;
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q) *(floatx4*)(po + q * 4) = floatx4{o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]};
-        if ((tid & 15) == 0) a.part_ml[pr] = make_float2(Mr, L);
+        *(floatx4*)po = floatx4{o[0], o[1], o[2], o[3]};
+        *(floatx4*)(po + 4) = floatx4{o[4], o[5], o[6], o[7]};
+        if (od == 0) a.part_ml[pr] = make_float2(Mr, L);
       }
     }
     __syncthreads();
   }
 }
 
-// Joins the chunks of a row tile: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c.
+// Joins the chunks of a row tile: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. A wave per row: its lanes read
+// the chunks' (m, l) side by side, then four groups of 16 lanes take the chunks in turn.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
-  const int tid = threadIdx.x;
+  const int lane = threadIdx.x & 63;
   const int h = blockIdx.x % (unsigned)a.Hkv;
   const int tile = blockIdx.x / (unsigned)a.Hkv;
   uint32_t bad = 0;
   const Tile t = find_tile<ROWS>(a, tile, bad);
-  if (t.rows <= 0 || t.chunks <= 1) return;
-  const int od = (tid & 15) * (D / 16);
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 6);
+  if (row >= t.rows || t.chunks <= 1) return;
   const size_t step = (size_t)a.tiles * a.Hkv * ROWS;
-  for (int row = blockIdx.y * 16 + (tid >> 4); row < t.rows; row += 16 * gridDim.y) {
-    const size_t pr = ((size_t)tile * a.Hkv + h) * ROWS + row;
-    float M = -INFINITY;
-    for (int c = 0; c < t.chunks; ++c) M = fmaxf(M, a.part_ml[pr + c * step].x);
-    float L = 0.0f, o[D / 16];
+  const size_t pr = ((size_t)tile * a.Hkv + h) * ROWS + row;
+  float M = -INFINITY;
+  for (int c = lane; c < t.chunks; c += 64) M = fmaxf(M, a.part_ml[pr + c * step].x);
+  M = wave_max_f32(M);
+  constexpr int NC = D / 16;
+  const int g = lane >> 4, od = (lane & 15) * NC;
+  float L = 0.0f, o[NC];
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) o[e] = 0.0f;
-    for (int c = 0; c < t.chunks; ++c) {
-      const float2 ml = a.part_ml[pr + c * step];
-      if (ml.x == -INFINITY && ml.y == ml.y) continue;  // no keys of the row in this chunk
-      const float f = __builtin_amdgcn_exp2f(ml.x - M);
-      L += ml.y * f;
-      const float* po = a.part_o + (pr + c * step) * D + od;
+  for (int e = 0; e < NC; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (int c = g; c < t.chunks; c += 4) {
+    const float2 ml = a.part_ml[pr + c * step];
+    const float* po = a.part_o + (pr + c * step) * D + od;
+    floatx4 x[NC / 4];
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        const floatx4 x = *(const floatx4*)(po + q * 4);
+    for (int q = 0; q < NC / 4; ++q) x[q] = *(const floatx4*)(po + q * 4);
+    // a chunk without keys of the row has (-inf, 0) and zeros
+    const float f = ml.x == -INFINITY && ml.y == ml.y ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
+    L += ml.y * f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[q * 4 + e] += x[e] * f;
-      }
-    }
-    store_row<D / 16>(a, t, row, h, od, o, M, L);
+    for (int q = 0; q < NC / 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[q * 4 + e] += x[q][e] * f;
   }
+#pragma unroll
+  for (int e = 0; e < NC; ++e) {
+    o[e] += __shfl_xor(o[e], 16);
+    o[e] += __shfl_xor(o[e], 32);
+  }
+  L += __shfl_xor(L, 16);
+  L += __shfl_xor(L, 32);
+  if (g == 0) store_row(a, t, row, h, od, o, M, L);
 }
 
-template <int D, bool E4M3, int NB>
-hipError_t launch_nb(const PagedAttnArgs& a, hipStream_t st) {
+template <int D, bool E4M3, int NB, int RG, int KG>
+hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
+  constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG>::kRows;
   const long long wgs = (long long)a.tiles * a.Hkv;
-  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB>), dim3((unsigned)(wgs * a.n_chunks)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
-  hipLaunchKernelGGL((attn_join_kernel<D, NB * 16>), dim3((unsigned)wgs, NB), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)wgs, ROWS / 4), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 template <int D, bool E4M3>
 hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
   switch (rows) {
-    case 16: return launch_nb<D, E4M3, 1>(a, st);
-    case 32: return launch_nb<D, E4M3, 2>(a, st);
-    default: return launch_nb<D, E4M3, 4>(a, st);
+    case 16: return launch_shape<D, E4M3, 1, 1, 4>(a, st);
+    case 32: return launch_shape<D, E4M3, 2, 1, 4>(a, st);
+    case 64: return launch_shape<D, E4M3, 2, 2, 4>(a, st);
+    default: return launch_shape<D, E4M3, 2, 8, 1>(a, st);
   }
 }
 
@@ -583,7 +639,7 @@ hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
 AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
   AttnPlan p;
   const long long most = (long long)max_q_len * G;  // rows of the longest request
-  p.rows = most <= 16 ? 16 : most <= 32 ? 32 : 64;
+  p.rows = most <= 16 ? 16 : most <= 32 ? 32 : most <= 128 ? 64 : 256;
   const long long direct = (most + p.rows - 1) / p.rows;
   const long long by_rows = (long long)T * G / p.rows + B;
   p.per_req = direct * B <= by_rows ? (int)direct : 0;
