@@ -547,7 +547,7 @@ int mds_debug_gumbel(int n, const uint32_t* words, float* gumbel, void* stream);
  * MDS_STATUS_BAD_INDEX. A slot named by two rows, or >= n_slots, makes all
  * those rows padding, with MDS_STATUS_BAD_INDEX.
  *   status          device uint32 or NULL: MDS_STATUS_* bits are OR-ed in
- * Limits: B <= 65535, n_slots <= 2^17, max_pages*page_size <= 2^30, max_tokens <= 2^24.
+ * Limits: B <= 65535, n_slots <= 2^17, max_pages*page_size < 2^30, max_tokens <= 2^24.
  * One launch for up to 4096 tokens, two above.
  */
 int mds_kv_page_tables(int B, int n_slots, int max_pages, int page_size, int n_pages, int max_tokens,

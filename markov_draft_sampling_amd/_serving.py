@@ -9,70 +9,91 @@ import math
 
 import torch
 
-from . import BF16, E4M3, F32, MdsError, _check, _lib, _need, _ptr
+from . import BF16, E4M3, F32, MdsError, _check, _lib, _need
 
 _I32, _I64, _F32, _BF16, _E4M3 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float8_e4m3fn
-_vp, _c_sz = ctypes.c_void_p, ctypes.c_size_t
+_c_sz = ctypes.c_size_t
+
+# These calls take a few microseconds on the GPU at decoding sizes, so the checks here are kept cheap: a device is
+# compared by its index, pointers go to ctypes as plain integers, and the stream is asked for once.
 
 
-def _call(what, fn, dev, stream, args, tail=()):
-    """fn(*args, stream, *tail) on the tensors' device and the given (or that device's current) stream."""
-    if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            rc = fn(*args, _vp(torch.cuda.current_stream(dev).cuda_stream), *tail)
-        else:
-            with torch.cuda.device(dev):
-                rc = fn(*args, _vp(torch.cuda.current_stream(dev).cuda_stream), *tail)
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _call(what, fn, index, stream, args):
+    """fn(*args, stream) on the tensors' device and the given (or that device's current) stream."""
+    if stream is None and torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
-        _need(stream.device == dev, "the stream belongs to another device than the tensors")
-        with torch.cuda.device(dev):
-            rc = fn(*args, _vp(stream.cuda_stream), *tail)
+        if stream is not None and stream.device.index != index:
+            raise MdsError("the stream belongs to another device than the tensors")
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, what)
 
 
-def _workspace(given, nbytes, dev, stream):
-    """The caller's workspace, or a new zeroed one made on the stream that the call runs on."""
-    if given is not None:
-        _need(given.dtype == torch.uint8 and given.is_contiguous() and given.device == dev,
-              "workspace must be a contiguous uint8 tensor on the tensors' device")
-        return given
+def _new_workspace(nbytes, index, stream):
+    """A zeroed workspace made on the stream that the call runs on."""
+    nbytes = max(nbytes, 256)
     if stream is None:
-        return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
     with torch.cuda.stream(stream):
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    return ws
+        return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
 
 
-def _vec(t, dtype, n, dev, name):
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != dev:
-        raise MdsError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+def _check_workspace(ws, index):
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise MdsError("workspace must be a contiguous uint8 tensor on the tensors' device")
 
 
-def _opt(t, dtype, n, dev, name):
-    if t is not None:
-        _vec(t, dtype, n, dev, name)
+def _index(t):
+    """The device index of a GPU tensor (the first argument of a call, which the others have to be beside)."""
+    i = t.get_device()
+    if i < 0:
+        raise MdsError("tensors must be on the GPU")
+    return i
 
 
-def _status(t, dev):
-    if t is not None:
-        _need(t.numel() == 1 and t.element_size() == 4 and t.device == dev, "status: one 4-byte word on the device")
+def _vec(t, dtype, n, index, name):
+    """The pointer of a contiguous tensor of n elements on the device."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise MdsError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{index}")
+    return t.data_ptr()
 
 
-def _pages(k_pages, v_pages, dev):
-    """(page size, pages, key heads, head dimension, dtype code) of a pair of page arrays."""
-    _need(k_pages.dim() == 4 and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
-          "k_pages and v_pages must be [n_pages, page_size, Hkv, D] of one shape and dtype")
-    _need(k_pages.device == dev and v_pages.device == dev, "the pages must be on the tensors' device")
-    _need(k_pages.stride(3) == 1 and v_pages.stride(3) == 1, "pages must have a unit last stride")
-    if k_pages.dtype == _BF16:
-        code = BF16
-    elif k_pages.dtype == _E4M3:
-        code = E4M3
-    else:
-        raise MdsError(f"unsupported cache dtype {k_pages.dtype}")
-    n, p, h, d = k_pages.shape
-    return p, n, h, d, code
+def _opt(t, dtype, n, index, name):
+    return None if t is None else _vec(t, dtype, n, index, name)
+
+
+def _status(t, index):
+    if t is None:
+        return None
+    if t.numel() != 1 or t.element_size() != 4 or t.get_device() != index:
+        raise MdsError("status: one 4-byte word on the device")
+    return t.data_ptr()
+
+
+def _pages(k_pages, v_pages, index):
+    """(shape, dtype code, strides of keys, strides of values) of a pair of page arrays."""
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
+        raise MdsError("k_pages and v_pages must be [n_pages, page_size, Hkv, D] of one shape and dtype")
+    if k_pages.get_device() != index or v_pages.get_device() != index:
+        raise MdsError("the pages must be on the tensors' device")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise MdsError("pages must have a unit last stride")
+    if dtype is _BF16:
+        return shape, BF16, ks, vs
+    if dtype is _E4M3:
+        return shape, E4M3, ks, vs
+    raise MdsError(f"unsupported cache dtype {dtype}")
 
 
 def kv_page_tables(kv_len, chunk_len, block_table, pages_held, free_list, free_count, page_size, query_start, seq_lens,
@@ -89,27 +110,19 @@ def kv_page_tables(kv_len, chunk_len, block_table, pages_held, free_list, free_c
     free_list, and kv_len_out, pages_held_out, free_count_out, which may be
     the inputs. status: one 4-byte device word or None.
     """
-    dev = kv_len.device
-    _need(kv_len.is_cuda, "tensors must be on the GPU")
+    dev = _index(kv_len)
     B, N = chunk_len.numel(), kv_len.numel()
     _need(block_table.dim() == 2 and block_table.shape[0] == N, "block_table must be [n_slots, max_pages]")
     MP, T, NP = block_table.shape[1], slot_map.numel(), free_list.numel()
-    for t, dt, n, name in ((kv_len, _I32, N, "kv_len"), (chunk_len, _I32, B, "chunk_len"),
-                           (block_table, _I32, N * MP, "block_table"), (pages_held, _I32, N, "pages_held"),
-                           (free_list, _I32, NP, "free_list"), (free_count, _I32, 1, "free_count"),
-                           (query_start, _I32, B + 1, "query_start"), (seq_lens, _I32, B, "seq_lens"),
-                           (positions, _I64, T, "positions"), (slot_map, _I64, T, "slot_map"),
-                           (kv_len_out, _I32, N, "kv_len_out"), (pages_held_out, _I32, N, "pages_held_out"),
-                           (free_count_out, _I32, 1, "free_count_out")):
-        _vec(t, dt, n, dev, name)
-    _opt(idx_map, _I32, B, dev, "idx_map")
-    _opt(advance, _I32, B, dev, "advance")
-    _status(status, dev)
     _call("kv_page_tables", _lib().mds_kv_page_tables, dev, stream,
-          (B, N, MP, page_size, NP, T, _ptr(idx_map), _ptr(kv_len), _ptr(advance), advance_add, _ptr(chunk_len),
-           _ptr(block_table), _ptr(pages_held), _ptr(free_list), _ptr(free_count), _ptr(query_start), _ptr(seq_lens),
-           _ptr(positions), _ptr(slot_map), _ptr(kv_len_out), _ptr(pages_held_out), _ptr(free_count_out),
-           _ptr(status)))
+          (B, N, MP, page_size, NP, T, _opt(idx_map, _I32, B, dev, "idx_map"), _vec(kv_len, _I32, N, dev, "kv_len"),
+           _opt(advance, _I32, B, dev, "advance"), advance_add, _vec(chunk_len, _I32, B, dev, "chunk_len"),
+           _vec(block_table, _I32, N * MP, dev, "block_table"), _vec(pages_held, _I32, N, dev, "pages_held"),
+           _vec(free_list, _I32, NP, dev, "free_list"), _vec(free_count, _I32, 1, dev, "free_count"),
+           _vec(query_start, _I32, B + 1, dev, "query_start"), _vec(seq_lens, _I32, B, dev, "seq_lens"),
+           _vec(positions, _I64, T, dev, "positions"), _vec(slot_map, _I64, T, dev, "slot_map"),
+           _vec(kv_len_out, _I32, N, dev, "kv_len_out"), _vec(pages_held_out, _I32, N, dev, "pages_held_out"),
+           _vec(free_count_out, _I32, 1, dev, "free_count_out"), _status(status, dev)))
 
 
 def kv_append(k, v, k_pages, v_pages, slot_map, k_scale=None, v_scale=None, status=None, stream=None) -> None:
@@ -120,21 +133,17 @@ def kv_append(k, v, k_pages, v_pages, slot_map, k_scale=None, v_scale=None, stat
     int64 [T] (< 0 skips the row); k_scale, v_scale float32 [Hkv], needed for
     an 8-bit cache; status: one 4-byte device word or None.
     """
-    dev = k.device
-    _need(k.is_cuda, "tensors must be on the GPU")
-    P, NP, H, D, code = _pages(k_pages, v_pages, dev)
+    dev = _index(k)
+    (NP, P, H, D), code, kp, vp = _pages(k_pages, v_pages, dev)
     T = slot_map.numel()
-    _need(k.dtype == _BF16 and v.dtype == _BF16 and k.dim() == 3 and k.shape == v.shape and v.device == dev
-          and tuple(k.shape) == (T, H, D), "k and v must be bf16 [T, Hkv, D] on one device")
-    _need(T == 0 or (k.stride(2) == 1 and v.stride(2) == 1), "k and v must have a unit last stride")
-    _vec(slot_map, _I64, T, dev, "slot_map")
-    _opt(k_scale, _F32, H, dev, "k_scale")
-    _opt(v_scale, _F32, H, dev, "v_scale")
-    _status(status, dev)
-    ks, vs, kp, vp = k.stride(), v.stride(), k_pages.stride(), v_pages.stride()
+    _need(k.dtype is _BF16 and v.dtype is _BF16 and k.shape == v.shape and k.shape == (T, H, D)
+          and v.get_device() == dev, "k and v must be bf16 [T, Hkv, D] on one device")
+    ks, vs = k.stride(), v.stride()
+    _need(T == 0 or (ks[2] == 1 and vs[2] == 1), "k and v must have a unit last stride")
     _call("kv_append", _lib().mds_kv_append, dev, stream,
-          (T, H, D, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _ptr(k_pages), _ptr(v_pages), code, P, NP, kp[0],
-           kp[1], kp[2], vp[0], vp[1], vp[2], _ptr(slot_map), _ptr(k_scale), _ptr(v_scale), _ptr(status)))
+          (T, H, D, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], k_pages.data_ptr(), v_pages.data_ptr(), code,
+           P, NP, kp[0], kp[1], kp[2], vp[0], vp[1], vp[2], _vec(slot_map, _I64, T, dev, "slot_map"),
+           _opt(k_scale, _F32, H, dev, "k_scale"), _opt(v_scale, _F32, H, dev, "v_scale"), _status(status, dev)))
 
 
 def paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window=0) -> int:
@@ -156,34 +165,29 @@ def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out
     scale defaults to 1/sqrt(D); lse float32 [T, Hq] or None. Returns the
     workspace used.
     """
-    dev = q.device
-    _need(q.is_cuda, "tensors must be on the GPU")
-    P, NP, Hk, D, code = _pages(k_pages, v_pages, dev)
-    _need(q.dtype == _BF16 and out.dtype == _BF16 and q.dim() == 3 and out.shape == q.shape and q.shape[2] == D
-          and out.device == dev, "q and out must be bf16 [T, Hq, D] on one device")
-    T, Hq, _ = q.shape
-    _need(T == 0 or (q.stride(2) == 1 and out.stride(2) == 1), "q and out must have a unit last stride")
+    dev = _index(q)
+    (NP, P, Hk, D), code, kp, vp = _pages(k_pages, v_pages, dev)
+    shape = q.shape
+    _need(q.dtype is _BF16 and out.dtype is _BF16 and len(shape) == 3 and out.shape == shape and shape[2] == D
+          and out.get_device() == dev, "q and out must be bf16 [T, Hq, D] on one device")
+    T, Hq, _ = shape
+    qs, os = q.stride(), out.stride()
+    _need(T == 0 or (qs[2] == 1 and os[2] == 1), "q and out must have a unit last stride")
     B = seq_lens.numel()
     _need(block_table.dim() == 2, "block_table must be [n_slots, max_pages]")
     N, MP = block_table.shape
-    _vec(block_table, _I32, N * MP, dev, "block_table")
-    _vec(query_start, _I32, B + 1, dev, "query_start")
-    _vec(seq_lens, _I32, B, dev, "seq_lens")
-    _opt(idx_map, _I32, B, dev, "idx_map")
-    _opt(k_scale, _F32, Hk, dev, "k_scale")
-    _opt(v_scale, _F32, Hk, dev, "v_scale")
-    _opt(lse, _F32, T * Hq, dev, "lse")
     if workspace is None:
-        workspace = _workspace(None, paged_attention_workspace_bytes(T, B, Hq, Hk, D, max_q_len, max_seq_len, window),
-                               dev, stream)
+        workspace = _new_workspace(paged_attention_workspace_bytes(T, B, Hq, Hk, D, max_q_len, max_seq_len, window),
+                                   dev, stream)
     else:
-        _workspace(workspace, 0, dev, stream)
-    qs, os, kp, vp = q.stride(), out.stride(), k_pages.stride(), v_pages.stride()
+        _check_workspace(workspace, dev)
     _call("paged_attention", _lib().mds_paged_attention, dev, stream,
-          (T, B, Hq, Hk, D, _ptr(q), qs[0], qs[1], _ptr(k_pages), _ptr(v_pages), code, P, NP, kp[0], kp[1], kp[2],
-           vp[0], vp[1], vp[2], _ptr(block_table), N, MP, _ptr(idx_map), _ptr(query_start), _ptr(seq_lens), max_q_len,
-           max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, _ptr(k_scale),
-           _ptr(v_scale), _ptr(out), os[0], os[1], _ptr(lse), _ptr(workspace), workspace.numel()))
+          (T, B, Hq, Hk, D, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, kp[0], kp[1],
+           kp[2], vp[0], vp[1], vp[2], _vec(block_table, _I32, N * MP, dev, "block_table"), N, MP,
+           _opt(idx_map, _I32, B, dev, "idx_map"), _vec(query_start, _I32, B + 1, dev, "query_start"),
+           _vec(seq_lens, _I32, B, dev, "seq_lens"), max_q_len, max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale,
+           1 if causal else 0, window, _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
+           out.data_ptr(), os[0], os[1], _opt(lse, _F32, T * Hq, dev, "lse"), workspace.data_ptr(), workspace.numel()))
     return workspace
 
 
@@ -193,12 +197,12 @@ def lm_head_fp8_tiled_bytes(V, H) -> int:
     return out.value
 
 
-def _tiled_out(out, V, H, dev):
+def _tiled_out(out, V, H, dev):  # dev: the device's index
     shape = ((V + 15) // 16, 16 * H)
     n = lm_head_fp8_tiled_bytes(V, H)
     if out is None:
-        out = torch.empty(shape, dtype=_E4M3, device=dev)
-    _need(out.dtype == _E4M3 and tuple(out.shape) == shape and out.is_contiguous() and out.device == dev,
+        out = torch.empty(shape, dtype=_E4M3, device=f"cuda:{dev}")
+    _need(out.dtype is _E4M3 and out.shape == shape and out.is_contiguous() and out.get_device() == dev,
           "the tiled matrix must be contiguous float8_e4m3fn [ceil(V/16), 16 H]")
     return out, n
 
@@ -209,8 +213,9 @@ def tile_lm_head_fp8(codes, out=None, stream=None):
     _need(codes.is_cuda and codes.dtype == _E4M3 and codes.dim() == 2 and codes.is_contiguous(),
           "codes must be a contiguous float8_e4m3fn [V, H] GPU tensor")
     V, H = codes.shape
-    out, n = _tiled_out(out, V, H, codes.device)
-    _call("tile_lm_head_fp8", _lib().mds_tile_lm_head_fp8, codes.device, stream, (V, H, _ptr(codes), _ptr(out), n))
+    dev = _index(codes)
+    out, n = _tiled_out(out, V, H, dev)
+    _call("tile_lm_head_fp8", _lib().mds_tile_lm_head_fp8, dev, stream, (V, H, codes.data_ptr(), out.data_ptr(), n))
     return out
 
 
@@ -220,14 +225,13 @@ def quantize_lm_head_fp8(lm_head, out=None, scales=None, stream=None):
     _need(lm_head.is_cuda and lm_head.dtype == _BF16 and lm_head.dim() == 2 and lm_head.is_contiguous(),
           "lm_head must be a contiguous bf16 [V, H] GPU tensor")
     V, H = lm_head.shape
-    dev = lm_head.device
+    dev = _index(lm_head)
     out, n = _tiled_out(out, V, H, dev)
     blocks = ((V + 127) // 128, H // 128)
     if scales is None:
-        scales = torch.empty(blocks, dtype=_F32, device=dev)
-    _vec(scales, _F32, blocks[0] * blocks[1], dev, "scales")
+        scales = torch.empty(blocks, dtype=_F32, device=f"cuda:{dev}")
     _call("quantize_lm_head_fp8", _lib().mds_quantize_lm_head_fp8, dev, stream,
-          (V, H, _ptr(lm_head), _ptr(out), n, _ptr(scales)))
+          (V, H, lm_head.data_ptr(), out.data_ptr(), n, _vec(scales, _F32, blocks[0] * blocks[1], dev, "scales")))
     return out, scales
 
 
@@ -245,27 +249,28 @@ def lm_head_fp8(hidden, lm_head, scales, out, K, workspace=None, stream=None):
     [B, >=K, V] with unit column stride (rows k < K are written). Returns the
     workspace used.
     """
-    dev = hidden.device
-    _need(hidden.is_cuda and hidden.dtype == _BF16 and hidden.dim() == 2 and hidden.stride(1) == 1 and K >= 1
-          and hidden.shape[0] % K == 0, "hidden must be bf16 [B*K, H] with unit column stride")
-    B, H = hidden.shape[0] // K, hidden.shape[1]
-    _need(out.dim() == 3 and out.shape[0] == B and out.shape[1] >= K and out.stride(2) == 1 and out.device == dev,
+    dev = _index(hidden)
+    _need(hidden.dtype is _BF16 and hidden.dim() == 2 and hidden.stride(1) == 1 and K >= 1 and hidden.shape[0] % K == 0,
+          "hidden must be bf16 [B*K, H] with unit column stride")
+    rows, H = hidden.shape
+    B = rows // K
+    _need(out.dim() == 3 and out.shape[0] == B and out.shape[1] >= K and out.stride(2) == 1 and out.get_device() == dev,
           "out must be [B, >=K, V] with unit column stride")
     V = out.shape[2]
-    _need(lm_head.dtype == _E4M3 and lm_head.is_contiguous() and lm_head.device == dev
-          and tuple(lm_head.shape) == ((V + 15) // 16, 16 * H), "lm_head must be the tiled [ceil(V/16), 16 H]")
-    _vec(scales, _F32, ((V + 127) // 128) * (H // 128), dev, "scales")
-    if out.dtype == _F32:
+    _need(lm_head.dtype is _E4M3 and lm_head.is_contiguous() and lm_head.get_device() == dev
+          and lm_head.shape == ((V + 15) // 16, 16 * H), "lm_head must be the tiled [ceil(V/16), 16 H]")
+    if out.dtype is _F32:
         code = F32
-    elif out.dtype == _BF16:
+    elif out.dtype is _BF16:
         code = BF16
     else:
         raise MdsError(f"unsupported dtype {out.dtype}")
     if workspace is None:
-        workspace = _workspace(None, lm_head_fp8_workspace_bytes(B, K, V, H), dev, stream)
+        workspace = _new_workspace(lm_head_fp8_workspace_bytes(B, K, V, H), dev, stream)
     else:
-        _workspace(workspace, 0, dev, stream)
+        _check_workspace(workspace, dev)
     _call("lm_head_fp8", _lib().mds_lm_head_fp8, dev, stream,
-          (B, K, V, H, _ptr(hidden), hidden.stride(0), _ptr(lm_head), _ptr(scales), _ptr(out), code, out.stride(0),
-           out.stride(1), _ptr(workspace), workspace.numel()))
+          (B, K, V, H, hidden.data_ptr(), hidden.stride(0), lm_head.data_ptr(),
+           _vec(scales, _F32, ((V + 127) // 128) * (H // 128), dev, "scales"), out.data_ptr(), code, out.stride(0),
+           out.stride(1), workspace.data_ptr(), workspace.numel()))
     return workspace

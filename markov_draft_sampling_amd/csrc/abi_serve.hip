@@ -52,8 +52,8 @@ int check_batch(int B, int n_slots, int max_pages, int lg, bool idx) {
   if (B < 1 || B > kMaxBatch) return abi_fail(MDS_ERR_INVALID_ARG, "B must be in [1, 65535]");
   if (n_slots < 1 || n_slots > kMaxSlots) return abi_fail(MDS_ERR_INVALID_ARG, "n_slots must be in [1, 2^17]");
   if (!idx && n_slots < B) return abi_fail(MDS_ERR_INVALID_ARG, "without idx_map: n_slots >= B");
-  if (max_pages < 1 || ((long long)max_pages << lg) > (1LL << 30))
-    return abi_fail(MDS_ERR_INVALID_ARG, "max_pages must be >= 1 and max_pages * page_size at most 2^30");
+  if (max_pages < 1 || ((long long)max_pages << lg) >= (1LL << 30))
+    return abi_fail(MDS_ERR_INVALID_ARG, "max_pages must be >= 1 and max_pages * page_size below 2^30");
   return MDS_OK;
 }
 
