@@ -504,7 +504,8 @@ int mds_debug_gumbel(int n, const uint32_t* words, float* gumbel, void* stream);
  * page_size tokens a page, page_size a power of two in [16, 1024]: element
  * (page, i, head, d) of a page array at page*page_stride + i*slot_stride +
  * head*head_stride + d, in elements, the array 16-byte aligned and the strides
- * whole multiples of 16 bytes (else MDS_ERR_UNSUPPORTED). Slot
+ * whole multiples of 16 bytes (else MDS_ERR_UNSUPPORTED), the slots of a page
+ * spanning less than 2 GiB. Slot
  * page*page_size + i names token i of a page. A state slot's block table row
  * [max_pages] lists its pages in order of position; position p of the request
  * is token p % page_size of page block_table[s][p / page_size].

@@ -30,12 +30,13 @@ int check_page(int page_size, int n_pages, int* lg) {
 
 // [n_pages][P][Hkv][D] pages of `es`-byte elements with a unit last stride: 16-byte aligned, strides that
 // are whole 16-byte pieces and fit the kernels' 32-bit offsets inside a page
-int check_pages(const void* p, int es, int64_t ps, int64_t ts, int64_t hs) {
+int check_pages(const void* p, int es, int64_t ps, int64_t ts, int64_t hs, int page_size) {
   const int64_t e16 = 16 / es;
   if (!aligned(p, 16) || ps % e16 || ts % e16 || hs % e16)
     return abi_fail(MDS_ERR_UNSUPPORTED, "pages must be 16-byte aligned with strides that are multiples of 16 bytes");
-  if (ps < 0 || ts < 0 || hs < 0 || ts * es > (1 << 26))
-    return abi_fail(MDS_ERR_INVALID_ARG, "page strides must be >= 0, a token's at most 64 MiB");
+  if (ps < 0 || ts < 0 || hs < 0 || ps > (int64_t{1} << 40) || ts > (1 << 30) || hs > (int64_t{1} << 40) ||
+      ts * es * page_size >= (1LL << 31))
+    return abi_fail(MDS_ERR_INVALID_ARG, "page strides must be >= 0, and a page's slots span less than 2 GiB");
   return MDS_OK;
 }
 
@@ -262,8 +263,8 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
   if (!k_pages || !v_pages || (T && (!k || !v || !slot_map)) || (a.e4m3 && (!k_scale || !v_scale)))
     return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   const int es = a.e4m3 ? 1 : 2;
-  if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride)) ||
-      (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride)))
+  if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride, page_size)) ||
+      (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride, page_size)))
     return rc;
   Dim kd[3] = {{n_pages, k_page_stride}, {page_size, k_slot_stride}, {Hkv, k_pages_head_stride}};
   Dim vd[3] = {{n_pages, v_page_stride}, {page_size, v_slot_stride}, {Hkv, v_pages_head_stride}};
@@ -332,8 +333,8 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   if (!(scale > 0.0f) || !(scale < 1e30f)) return abi_fail(MDS_ERR_INVALID_ARG, "scale must be positive and finite");
   if (causal != 0 && causal != 1) return abi_fail(MDS_ERR_INVALID_ARG, "causal must be 0 or 1");
   const int es = a.e4m3 ? 1 : 2;
-  if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride)) ||
-      (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride)))
+  if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride, page_size)) ||
+      (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride, page_size)))
     return rc;
   if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 ||
       out_head_stride % 8)

@@ -50,7 +50,7 @@ struct Tile {
   int b, slot, q0, n, r0, rows;  // request, state slot, first token, tokens, first row, rows (0: nothing to do)
   int seq, lim;                  // sequence length, and that within the block table
   int lo, hi;                    // keys that some row sees: [lo, hi)
-  int base;                      // lo rounded down to a block
+  int base;                      // lo rounded down to a block of 64
   int chunks;                    // chunks with keys (at least 1)
 };
 
@@ -123,7 +123,7 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, uint
   token_keys(a, t, (t.r0 + t.rows - 1) / a.G, l1, t.hi);
   t.hi = max(t.hi, 0);
   t.lo = min(t.lo, t.hi);
-  t.base = t.lo & ~31;
+  t.base = t.lo & ~63;
   t.chunks = min(max((t.hi - t.base + a.chunk - 1) / a.chunk, 1), a.n_chunks);
   return t;
 }
@@ -150,39 +150,12 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const Tile& t,
     a.lse[(long long)(t.q0 + tok) * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Transposing LDS reads, a group of 16 lanes reading 4 (8) keys of 16 columns, and the wait for them: as
-// one asm block, since the compiler would have the intrinsics wait for every copy in flight.
-// F[q]: the 4 keys at a[q] and the 4 at a[q] + OFF.
-template <int OFF>
-__device__ __forceinline__ void read_tr16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, bf16x8 (&F)[4]) {
-  u32x2 x[8];
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %8\n\t"
-      "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %2, %9\n\t"
-      "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %4, %10\n\t"
-      "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %6, %11\n\t"
-      "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
-      : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(OFF)
-      : "memory");
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    F[q] = __builtin_bit_cast(bf16x8, u32x4{x[2 * q][0], x[2 * q][1], x[2 * q + 1][0], x[2 * q + 1][1]});
+// Transposing LDS reads, a group of 16 lanes reading 4 (8) keys of 16 columns: a lane gets its column's.
+__device__ __forceinline__ s16x4 read_tr16(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MDS_LDS s16x4*)(uintptr_t)at);
 }
-__device__ __forceinline__ void read_tr8(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, i32x2 (&x)[4]) {
-  asm volatile(
-      "ds_read_b64_tr_b8 %0, %4\n\t"
-      "ds_read_b64_tr_b8 %1, %5\n\t"
-      "ds_read_b64_tr_b8 %2, %6\n\t"
-      "ds_read_b64_tr_b8 %3, %7\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
-      : "v"(a0), "v"(a1), "v"(a2), "v"(a3)
-      : "memory");
+__device__ __forceinline__ i32x2 read_tr8(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((MDS_LDS i32x2*)(uintptr_t)at);
 }
 
 // 16 bytes a lane straight into LDS at `lds` (uniform) + 16 * lane, from base (uniform) + off. As assembly:
@@ -197,29 +170,33 @@ __device__ __forceinline__ void wait_copies() {  // at most N of this wave's cop
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// D: head dimension; E4M3: 8-bit cache; NB: 16-row blocks a wave; RG x KG waves: RG groups of rows, KG of keys
-template <int D, bool E4M3, int NB, int RG, int KG>
+// D: head dimension; E4M3: 8-bit cache; NB: 16-row blocks a wave; RG x KG waves: RG groups of rows, KG of keys;
+// KB: keys of a block; LB: KB of LDS for the ring
+template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
 struct AttnShape {
   static constexpr int kRows = NB * 16 * RG;
   static constexpr int RB = D * (E4M3 ? 1 : 2);  // bytes of a key (or value)
-  static constexpr int kPart = 32 * RB;          // bytes of a block's keys
-  static constexpr int kStage = 2 * kPart;       // a block of 32 keys and values
-  // blocks in flight per key group: what fits 128 KB, four at most
-  static constexpr int NST = KG * kStage * 4 <= 131072 ? 4 : KG * kStage * 3 <= 131072 ? 3 : 2;
+  static constexpr int kPart = KB * RB;          // bytes of a block's keys
+  static constexpr int kStage = 2 * kPart;       // a block of keys and values
+  // blocks in flight per key group: what fits, four at most
+  static constexpr int NST = KG * kStage * 4 <= LB * 1024 ? 4 : KG * kStage * 3 <= LB * 1024 ? 3 : 2;
   static constexpr int kRing = KG * kStage * NST;
   static constexpr int kJoin = RG * KG * 16 * D * 4;  // the waves' o, 16 rows each
   static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
 };
 
-template <int D, bool E4M3, int NB, int RG, int KG>
-__global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG * KG / 4, RG * KG / 4))) void attn_kernel(
+template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
+__global__ __launch_bounds__(64 * RG * KG) __attribute__((
+    amdgpu_waves_per_eu(RG * KG / 4 * (LB <= 64 ? 2 : 1), RG * KG / 4 * (LB <= 64 ? 2 : 1)))) void attn_kernel(
     PagedAttnArgs a) {
-  using Sh = AttnShape<D, E4M3, NB, RG, KG>;
+  using Sh = AttnShape<D, E4M3, NB, RG, KG, KB, LB>;
   constexpr int ROWS = Sh::kRows, RB = Sh::RB, kPart = Sh::kPart, kStage = Sh::kStage, NST = Sh::NST;
   constexpr int SPR = RB / 16;                 // 16-byte slots of a key
   constexpr int RPI = 64 / SPR;                // keys per copy (1 KB)
-  constexpr int NI = 32 / RPI;                 // copies of a block's keys (as many for its values)
-  constexpr int kMine = (2 * NI + RG - 1) / RG;  // of them, a wave's (the RG waves of a key group share a block)
+  constexpr int NI = KB / RPI;                 // copies of a block's keys (as many for its values)
+  constexpr int NH = KB / 16;                  // half blocks of 16 keys, each in one page
+  constexpr int NP = 64 / NH;                  // blocks whose page ids a wave holds
+  constexpr int kMine = (NI + RG - 1) / RG;    // of them, a wave's (the RG waves of a key group share a block)
   constexpr int NS = D / 32;                   // 32-wide slices of the first product
   constexpr int ND = D / 16;                   // 16-wide column blocks of the second
   __shared__ __attribute__((aligned(16))) unsigned char s_kv[Sh::kLds];
@@ -240,7 +217,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
   }
   const int c0 = t.base + c * a.chunk;
   const int lo = max(t.lo, c0), hi = c == a.n_chunks - 1 ? t.hi : min(t.hi, c0 + a.chunk);
-  const int nblk = hi > lo ? (hi - c0 + 31) >> 5 : 0;
+  const int nblk = hi > lo ? (hi - c0 + KB - 1) / KB : 0;
   const int nit = (nblk + KG - 1) / KG;                 // rounds; key group kg takes blocks kg, kg + KG, ..
   const int nmy = nblk > kg ? (nblk - kg + KG - 1) / KG : 0;  // of them, its own
 
@@ -282,21 +259,22 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
   const char* kb_h = (const char*)a.k_pages + h * a.k_hs;
   const char* vb_h = (const char*)a.v_pages + h * a.v_hs;
   const int pmask = (1 << a.page_log2) - 1;
-  // this wave's copies of a block: number x = rg + RG n, keys for x < NI, values above. Offset of a lane's 16
-  // bytes from the first key of the half block (16 keys, which lie in one page)
-  uint32_t off[kMine];
+  // this wave's copies of a block: numbers rg + RG m of its keys and of its values. Offsets of a lane's 16 bytes
+  // from the first of the 16 keys (which lie in one page) that the copy is part of
+  uint32_t ko[kMine], vo[kMine];
 #pragma unroll
-  for (int n = 0; n < kMine; ++n) {
-    const int x = rg + RG * n, p = x % NI, r = p * RPI + lrow;
-    const bool v = x >= NI;
-    off[n] = (uint32_t)((r & 15) * (int)(v ? a.v_ts : a.k_ts)) + (uint32_t)((lslot ^ (v ? vswz(r) : kswz(r))) * 16);
+  for (int m = 0; m < kMine; ++m) {
+    const int r = ((rg + RG * m) * RPI + lrow) % KB;
+    ko[m] = (uint32_t)((r & 15) * (int)a.k_ts) + (uint32_t)((lslot ^ kswz(r)) * 16);
+    vo[m] = (uint32_t)((r & 15) * (int)a.v_ts) + (uint32_t)((lslot ^ vswz(r)) * 16);
   }
-  // Page ids of the key group's blocks i0 .. i0 + 31: lane 2 (i - i0) + j has the page of half j of block i.
+  // Page ids of the key group's blocks i0 .. i0 + NP - 1: lane NH (i - i0) + j has the page of 16-key piece j of
+  // block i.
   // Keys outside [lo, hi) repeat the nearest one inside: what lies behind a sequence's end is never read, and
   // their probability is zero.
   int pages = 0;
   auto load_pages = [&](int i0) {
-    const int kh = c0 + (kg + KG * (i0 + (lane >> 1))) * 32 + 16 * (lane & 1);
+    const int kh = c0 + (kg + KG * (i0 + lane / NH)) * KB + 16 * (lane % NH);
     pages = trow[min(max(kh, lo), hi - 1) >> a.page_log2];
     if ((unsigned)pages >= (unsigned)a.n_pages) {
       pages = 0;
@@ -304,32 +282,26 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
     }
   };
   auto copy_block = [&](int i, int st) {
-    if (i && (i & 31) == 0) load_pages(i);
-    const int k0 = c0 + (kg + KG * i) * 32;
-    const bool inside = k0 >= lo && k0 + 32 <= hi;
-    const char* kp[2];
-    const char* vp[2];
-    int kc[2];
+    if (i && i % NP == 0) load_pages(i);
+    const int k0 = c0 + (kg + KG * i) * KB;
+    const bool inside = k0 >= lo && k0 + KB <= hi;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      kc[j] = min(max(k0 + 16 * j, lo), hi - 1);
-      const int pg = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + j);
-      kp[j] = kb_h + pg * a.k_ps + (kc[j] & pmask) * a.k_ts;
-      vp[j] = vb_h + pg * a.v_ps + (kc[j] & pmask) * a.v_ts;
-    }
-#pragma unroll
-    for (int n = 0; n < kMine; ++n) {
-      const int x = rg + RG * n;
-      if ((2 * NI) % RG != 0 && x >= 2 * NI) break;
-      const int p = x % NI, j = p >= NI / 2;
-      const bool v = x >= NI;
-      uint32_t o = off[n];
+    for (int m = 0; m < kMine; ++m) {
+      const int p = rg + RG * m, j = p * RPI / 16;  // copy p lies in 16-key piece j
+      if (NI % RG != 0 && p >= NI) break;
+      const int kc = min(max(k0 + 16 * j, lo), hi - 1);
+      const int pg = __builtin_amdgcn_readlane(pages, NH * (i % NP) + j);
+      const char* kp = kb_h + pg * a.k_ps + (kc & pmask) * (int)a.k_ts;
+      const char* vp = vb_h + pg * a.v_ps + (kc & pmask) * (int)a.v_ts;
+      uint32_t kof = ko[m], vof = vo[m];
       if (!inside) {
         const int r = (p * RPI + lrow) & 15;
-        const int d = min(max(k0 + 16 * j + r, lo), hi - 1) - kc[j] - r;  // from the row's own place to the key copied
-        o = (uint32_t)((int)o + d * (int)(v ? a.v_ts : a.k_ts));
+        const int d = min(max(k0 + 16 * j + r, lo), hi - 1) - kc - r;  // from the row's own place to the key copied
+        kof = (uint32_t)((int)kof + d * (int)a.k_ts);
+        vof = (uint32_t)((int)vof + d * (int)a.v_ts);
       }
-      copy_1k(v ? vp[j] : kp[j], o, ring + st * kStage + x * 1024);
+      copy_1k(kp, kof, ring + st * kStage + p * 1024);
+      copy_1k(vp, vof, ring + st * kStage + kPart + p * 1024);
     }
   };
 
@@ -363,12 +335,13 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
     return up ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true))
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
   };
+  constexpr int NK = KB / 16;
   auto block = [&](int st, int i) {
-    const int k0 = c0 + (kg + KG * i) * 32;
+    const int k0 = c0 + (kg + KG * i) * KB;
     const unsigned char* buf = s_kv + (kg * NST + st) * kStage;
-    floatx4 S[2][NB];
+    floatx4 S[NK][NB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < NK; ++kb) {
       const int r = kb * 16 + lr;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) S[kb][nb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -393,9 +366,9 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
           S[kb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[s], Q[nb][s], S[kb][nb], 0, 0, 0);
     }
     // lane: row lr of each nb, keys k0 + 16 kb + 4 lg + i
-    if (k0 < all_lo || k0 + 32 > all_hi) {
+    if (k0 < all_lo || k0 + KB > all_hi) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -408,8 +381,10 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
     bool grow = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const floatx4 x = S[0][nb], y = S[1][nb];
-      top[nb] = fmaxf(fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), x[3]), fmaxf(fmaxf(fmaxf(y[0], y[1]), y[2]), y[3])) * sc;
+      float x = S[0][nb][0];
+#pragma unroll
+      for (int e = 1; e < 4 * NK; ++e) x = fmaxf(x, S[e >> 2][nb][e & 3]);
+      top[nb] = x * sc;
       grow |= top[nb] > m[nb] + kRescale;
     }
     if (__any(grow)) {
@@ -426,36 +401,36 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
         for (int d = 0; d < ND; ++d) O[nb][d] *= f;
       }
     }
-    bf16x8 P[NB];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[e >> 2][nb][e & 3], sc, -mc[nb]));
-      l[nb] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) P[nb][e] = (__bf16)p[e];
-    }
-    // values: lane column d = 16 db + lr, keys 4 lg + (0 .. 3) and 16 + 4 lg + (0 .. 3)
+    // values: lane column d = 16 db + lr, keys 4 lg + (0 .. 3) and 16 + 4 lg + (0 .. 3) of each 32
     const uint32_t vb = ring + st * kStage + kPart;
 #pragma unroll
-    for (int d0 = 0; d0 < ND; d0 += 4) {
-      bf16x8 Vf[4];
-      if constexpr (E4M3) {
-        i32x2 x[4];
-        read_tr8(vb + va[d0], vb + va[d0 + 1], vb + va[d0 + 2], vb + va[d0 + 3], x);
+    for (int k2 = 0; k2 < NK / 2; ++k2) {
+      bf16x8 P[NB];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          Vf[q] = __builtin_bit_cast(bf16x8, u32x4{widen(x[q][0], false), widen(x[q][0], true), widen(x[q][1], false),
-                                                   widen(x[q][1], true)});
-      } else {
-        read_tr16<16 * RB>(vb + va[d0], vb + va[d0 + 1], vb + va[d0 + 2], vb + va[d0 + 3], Vf);
+      for (int nb = 0; nb < NB; ++nb) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[2 * k2 + (e >> 2)][nb][e & 3], sc, -mc[nb]));
+        l[nb] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) P[nb][e] = (__bf16)p[e];
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int db = 0; db < ND; ++db) {
+        const uint32_t at = vb + k2 * 32 * RB + va[db];
+        bf16x8 V;
+        if constexpr (E4M3) {
+          const i32x2 x = read_tr8(at);
+          V = __builtin_bit_cast(bf16x8, u32x4{widen(x[0], false), widen(x[0], true), widen(x[1], false), widen(x[1], true)});
+        } else {
+          const s16x4 x = read_tr16(at), y = read_tr16(at + 16 * RB);
+          V = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          O[nb][d0 + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Vf[q], P[nb], O[nb][d0 + q], 0, 0, 0);
+          O[nb][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, P[nb], O[nb][db], 0, 0, 0);
+      }
     }
   };
 
@@ -484,7 +459,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
   } else {
     // the RG waves of a key group share its blocks: one barrier a round, after which block i is there for all of
     // them and the place of block i - 1 is free
-    constexpr int kLeast = 2 * NI / RG;  // copies that every wave of the group makes of a block
+    constexpr int kLeast = 2 * (NI / RG);  // copies that every wave of the group makes of a block
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i)
       if (i < nmy) copy_block(i, i);
@@ -498,8 +473,8 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(RG
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (i + NST - 1 < nmy) copy_block(i + NST - 1, st == 0 ? NST - 1 : st - 1);
       if (i < nmy) {
-        const int k0 = c0 + (kg + KG * i) * 32;
-        if (k0 < any_hi && k0 + 32 > any_lo) block(st, i);  // else no row of this wave sees a key of it
+        const int k0 = c0 + (kg + KG * i) * KB;
+        if (k0 < any_hi && k0 + KB > any_lo) block(st, i);  // else no row of this wave sees a key of it
       }
       st = st + 1 == NST ? 0 : st + 1;
     }
@@ -613,11 +588,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
   if (g == 0) store_row(a, t, row, h, od, o, M, L);
 }
 
-template <int D, bool E4M3, int NB, int RG, int KG>
+template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
 hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
-  constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG>::kRows;
+  constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG, KB, LB>::kRows;
   const long long wgs = (long long)a.tiles * a.Hkv;
-  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0, st, a);
+  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
   hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)wgs, ROWS / 4), dim3(256), 0, st, a);
@@ -627,10 +602,10 @@ hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
 template <int D, bool E4M3>
 hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
   switch (rows) {
-    case 16: return launch_shape<D, E4M3, 1, 1, 4>(a, st);
-    case 32: return launch_shape<D, E4M3, 2, 1, 4>(a, st);
-    case 64: return launch_shape<D, E4M3, 2, 2, 4>(a, st);
-    default: return launch_shape<D, E4M3, 2, 8, 1>(a, st);
+    case 16: return launch_shape<D, E4M3, 1, 1, 4, 32, 128>(a, st);
+    case 32: return launch_shape<D, E4M3, 2, 1, 4, 32, 128>(a, st);
+    case 64: return launch_shape<D, E4M3, 2, 2, 2, 32, 64>(a, st);
+    default: return launch_shape<D, E4M3, 2, 4, 1, 64, 64>(a, st);
   }
 }
 
@@ -639,7 +614,7 @@ hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
 AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
   AttnPlan p;
   const long long most = (long long)max_q_len * G;  // rows of the longest request
-  p.rows = most <= 16 ? 16 : most <= 32 ? 32 : most <= 128 ? 64 : 256;
+  p.rows = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
   const long long direct = (most + p.rows - 1) / p.rows;
   const long long by_rows = (long long)T * G / p.rows + B;
   p.per_req = direct * B <= by_rows ? (int)direct : 0;
@@ -652,11 +627,11 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   if (window > 0) span = span < (long long)window + max_q_len ? span : (long long)window + max_q_len;
   const long long wgs = (long long)p.tiles * Hkv;
   const long long want = (256 + wgs - 1) / wgs;
-  long long chunk = (span + 32 + want - 1) / want;
+  long long chunk = (span + 64 + want - 1) / want;
   if (chunk > 16384) chunk = 16384;
   chunk = (chunk + 127) / 128 * 128;
   if (chunk < 256) chunk = 256;
-  long long n = (span + 31 + chunk - 1) / chunk;
+  long long n = (span + 63 + chunk - 1) / chunk;
   if (n < 1) n = 1;
   p.chunk = (int)chunk;
   p.n_chunks = (int)n;
