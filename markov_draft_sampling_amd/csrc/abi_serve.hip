@@ -382,6 +382,7 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   a.lse = lse;
   a.tiles = p.tiles;
   a.per_req = p.per_req;
+  a.by_length = p.by_length;
   a.chunk = p.chunk;
   a.n_chunks = p.n_chunks;
   a.part_o = (float*)((unsigned char*)workspace + p.part_o);

@@ -334,6 +334,7 @@ struct PagedAttnArgs {
   // plan (attn_plan): row tiles and key chunks
   int tiles;                         // row tiles of the launch, over all requests
   int per_req;                       // row tiles per request (> 0), or 0: tile of a request by its row offset
+  int by_length;                     // tiles in the order of falling sequence length (per_req > 0, B <= 128)
   int chunk, n_chunks;               // keys per chunk; the last chunk takes what is left
   float* part_o;                     // [n_chunks][tiles][Hkv][rows][D] (n_chunks > 1)
   float2* part_ml;                   // [n_chunks][tiles][Hkv][rows] (max, sum) in base 2
@@ -342,6 +343,7 @@ struct PagedAttnArgs {
 // Row tiles, chunks and workspace bytes of a call (host only); cus: compute units.
 struct AttnPlan {
   int rows, tiles, per_req, chunk, n_chunks;
+  bool by_length;
   size_t part_o, part_ml, total;  // workspace offsets and size
 };
 AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window);

@@ -159,6 +159,46 @@ def test_many_requests_and_empty_ones():
     _case(ctx, chunk, 2, 1, 64, 16, seed=7)
 
 
+@pytest.mark.parametrize("B,Hk", [(40, 8), (100, 4), (128, 3)])
+def test_longest_first_order(B, Hk):
+    # more work-groups than the CUs hold: requests are taken by falling length (ties, empty ones and all)
+    rng = np.random.default_rng(B)
+    ctx = rng.choice([0, 3, 3, 40, 77, 130], B).tolist()
+    chunk = rng.choice([1, 1, 2, 0], B).tolist()
+    _case(ctx, chunk, 2 * Hk, Hk, 64, 16, seed=B, idx=True)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 20, 100])
+@pytest.mark.parametrize("window", [0, 9])
+def test_infinities_and_nan_stay_with_the_rows_that_see_them(rows, window):
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    D, P, L = 64, 16, 200
+    n = rows
+    g = torch.Generator().manual_seed(rows)
+    q = torch.randn(n, 2, D, generator=g).to(torch.bfloat16)
+    k = torch.randn(16, P, 1, D, generator=g).to(torch.bfloat16)
+    v = torch.randn(16, P, 1, D, generator=g).to(torch.bfloat16)
+    kf, vf = k.view(-1, D), v.view(-1, D)
+    inf, nan = float("inf"), float("nan")
+    # seen by the last rows only (causal), and by the first rows only (window)
+    vf[L - 1, 3], vf[L - 1, 4], vf[L - 1, 5] = inf, nan, -inf
+    vf[L - 2, 3] = -inf
+    kf[L - 1, 0] = nan
+    vf[L - n - 8 if window else 5, 7] = inf
+    kf[L - n - 8 if window else 6, 1] = 1.0
+    out, lse = torch.zeros_like(q).cuda(), torch.zeros(n, 2, device="cuda")
+    table = t([list(range(16))])
+    mds.paged_attention(q.cuda(), k.cuda(), v.cuda(), table, t([0, n]), t([L]), out, n, L, window=window, lse=lse)
+    ref, _, _, _ = sr.attention(q, k, v, table.cpu().numpy(), [0, n], [L], 1 / math.sqrt(D), True, window)
+    o = out.cpu().double()
+    assert torch.equal(torch.isnan(o), torch.isnan(ref))
+    assert torch.equal(torch.isinf(o), torch.isinf(ref)) and torch.equal(o[torch.isinf(o)], ref[torch.isinf(ref)])
+    ok = torch.isfinite(ref)
+    assert ((o - ref).abs()[ok] < 2.0 ** -8 * (ref.abs()[ok] + 4.0)).all()
+
+
 def test_requests_without_keys_give_zero():
     import torch
     import markov_draft_sampling_amd as mds
