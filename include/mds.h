@@ -659,7 +659,8 @@ int mds_quantize_lm_head_fp8(int V, int H, const void* lm_head, void* tiled, siz
  * logits. Arguments as for mds_draft_lm_head, with 1 <= K <= 64; lm_head in
  * the tiled order, 16-byte aligned; workspace of
  * mds_lm_head_fp8_workspace_bytes(B, K, V, H), 256-byte aligned, without state.
- * Two launches; the matrix is read once for up to 224 rows.
+ * Two launches; the matrix is read once for up to 112 rows, and for more once
+ * from memory and then from the caches.
  */
 int mds_lm_head_fp8_workspace_bytes(int B, int K, int V, int H, size_t* out_bytes);
 int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidden_row_stride, const void* lm_head,

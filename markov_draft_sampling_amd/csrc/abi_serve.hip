@@ -123,7 +123,7 @@ int lm_head_fp8_rows(int B, int K, int* rows) {
 size_t lm_head_fp8_ws(int rows, int H) {
   const int mb = mds::lm_head_fp8_blocks(rows);
   const size_t tiles = (size_t)((rows + 15) / 16 + mb - 1) / mb;
-  return tiles * (H / 64) * mds::fp8_unit_bytes(mb);
+  return tiles * (H / 128) * mds::fp8_stage_bytes(mb);
 }
 
 }  // namespace

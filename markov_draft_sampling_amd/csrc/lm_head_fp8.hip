@@ -12,17 +12,17 @@
 // the float32 total.
 //
 // The matrix is kept in tiles of 16 rows by 128 columns in operand order
-// (fp8_tile_index): a wave reads its operands straight into registers as 1 KB
-// runs, a chunk (128 columns) or more ahead, and widens them there; which
-// columns a lane holds does not matter as long as both operands agree. The
-// quantising kernel writes the hidden rows' codes, widened to bf16, in the
-// same order, chunk by chunk with the rows' scales behind, so that a chunk goes
-// into LDS as one linear copy without registers, shared by the waves.
+// (fp8_tile_index): a wave reads its operands as 1 KB runs, straight into
+// registers or its own part of LDS, and widens them there; which columns a
+// lane holds does not matter as long as both operands agree. The quantising
+// kernel writes the hidden rows' codes in the same order, chunk (128 columns)
+// by chunk with the rows' scales behind, so that a chunk goes into LDS as one
+// linear copy without registers, shared by the waves.
 //
-// Bound by the matrix's V * H bytes for few rows; at 224 rows by the matrix
-// cores and the LDS reads of the hidden rows, which is why a wave takes 64
-// vocabulary rows (every hidden operand serves four products) and two waves
-// share a vocabulary tile, each with half the hidden rows.
+// For few rows the call is bound by the matrix's V * H bytes (7 rows, V =
+// 200064, H = 4096: 149 us, 5.5 TB/s); at 224 rows by the matrix cores and the
+// operand reads from LDS (382 us, 960 TFLOP/s), which is why a wave takes 64
+// vocabulary rows: every hidden operand serves four products.
 #include "mds_device.h"
 #include "mds_internal.h"
 
@@ -53,8 +53,6 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
 }
 
 // Hidden rows: a wave per 16 rows and 128 columns, a lane 32 columns of a row.
-// Column c of row r of a block goes to unit c / 64, 1 KB run c / 8 % 2 of it, lane (c / 16 % 4) * 16 + r; both
-// units of a chunk have its scales.
 __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int HB = a.H >> 7, MBt = (a.M + 15) >> 4;
   const int wv = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -63,9 +61,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int mb = wv % MBt, j = wv / MBt;
   const int r = lane >> 2, m = mb * 16 + r, c0 = (lane & 3) * 32;
   const int mt = mb / a.mb, mi = mb - mt * a.mb;
-  uint8_t* unit = a.xq + (((size_t)mt * HB + j) * 2 + (c0 >> 6)) * fp8_unit_bytes(a.mb);
-  uint8_t* dst = unit + mi * 2048 + ((c0 >> 4 & 3) * 16 + r) * 16;
-  float* xs = (float*)(unit + a.mb * 2048) + mi * 16 + r;
+  uint8_t* stage = a.xq + ((size_t)mt * HB + j) * fp8_stage_bytes(a.mb);
+  uint8_t* dst = stage + mi * 2048 + (c0 >> 4) * 256 + r * 16;
+  float* xs = (float*)(stage + a.mb * 2048) + mi * 16 + r;
   float x[32];
   if (m < a.M) {
     const uint16_t* src = a.hidden + (long long)m * a.hidden_rs + j * 128 + c0;
@@ -88,17 +86,17 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   am = fmaxf(am, __shfl_xor(am, 1));
   am = fmaxf(am, __shfl_xor(am, 2));
   const float s = am / kE4m3Max;
-  // 16 columns (two runs) from c0, 16 from c0 + 16 (the next 16 lanes of the same runs)
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
+  for (int q = 0; q < 2; ++q) {
+    uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float* y = x + q * 16 + e * 8;
-      const uint32_t lo = quant4(clamp_e4m3(y[0] / s), clamp_e4m3(y[1] / s), clamp_e4m3(y[2] / s), clamp_e4m3(y[3] / s));
-      const uint32_t hi = quant4(clamp_e4m3(y[4] / s), clamp_e4m3(y[5] / s), clamp_e4m3(y[6] / s), clamp_e4m3(y[7] / s));
-      *(bf16x8*)(dst + e * 1024 + q * 256) = widen8(lo, hi);
+    for (int e = 0; e < 4; ++e) {
+      const float* y = x + q * 16 + e * 4;
+      o[e] = quant4(clamp_e4m3(y[0] / s), clamp_e4m3(y[1] / s), clamp_e4m3(y[2] / s), clamp_e4m3(y[3] / s));
     }
-  if ((lane & 1) == 0) *xs = s;
+    *(u32x4*)(dst + q * 256) = u32x4{o[0], o[1], o[2], o[3]};
+  }
+  if ((lane & 3) == 0) *xs = s;
 }
 
 // Work-group barrier once this wave's copies of the next chunk have landed in
@@ -149,19 +147,19 @@ __device__ __forceinline__ void copy_1k_asm(u32x4 r, const uint8_t* to, int lane
 template <int MB, int NBW>
 __device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* sx, float sw, const bf16x8 (&A)[NBW][2],
                                                 floatx4 (&acc)[NBW][MB]) {
-  bf16x8 b0 = *(const bf16x8*)xb, b1 = *(const bf16x8*)(xb + 1024);
+  u32x4 raw = *(const u32x4*)xb;
   float s = sx[0], sp = 0.0f;
   floatx4 z[NBW], zp[NBW];
 #pragma unroll
   for (int mb = 0; mb <= MB; ++mb) {
-    bf16x8 n0 = b0, n1 = b1;
+    u32x4 rn = raw;
     float sn = s;
     if (mb + 1 < MB) {
-      n0 = *(const bf16x8*)(xb + (mb + 1) * 2048);
-      n1 = *(const bf16x8*)(xb + (mb + 1) * 2048 + 1024);
+      rn = *(const u32x4*)(xb + (mb + 1) * 2048);
       sn = sx[(mb + 1) * 16];
     }
     if (mb < MB) {
+      const bf16x8 b0 = widen8(raw[0], raw[1]), b1 = widen8(raw[2], raw[3]);
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb)
         z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
@@ -176,8 +174,7 @@ __device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* 
         for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    b0 = n0;
-    b1 = n1;
+    raw = rn;
     sp = s;
     s = sn;
 #pragma unroll
@@ -225,29 +222,26 @@ __device__ __forceinline__ void store_logits(const LmHeadFp8Args& a, const float
   }
 }
 
-// A work-group has MW x VW waves: wave (wm, wv) takes MB 16-row blocks of hidden rows from wm * MB and NBW
-// 16-row blocks of the vocabulary. NST chunks of hidden rows in LDS, R chunks of the matrix in registers.
-template <int MB, int NBW, int MW, int VW, int NST, int R, int WPE>
-__global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void lm_head_fp8_kernel(
-    LmHeadFp8Args a) {
-  static_assert((NST == 2 || NST == 4) && NST % R == 0 && 8 % NBW == 0, "ring sizes, one scale block a wave");
-  constexpr int NW = MW * VW;
-  constexpr int kUnit = fp8_unit_bytes(MB * MW);    // 64 columns of the hidden rows, and their scales
-  constexpr int kStage = 2 * kUnit;
+// Up to 64 hidden rows (MB 16-row blocks): four waves, each with all the rows and NBW 16-row blocks of the
+// vocabulary. Bound by the matrix, which each wave reads on its own: four chunks of it are in flight in registers,
+// four of the hidden rows in LDS.
+template <int MB, int NBW>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_kernel(LmHeadFp8Args a) {
+  static_assert(8 % NBW == 0, "one scale block a wave");
+  constexpr int NW = 4, NST = 4;
+  constexpr int kStage = fp8_stage_bytes(MB);       // a chunk's hidden rows and their scales
   constexpr int kCopy = kStage / 1024;              // 1 KB copies of it, dealt to the waves in turn
   constexpr int kQ = (kCopy + NW - 1) / NW;
   constexpr int kLoads = 2 * NBW + 1;               // a wave's loads of a chunk of the matrix
   // newer operations than the copies of the next chunk: its loads, and all of the chunks after it
   constexpr int kNewer = kLoads + (NST - 2) * (kQ + kLoads);
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kStage], s_x1[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t s_x2[NST > 2 ? kStage : 16], s_x3[NST > 2 ? kStage : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kStage], s_x1[kStage], s_x2[kStage], s_x3[kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = w / VW, wv = w % VW;
   const int lr = lane & 15;
   const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
-  const int mb0 = (blockIdx.y * MW + wm) * MB;
-  const int vb0 = a.vb_first + (blockIdx.x * VW + wv) * NBW;  // first 16-row block of this wave
+  const int mb0 = blockIdx.y * MB;
+  const int vb0 = (blockIdx.x * NW + w) * NBW;  // first 16-row block of this wave
   const int coff = (int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB);
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
 
@@ -264,8 +258,8 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(WP
       copy_1k(xrs, buf + p * 1024, lane * 16, chunk_of(c) * kStage + p * 1024);
     }
   };
-  u32x4 raw[R][2][NBW];  // codes of 64 columns each
-  float ws[R];
+  u32x4 raw[NST][2][NBW];  // codes of 64 columns each
+  float ws[NST];
   auto load = [&](int slot, int p, int c) {
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
@@ -277,44 +271,37 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(WP
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // chunk c: hidden rows in LDS stage c % NST, matrix in register slot c % R. At its start the copies of chunk
-  // c + NST - 1 go out; each half's registers are loaded with chunk c + R once they are widened.
+  // chunk c: hidden rows in LDS stage c % 4, matrix in register slot c % 4. At its start the copies of chunk c + 3
+  // go out; each half's registers are loaded with chunk c + 4 once they are widened.
   auto stage_of = [&](int i) { return i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3; };
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) {
-    copy(stage_of(i), min(i, HB - 1));
-    if (i < R) {
-      load(i, 0, min(i, HB - 1));
-      load(i, 1, min(i, HB - 1));
-      ws[i] = wsp[chunk_of(min(i, HB - 1))];
-    }
+  for (int i = 0; i < NST; ++i) {
+    if (i < NST - 1) copy(stage_of(i), min(i, HB - 1));
+    load(i, 0, min(i, HB - 1));
+    load(i, 1, min(i, HB - 1));
+    ws[i] = wsp[chunk_of(min(i, HB - 1))];
     __builtin_amdgcn_sched_barrier(0);
   }
-  if constexpr (R == NST) {
-    load(R - 1, 0, min(R - 1, HB - 1));
-    load(R - 1, 1, min(R - 1, HB - 1));
-    ws[R - 1] = wsp[chunk_of(min(R - 1, HB - 1))];
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  chunk_barrier<kLoads>();
-  auto chunk = [&](int c, int st, int slot) {
-    const uint8_t* cur = stage_of(st) + wm * MB * 2048;
-    const float* sx = (const float*)(stage_of(st) + MB * MW * 2048) + wm * MB * 16 + lr;
+  // chunk 0 has landed: newer are its loads, two more chunks' copies and loads, and the last loads
+  chunk_barrier<kNewer + kLoads>();
+  auto chunk = [&](int c, int st) {
+    const uint8_t* cur = stage_of(st);
+    const float* sx = (const float*)(cur + MB * 2048) + lr;
     copy(stage_of((st + NST - 1) % NST), min(c + NST - 1, HB - 1));  // the last chunk again at the end, never used
-    const float sw = ws[slot];
+    const float sw = ws[st];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       bf16x8 A[NBW][2];
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
-        const u32x4 x = raw[slot][p][nb];
+        const u32x4 x = raw[st][p][nb];
         A[nb][0] = widen8(x[0], x[1]);
         A[nb][1] = widen8(x[2], x[3]);
       }
-      load(slot, p, min(c + R, HB - 1));
-      if (p == 1) ws[slot] = wsp[chunk_of(min(c + R, HB - 1))];
+      load(st, p, min(c + NST, HB - 1));
+      if (p == 1) ws[st] = wsp[chunk_of(min(c + NST, HB - 1))];
       __builtin_amdgcn_sched_barrier(0);
-      scaled_products<MB, NBW>(cur + p * kUnit + lane * 16, sx, sw, A, acc);
+      scaled_products<MB, NBW>(cur + p * 1024 + lane * 16, sx, sw, A, acc);
     }
     chunk_barrier<kNewer>();  // chunk c + 1's copies have landed
   };
@@ -322,55 +309,61 @@ __global__ __launch_bounds__(64 * MW * VW) __attribute__((amdgpu_waves_per_eu(WP
 #pragma nounroll
   for (; c + NST <= HB; c += NST)
 #pragma unroll
-    for (int i = 0; i < NST; ++i) chunk(c + i, i, i % R);
+    for (int i = 0; i < NST; ++i) chunk(c + i, i);
 #pragma unroll
   for (int i = 0; i + 1 < NST; ++i)
-    if (c + i < HB) chunk(c + i, i, i % R);
+    if (c + i < HB) chunk(c + i, i);
   store_logits<MB, NBW>(a, acc, mb0, vb0);
 }
 
-// Up to 224 hidden rows a tile: eight waves, wave (wm, wv) takes 7 row blocks from 7 wm and 4 vocabulary blocks
-// from 4 wv. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS; the matrix's chunk (32 KB,
-// each run read by two waves) one deep, widened into registers at the chunk's start, after which the next one
-// is copied over it. The vector unit would be the bound, so a chunk's sums are scaled once, not once a half.
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_wide_kernel(LmHeadFp8Args a) {
+// 112 hidden rows by 512 vocabulary rows: eight waves, each with all 7 row blocks and 4 vocabulary blocks of its
+// own. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS, shared; the wave's part of the
+// matrix (8 KB a chunk) one deep in a part of LDS of its own, widened into registers at the chunk's start, after
+// which the next chunk is copied over it. One barrier a chunk. A chunk's sums are scaled once, since the vector
+// unit would be the bound otherwise. The two row tiles of 224 rows run on the same XCD next to each other, so that
+// the second one finds the matrix in the caches.
+template <int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_wide_kernel(
+    LmHeadFp8Args a, int v_tiles, int m_tiles) {
   constexpr int MB = 7, NBW = 4;
-  constexpr int kUnit = fp8_unit_bytes(2 * MB);
-  constexpr int kCopy = 2 * kUnit / 1024;
-  constexpr int kQ = (kCopy + 7) / 8;
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[2][2 * kUnit];
-  __shared__ __attribute__((aligned(16))) uint8_t s_w[16 * 2048];
-  __shared__ float s_ws[2][512];  // the two scale blocks' scales, by chunk (H <= 65536)
+  constexpr int kStage = fp8_stage_bytes(MB);
+  constexpr int kCopy = kStage / 1024;
+  constexpr int kQ = (kCopy + NW - 1) / NW;
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[2][kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[NW][4 * 2048];
+  __shared__ float s_ws[NW / 2][512];  // the scale blocks' scales, by chunk (H <= 65536)
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = w >> 2, wv = w & 3;
   const int lr = lane & 15;
   const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
-  const int vt0 = a.vb_first + blockIdx.x * 16;
-  const int coff = __builtin_amdgcn_readfirstlane((int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB));
+  // work-groups go to the eight XCDs in turn: row tile after row tile of eight vocabulary tiles
+  const int grp = blockIdx.x / (8u * (unsigned)m_tiles), in = blockIdx.x - grp * 8 * m_tiles;
+  const int vt = grp * 8 + (in & 7), mt = in >> 3;
+  if (vt >= v_tiles) return;
+  const int vt0 = vt * NW * NBW;
+  const int coff = __builtin_amdgcn_readfirstlane((int)(((unsigned)vt * (unsigned)kStagger) % (unsigned)HB));
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
-  for (int i = tid; i < 2 * HB; i += 512) {
-    const int b = i >= HB ? 1 : 0;
+  for (int i = tid; i < NW / 2 * HB; i += 64 * NW) {
+    const int b = i / HB;
     s_ws[b][i - b * HB] = a.w_scale[(size_t)min((vt0 >> 3) + b, (a.V - 1) >> 7) * HB + i - b * HB];
   }
-  const u32x4 xrs = words_at(a.xq + (size_t)blockIdx.y * HB * 2 * kUnit, HB * 2 * kUnit);
-  // the tile's rows of the matrix: 16 blocks of HB * 2 KB (those past the last repeat it)
-  const int nblk = __builtin_amdgcn_readfirstlane(min(16, VB - vt0));
-  const u32x4 wrs = words_at(a.w + (size_t)vt0 * HB * 2048, nblk * HB * 2048);
+  const u32x4 xrs = words_at(a.xq + (size_t)mt * HB * kStage, HB * kStage);
+  // the wave's rows of the matrix: 4 blocks of HB * 2 KB (those past the last repeat it)
+  const int vb0 = vt0 + w * NBW, vbc = min(vb0, VB - 1);
+  const int nblk = __builtin_amdgcn_readfirstlane(min(NBW, VB - vbc));
+  const u32x4 wrs = words_at(a.w + (size_t)vbc * HB * 2048, nblk * HB * 2048);
   auto copy_x = [&](uint8_t* buf, int c) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-      const int p = min(q * 8 + w, kCopy - 1);
-      copy_1k_asm<false>(xrs, buf + p * 1024, lane * 16, chunk_of(c) * 2 * kUnit + p * 1024);
+      const int p = min(q * NW + w, kCopy - 1);
+      copy_1k_asm<false>(xrs, buf + p * 1024, lane * 16, chunk_of(c) * kStage + p * 1024);
     }
   };
   auto copy_w = [&](int c) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int p = q * 8 + w;  // 1 KB run p of the chunk: half p % 2 of block p / 2
-      copy_1k_asm<true>(wrs, s_w + p * 1024, lane * 16,
+    for (int p = 0; p < 2 * NBW; ++p)  // 1 KB run p of the wave's chunk: half p % 2 of block p / 2
+      copy_1k_asm<true>(wrs, s_w[w] + p * 1024, lane * 16,
                         min(p >> 1, nblk - 1) * HB * 2048 + chunk_of(c) * 2048 + (p & 1) * 1024);
-    }
   };
   floatx4 acc[NBW][MB];
 #pragma unroll
@@ -383,29 +376,28 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma nounroll
   for (int c = 0; c < HB; ++c) {
     const uint8_t* cur = s_x[c & 1];
-    if (c + 1 < HB) copy_x(s_x[(c + 1) & 1], c + 1);
     bf16x8 A[NBW][4];
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const u32x4 x = *(const u32x4*)(s_w + (wv * NBW + nb) * 2048 + p * 1024 + lane * 16);
+        const u32x4 x = *(const u32x4*)(s_w[w] + nb * 2048 + p * 1024 + lane * 16);
         A[nb][2 * p] = widen8(x[0], x[1]);
         A[nb][2 * p + 1] = widen8(x[2], x[3]);
       }
-    const float sw = s_ws[wv >> 1][chunk_of(c)];
-    // every wave has read the matrix's chunk: the next one may land on it
+    const float sw = s_ws[w >> 1][chunk_of(c)];
+    // the wave has read its part of the matrix: its next chunk may land on it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    if (c + 1 < HB) copy_w(c + 1);
-    const uint8_t* xb = cur + wm * MB * 2048 + lane * 16;
-    const float* sx = (const float*)(cur + 2 * MB * 2048) + wm * MB * 16 + lr;
-    auto operand = [&](int mb, int e) { return *(const bf16x8*)(xb + (e >> 1) * kUnit + mb * 2048 + (e & 1) * 1024); };
+    if (c + 1 < HB) {
+      copy_w(c + 1);
+      copy_x(s_x[(c + 1) & 1], c + 1);
+    }
+    const uint8_t* xb = cur + lane * 16;
+    const float* sx = (const float*)(cur + MB * 2048) + lr;
+    auto operand = [&](int mb, int p) { return *(const u32x4*)(xb + mb * 2048 + p * 1024); };
     // one row block after the other, operand reads one block ahead, scaling one block behind (the order is
     // pinned: left alone the compiler holds every block's sums at once)
-    bf16x8 b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = operand(0, e);
+    u32x4 b[2] = {operand(0, 0), operand(0, 1)};
     float s = sx[0], sp = 0.0f;
     floatx4 z[NBW], zp[NBW];
 #pragma unroll
@@ -414,11 +406,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if (mb < MB) {
         if (mb + 1 < MB) sn = sx[(mb + 1) * 16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int p = 0; p < 2; ++p) {
+          const bf16x8 b0 = widen8(b[p][0], b[p][1]), b1 = widen8(b[p][2], b[p][3]);
+          if (mb + 1 < MB) b[p] = operand(mb + 1, p);
 #pragma unroll
           for (int nb = 0; nb < NBW; ++nb)
-            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][e], b[e], e ? z[nb] : floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-          if (mb + 1 < MB) b[e] = operand(mb + 1, e);
+            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][2 * p], b0, p ? z[nb] : floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+            z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][2 * p + 1], b1, z[nb], 0, 0, 0);
         }
       }
       if (mb > 0) {
@@ -427,6 +423,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
+      }
+      // the block's order: operand reads, then every product followed by two of the vector unit's instructions
+      // (without it: 142 us against 118 us for V = 65536, 224 rows)
+      if (mb < MB) {
+        if (mb + 1 < MB) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
       sp = s;
@@ -441,7 +448,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       for (int mb = 0; mb < MB; ++mb) asm volatile("" : "+v"(acc[nb][mb]));
     chunk_barrier<0>();  // chunk c + 1 has landed
   }
-  store_logits<MB, NBW>(a, acc, (blockIdx.y * 2 + wm) * MB, vt0 + wv * NBW);
+  store_logits<MB, NBW>(a, acc, mt * MB, vb0);
 }
 
 // Row-major codes [V][H] into the tiles, 16 bytes a thread; rows past V are zero.
@@ -506,29 +513,24 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(int V, int H, const u
   }
 }
 
-template <int MB, int NBW, int MW, int VW, int NST, int R, int WPE>
+template <int MB, int NBW>
 hipError_t launch_mb(const LmHeadFp8Args& a, hipStream_t st) {
-  const int VB = ((a.V + 15) >> 4) - a.vb_first, MBt = (a.M + 15) >> 4;
-  const dim3 grid((unsigned)((VB + VW * NBW - 1) / (VW * NBW)), (unsigned)((MBt + MB * MW - 1) / (MB * MW)));
-  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW, MW, VW, NST, R, WPE>), grid, dim3(64 * MW * VW), 0, st, a);
+  const int VB = (a.V + 15) >> 4, MBt = (a.M + 15) >> 4;
+  const dim3 grid((unsigned)((VB + 4 * NBW - 1) / (4 * NBW)), (unsigned)((MBt + MB - 1) / MB));
+  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-// The wide kernel's work-groups fill the device in rounds of one a CU. A last round of few of them would take
-// as long as a full one (90 us at H = 4096): its vocabulary goes to work-groups of 16 vocabulary rows instead
-// (seven waves, two row blocks each; 55 us for the 256 that one round of them holds, 105 us for 640).
-constexpr int kCus = 256, kTailTiles = 16;
-hipError_t launch_wide(LmHeadFp8Args a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + 13) / 14;
-  int tiles = (VB + 15) / 16;
-  const int rest = tiles % kCus;
-  const bool tail = mt == 1 && tiles > kCus && rest > 0 && rest <= kTailTiles;
-  if (tail) tiles -= rest;
-  hipLaunchKernelGGL(lm_head_fp8_wide_kernel, dim3((unsigned)tiles, (unsigned)mt), dim3(512), 0, st, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !tail) return e;
-  a.vb_first = tiles * 16;
-  return launch_mb<2, 1, 7, 1, 2, 2, 2>(a, st);
+// 256 vocabulary rows a work-group, two work-groups a CU: against one of 512 (eight waves) 77 us to 104 us at
+// V = 32000 and 284 us to 317 us at V = 151936, whose last round would be short of work-groups, and as fast where
+// the rounds come out even (H = 4096, 224 rows).
+constexpr int kWideWaves = 4;
+hipError_t launch_wide(const LmHeadFp8Args& a, hipStream_t st) {
+  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + 6) / 7;
+  const int tiles = (VB + kWideWaves * 4 - 1) / (kWideWaves * 4);
+  hipLaunchKernelGGL(lm_head_fp8_wide_kernel<kWideWaves>, dim3((unsigned)((tiles + 7) / 8 * 8 * mt)),
+                     dim3(64 * kWideWaves), 0, st, a, tiles, mt);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -539,17 +541,16 @@ hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (a.mb) {
-    case 1: return launch_mb<1, 1, 1, 4, 4, 4, 2>(a, st);
-    case 2: return launch_mb<2, 1, 1, 4, 4, 4, 2>(a, st);
-    case 4: return launch_mb<4, 2, 1, 4, 4, 4, 2>(a, st);
-    case 7: return launch_mb<7, 4, 1, 4, 2, 1, 2>(a, st);
+    case 1: return launch_mb<1, 1>(a, st);
+    case 2: return launch_mb<2, 1>(a, st);
+    case 4: return launch_mb<4, 2>(a, st);
     default: return launch_wide(a, st);
   }
 }
 
 int lm_head_fp8_blocks(int M) {
   const int n = (M + 15) >> 4;
-  return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 7 ? 7 : 14;
+  return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 7;
 }
 
 hipError_t launch_tile_fp8(int V, int H, const uint8_t* codes, uint8_t* tiled, hipStream_t st) {

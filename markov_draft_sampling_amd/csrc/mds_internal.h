@@ -364,15 +364,14 @@ struct LmHeadFp8Args {
   const uint8_t* w;              // tiled e4m3 [ceil(V / 16)][16 H]
   const float* w_scale;          // [ceil(V / 128)][H / 128]
   int mb;                        // 16-row blocks of a row tile (lm_head_fp8_blocks)
-  uint8_t* xq;                   // workspace: [row tiles][H / 64] units of fp8_unit_bytes(mb): mb blocks of 2 KB (16
-                                 // rows by 64 columns of codes, widened to bf16), then the 16 mb row scales
-  int vb_first;                  // first 16-row block of the vocabulary of a launch
+  uint8_t* xq;                   // workspace: [row tiles][H / 128] stages of fp8_stage_bytes(mb): mb tiles of 2 KB (16
+                                 // rows by 128 columns of codes, in the matrix's tile order), then the 16 mb row scales
   void* out;
   long long out_rs, out_ss;
   int out_bf16, vec_out, cus;
 };
-// bytes of a row tile's quantised 64 columns: codes, scales, up to whole KB (the copies' size)
-__host__ __device__ constexpr int fp8_unit_bytes(int mb) { return (mb * 2112 + 1023) / 1024 * 1024; }
+// bytes of a row tile's quantised chunk of 128 columns: codes, scales, up to whole KB (the copies' size)
+__host__ __device__ constexpr int fp8_stage_bytes(int mb) { return (mb * 2112 + 1023) / 1024 * 1024; }
 int lm_head_fp8_blocks(int M);
 hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st);
 hipError_t launch_tile_fp8(int V, int H, const uint8_t* codes, uint8_t* tiled, hipStream_t st);
