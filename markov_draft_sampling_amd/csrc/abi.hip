@@ -6,6 +6,7 @@
 
 #include "../../include/mds.h"
 #include "mds_internal.h"
+#include "mds_serve.h"
 
 namespace {
 

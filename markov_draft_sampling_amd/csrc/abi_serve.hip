@@ -2,7 +2,7 @@
 // paged attention, the 8-bit LM head): argument checks on the host, then the
 // kernels on the caller's stream. See include/mds.h for the contract.
 #include "../../include/mds.h"
-#include "mds_internal.h"
+#include "mds_serve.h"
 
 namespace {
 

@@ -16,7 +16,7 @@
 // (two reads and one write for an 8-bit cache): bound by HBM for long
 // prompts, by the launch for a decoding step.
 #include "mds_device.h"
-#include "mds_internal.h"
+#include "mds_serve.h"
 
 namespace mds {
 namespace {

@@ -24,7 +24,7 @@
 // operand reads from LDS (382 us, 960 TFLOP/s), which is why a wave takes 64
 // vocabulary rows: every hidden operand serves four products.
 #include "mds_device.h"
-#include "mds_internal.h"
+#include "mds_serve.h"
 
 namespace mds {
 namespace {

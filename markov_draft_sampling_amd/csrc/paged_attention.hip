@@ -30,17 +30,15 @@
 // 8-bit caches are widened to bf16 (exactly) after the LDS read; the key scale
 // joins the softmax scale, the value scale the final division.
 #include "mds_device.h"
-#include "mds_internal.h"
+#include "mds_serve.h"
 
 namespace mds {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #define MDS_LDS __attribute__((address_space(3)))
-#define MDS_GLOBAL __attribute__((address_space(1)))
 
 constexpr float kLn2 = 0x1.62e430p-1f;
 constexpr float kRescale = 8.0f;  // a maximum's growth (base 2) up to which the running one stays
