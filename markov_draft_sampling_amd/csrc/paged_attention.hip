@@ -100,19 +100,23 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, uint
     t.r0 = (tile - t.b * a.per_req) * ROWS;
     if (a.by_length) t.b = nth_longest(a, t.b);
   } else {
-    // request b's tiles start at floor(q0 G / ROWS) + b: enough for its rows,
-    // since ceil(x) of its rows is at most the step to the next request's start
+    // Request b's tiles start at floor(q0 G / ROWS) + b: enough for its rows, since ceil(x) of its rows is at most
+    // the step to the next request's start. The last request that starts at or before the tile, 64 probes a round.
     const int lane = threadIdx.x & 63;
-    int cnt = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-      const int b = b0 + lane;
+    int step = 1;
+    while (step * 64 < a.B) step *= 64;
+    t.b = 0;
+    for (; step > 0; step >>= 6) {
+      const int b = t.b + lane * step;
       uint32_t dummy = 0;
       const int q = clamp_tok(a, a.query_start[min(b, a.B - 1)], dummy);
-      const bool before = b < a.B && (int)((unsigned)q * (unsigned)a.G / ROWS) + b <= tile;
-      cnt += __popcll(__ballot(before));
+      const int k = __popcll(__ballot(b < a.B && (int)((unsigned)q * (unsigned)a.G / ROWS) + b <= tile));
+      if (k == 0) {  // no request starts that early, or query_start falls somewhere
+        t.b = 0;
+        break;
+      }
+      t.b += (k - 1) * step;
     }
-    if (cnt == 0) return t;
-    t.b = cnt - 1;
   }
   t.b = __builtin_amdgcn_readfirstlane(t.b);
   const int qa = __builtin_amdgcn_readfirstlane(a.query_start[t.b]);
@@ -127,8 +131,9 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, uint
   } else {
     t.r0 = (tile - ((int)((unsigned)t.q0 * (unsigned)a.G / ROWS) + t.b)) * ROWS;
   }
+  if (t.r0 < 0) bad |= kStatusBadIndex;  // query_start falls somewhere
   t.rows = min(ROWS, t.n * a.G - t.r0);
-  if (t.n <= 0 || t.rows <= 0) {
+  if (t.n <= 0 || t.rows <= 0 || t.r0 < 0) {
     t.rows = 0;
     return t;
   }

@@ -159,6 +159,43 @@ def test_many_requests_and_empty_ones():
     _case(ctx, chunk, 2, 1, 64, 16, seed=7)
 
 
+@pytest.mark.parametrize("B", [65, 300, 4500])
+def test_prompts_among_many_requests(B):
+    # tiles found by row offset in one, two and three rounds of 64 probes
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(0, 20, B).tolist()
+    chunk = rng.choice([0, 1, 1, 3], B).tolist()
+    for b, n in ((0, 40), (B // 2, 130), (B - 1, 33)):
+        chunk[b] = n
+    _case(ctx, chunk, 2, 1, 64, 16, seed=B)
+
+
+def test_decreasing_starts_among_row_tiles_stay_in_bounds():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    T, D = 400, 64
+    g = torch.Generator().manual_seed(0)
+    q = torch.randn(T, 4, D, generator=g).to(torch.bfloat16).cuda()
+    kp = torch.randn(8, 16, 1, D, generator=g).to(torch.bfloat16).cuda()
+    table = t([[0, 1], [2, 3], [4, 5], [6, 7]])
+    run = lambda starts: _run_mixed(mds, q, kp, table, t(starts))  # noqa: E731
+    st, out = run([0, 300, 350, 350, 400])
+    assert st == 0
+    st2, out2 = run([0, 300, 20, 350, 400])  # requests 1 and 2 are out of order
+    assert st2 & 8
+    assert torch.equal(out2[350:], out[350:]) and torch.isfinite(out2).all()
+
+
+def _run_mixed(mds, q, kp, table, starts):
+    import torch
+    out = torch.zeros_like(q)
+    seq = torch.tensor([30, 31, 20, 32], dtype=torch.int32, device="cuda")
+    ws = mds.paged_attention(q, kp, kp, table, starts, seq, out, 300, 32, causal=False)
+    torch.cuda.synchronize()
+    return mds.workspace_status(ws), out
+
+
 @pytest.mark.parametrize("B,Hk", [(40, 8), (100, 4), (128, 3)])
 def test_longest_first_order(B, Hk):
     # more work-groups than the CUs hold: requests are taken by falling length (ties, empty ones and all)
