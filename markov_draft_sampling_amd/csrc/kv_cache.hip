@@ -87,11 +87,12 @@ __global__ __launch_bounds__(kPlanThreads) void page_plan_kernel(PageTableArgs a
   if (tid == 0) s_taken = 0;
   // the first tile's inputs and the free list's length, asked for together: the rest of the plan is a chain of
   // loads that wait for each other
-  int slot_in = -1, n_first = 0, adv_first = 0;
+  int slot_in = -1, n_first = 0;
+  long long adv_first = 0;
   if (tid < a.B) {
     slot_in = a.idx_map ? a.idx_map[tid] : tid;
     n_first = a.chunk_len[tid];
-    adv_first = a.advance ? a.advance[tid] + a.advance_add : 0;
+    adv_first = a.advance ? (long long)a.advance[tid] + a.advance_add : 0;
   }
   long long count = a.free_count[0];
 
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(kPlanThreads) void page_plan_kernel(PageTableArgs a
     long long ctx = 0;
     int held = 0;
     if (here) {
-      ctx = (long long)a.kv_len[s] + (b0 == 0 ? adv_first : a.advance ? a.advance[b] + a.advance_add : 0);
+      ctx = a.kv_len[s] + (b0 == 0 ? adv_first : a.advance ? (long long)a.advance[b] + a.advance_add : 0);
       held = a.pages_held[s];
       if (ctx < 0 || ctx > 0x7FFFFFFF) {
         bad |= kStatusBadIndex;

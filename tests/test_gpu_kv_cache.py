@@ -138,6 +138,31 @@ def test_counts_out_of_range_are_clamped():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("B", [3, 300])
+def test_advances_at_the_ends_of_their_range(B):
+    ref, dev = _pair(B, 4, 16, 4 * B, 64)
+    top = 2 ** 31 - 1
+    d = dev.step(16, [1] * B, advance=[top, 0, -top - 1] + ([-1] * (B - 4) + [top] if B > 3 else []), advance_add=1)
+    assert d["status"] == 8 | 32  # clamped, and no room for the first (and the last)
+    assert dev.kv_len.tolist()[:3] == [top, 1, 0] and d["seq_lens"][:3] == [0, 2, 1]
+    if B > 3:
+        assert dev.kv_len.tolist()[-1] == top and d["seq_lens"][-1] == 0
+
+
+@pytest.mark.parametrize("B", [200, 3000])
+def test_the_most_state_slots(B):
+    n_slots = 1 << 17
+    ref, dev = _pair(n_slots, 2, 16, 4096, 3 * B)
+    idx = np.random.default_rng(B).permutation(n_slots)[:B].tolist()
+    idx[0], idx[7], idx[9], idx[11] = n_slots - 1, n_slots, idx[B - 1], -1
+    chunk = [3 if b % 5 else 1 for b in range(B)]
+    for _ in range(2):
+        r = ref.step(chunk, idx_map=idx, max_tokens=3 * B)
+        d = dev.step(16, chunk, idx_map=idx)
+        _same(ref, dev, r, d)
+        chunk = [-1 if b % 3 == 0 else c for b, c in enumerate(chunk)]
+
+
 def test_tables_on_a_side_stream_and_in_a_graph():
     import torch
     import markov_draft_sampling_amd as mds
