@@ -38,13 +38,17 @@ def _call(what, fn, index, stream, args):
         _check(rc, what)
 
 
-def _new_workspace(nbytes, index, stream):
-    """A zeroed workspace made on the stream that the call runs on."""
-    nbytes = max(nbytes, 256)
+def _on(stream, make, *args, **kw):
+    """make(*args, **kw) on the stream that a call runs on: memory that its results take over from a freed tensor may
+    still be in use on another stream."""
     if stream is None:
-        return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+        return make(*args, **kw)
     with torch.cuda.stream(stream):
-        return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+        return make(*args, **kw)
+
+
+def _new_workspace(nbytes, index, stream):
+    return _on(stream, torch.zeros, max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{index}")
 
 
 def _check_workspace(ws, index):
@@ -197,11 +201,11 @@ def lm_head_fp8_tiled_bytes(V, H) -> int:
     return out.value
 
 
-def _tiled_out(out, V, H, dev):  # dev: the device's index
+def _tiled_out(out, V, H, dev, stream):  # dev: the device's index
     shape = ((V + 15) // 16, 16 * H)
     n = lm_head_fp8_tiled_bytes(V, H)
     if out is None:
-        out = torch.empty(shape, dtype=_E4M3, device=f"cuda:{dev}")
+        out = _on(stream, torch.empty, shape, dtype=_E4M3, device=f"cuda:{dev}")
     _need(out.dtype is _E4M3 and out.shape == shape and out.is_contiguous() and out.get_device() == dev,
           "the tiled matrix must be contiguous float8_e4m3fn [ceil(V/16), 16 H]")
     return out, n
@@ -214,7 +218,7 @@ def tile_lm_head_fp8(codes, out=None, stream=None):
           "codes must be a contiguous float8_e4m3fn [V, H] GPU tensor")
     V, H = codes.shape
     dev = _index(codes)
-    out, n = _tiled_out(out, V, H, dev)
+    out, n = _tiled_out(out, V, H, dev, stream)
     _call("tile_lm_head_fp8", _lib().mds_tile_lm_head_fp8, dev, stream, (V, H, codes.data_ptr(), out.data_ptr(), n))
     return out
 
@@ -226,10 +230,10 @@ def quantize_lm_head_fp8(lm_head, out=None, scales=None, stream=None):
           "lm_head must be a contiguous bf16 [V, H] GPU tensor")
     V, H = lm_head.shape
     dev = _index(lm_head)
-    out, n = _tiled_out(out, V, H, dev)
+    out, n = _tiled_out(out, V, H, dev, stream)
     blocks = ((V + 127) // 128, H // 128)
     if scales is None:
-        scales = torch.empty(blocks, dtype=_F32, device=f"cuda:{dev}")
+        scales = _on(stream, torch.empty, blocks, dtype=_F32, device=f"cuda:{dev}")
     _call("quantize_lm_head_fp8", _lib().mds_quantize_lm_head_fp8, dev, stream,
           (V, H, lm_head.data_ptr(), out.data_ptr(), n, _vec(scales, _F32, blocks[0] * blocks[1], dev, "scales")))
     return out, scales
@@ -270,7 +274,7 @@ def lm_head_fp8(hidden, lm_head, scales, out, K, workspace=None, stream=None):
     else:
         _check_workspace(workspace, dev)
     _call("lm_head_fp8", _lib().mds_lm_head_fp8, dev, stream,
-          (B, K, V, H, hidden.data_ptr(), hidden.stride(0), lm_head.data_ptr(),
+          (B, K, V, H, hidden.data_ptr(), hidden.stride(0) if rows > 1 else H, lm_head.data_ptr(),
            _vec(scales, _F32, ((V + 127) // 128) * (H // 128), dev, "scales"), out.data_ptr(), code, out.stride(0),
            out.stride(1), workspace.data_ptr(), workspace.numel()))
     return workspace

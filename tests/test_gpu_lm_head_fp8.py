@@ -152,6 +152,42 @@ def test_lm_head_fp8_graph_replays():
         assert torch.equal(out, want)
 
 
+def test_side_stream_makes_its_outputs_there():
+    import torch
+    import markov_draft_sampling_amd as mds
+    V, H = 3000, 512
+    w, _, tiled, sd = _weights(V, H, 8, "quantize")
+    wd = torch.randn(V, H, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    want, want_s = mds.quantize_lm_head_fp8(wd)
+    codes = torch.randint(0, 120, (V, H), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    want_t = mds.tile_lm_head_fp8(codes)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    # memory that the current stream still writes, freed for whoever asks on that stream
+    busy = torch.zeros(V * H, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        busy.add_(1)
+    del busy
+    got, got_s = mds.quantize_lm_head_fp8(wd, stream=side)
+    got_t = mds.tile_lm_head_fp8(codes, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    u8 = lambda x: x.view(torch.uint8)  # noqa: E731
+    assert torch.equal(u8(got), u8(want)) and torch.equal(got_s, want_s) and torch.equal(u8(got_t), u8(want_t))
+
+
+def test_one_row_of_any_stride():
+    import torch
+    import markov_draft_sampling_amd as mds
+    V, H = 1000, 256
+    _, _, tiled, sd = _weights(V, H, 3, "quantize")
+    x = torch.randn(1, H, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    out, out2 = torch.empty(1, 1, V, device="cuda"), torch.empty(1, 1, V, device="cuda")
+    mds.lm_head_fp8(x, tiled, sd, out, 1)
+    mds.lm_head_fp8(x.as_strided((1, H), (0, 1)), tiled, sd, out2.as_strided((1, 1, V), (3, 1, 1)), 1)
+    assert torch.equal(out, out2)
+
+
 def test_refuses_mismatched_tensors():
     import torch
     import markov_draft_sampling_amd as mds
