@@ -420,6 +420,28 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
     return up ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true))
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
   };
+  // Wave priorities, where two work-groups share a CU and so each SIMD holds two waves that need the matrix cores and
+  // the vector unit in turn: softmax and values go ahead of the other wave's scores, which would otherwise be cut into
+  // (2048 prompt tokens: 491 us against 530 us). Where the key groups of a work-group wait for each other only
+  // at its end, every second batch of work-groups also goes ahead as a whole, so that the two do not
+  // keep in step (128 requests over an 8-bit cache: 135 us, with the first rule alone 141 us, without either 146 us).
+  const bool ahead = KG > 1 && (blockIdx.x & 256) != 0;
+  auto low = [&]() {
+    if constexpr (RG > 1) {
+      if (ahead)
+        __builtin_amdgcn_s_setprio(1);
+      else
+        __builtin_amdgcn_s_setprio(0);
+    }
+  };
+  auto high = [&]() {
+    if constexpr (RG > 1) {
+      if (ahead)
+        __builtin_amdgcn_s_setprio(2);
+      else
+        __builtin_amdgcn_s_setprio(1);
+    }
+  };
   constexpr int NK = KB / 16;
   auto block = [&](int st, int i) {
     const int k0 = c0 + (kg + KG * i) * KB;
@@ -450,6 +472,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
         for (int nb = 0; nb < NB; ++nb)
           S[kb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[s], Q[nb][s], S[kb][nb], 0, 0, 0);
     }
+    high();
     // lane: row lr of each nb, keys k0 + 16 kb + 4 lg + i
     const bool masked = k0 < all_lo || k0 + KB > all_hi;
     if (masked) {
@@ -532,8 +555,10 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
         for (int nb = 0; nb < NB; ++nb)
           O[nb][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V[db], P[nb], O[nb][db], 0, 0, 0);
     }
+    low();
   };
 
+  low();
   if (nmy > 0) load_pages(0);
   if constexpr (RG == 1) {
     // a key group is one wave: its ring is its own, no barrier
