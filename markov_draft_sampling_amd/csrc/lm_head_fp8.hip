@@ -52,51 +52,33 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, u32x4{widen(lo, false), widen(lo, true), widen(hi, false), widen(hi, true)});
 }
 
-// Hidden rows: a wave per 16 rows and 128 columns, a lane 32 columns of a row.
+// Hidden rows: a wave per 4 rows and 128 columns, a lane 8 columns of a row (the call waits for it: short rows of
+// divisions a lane, 4.7 us with 32 columns).
 __global__ __launch_bounds__(256) void quant_rows_kernel(LmHeadFp8Args a) {
   const int HB = a.H >> 7, MBt = (a.M + 15) >> 4;
-  const int wv = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (wv >= HB * MBt) return;
-  const int lane = threadIdx.x & 63;
-  const int mb = wv % MBt, j = wv / MBt;
-  const int r = lane >> 2, m = mb * 16 + r, c0 = (lane & 3) * 32;
+  // a work-group per 16 rows and 128 columns
+  const int mb = blockIdx.x % (unsigned)MBt, j = blockIdx.x / (unsigned)MBt;
+  const int r = threadIdx.x >> 4, m = mb * 16 + r, c0 = (threadIdx.x & 15) * 8;
   const int mt = mb / a.mb, mi = mb - mt * a.mb;
   uint8_t* stage = a.xq + ((size_t)mt * HB + j) * fp8_stage_bytes(a.mb);
-  uint8_t* dst = stage + mi * 2048 + (c0 >> 4) * 256 + r * 16;
-  float* xs = (float*)(stage + a.mb * 2048) + mi * 16 + r;
-  float x[32];
-  if (m < a.M) {
-    const uint16_t* src = a.hidden + (long long)m * a.hidden_rs + j * 128 + c0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const u32x4 v = *(const u32x4*)(src + q * 8);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[q * 8 + 2 * i] = __uint_as_float(v[i] << 16);
-        x[q * 8 + 2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
-  }
+  float x[8];
+  u32x4 v = u32x4{0, 0, 0, 0};
+  if (m < a.M) v = *(const u32x4*)(a.hidden + (long long)m * a.hidden_rs + j * 128 + c0);
   float am = kAmaxFloor;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) am = fmaxf(am, fabsf(x[i]));
-  am = fmaxf(am, __shfl_xor(am, 1));
-  am = fmaxf(am, __shfl_xor(am, 2));
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(v[i] << 16);
+    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    am = fmaxf(am, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+  }
+#pragma unroll
+  for (int i = 1; i < 16; i *= 2) am = fmaxf(am, __shfl_xor(am, i));
   const float s = am / kE4m3Max;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float* y = x + q * 16 + e * 4;
-      o[e] = quant4(clamp_e4m3(y[0] / s), clamp_e4m3(y[1] / s), clamp_e4m3(y[2] / s), clamp_e4m3(y[3] / s));
-    }
-    *(u32x4*)(dst + q * 256) = u32x4{o[0], o[1], o[2], o[3]};
-  }
-  if ((lane & 3) == 0) *xs = s;
+  for (int i = 0; i < 8; ++i) x[i] = clamp_e4m3(x[i] / s);
+  *(u32x2*)(stage + mi * 2048 + (c0 >> 4) * 256 + r * 16 + (c0 & 8)) =
+      u32x2{quant4(x[0], x[1], x[2], x[3]), quant4(x[4], x[5], x[6], x[7])};
+  if (c0 == 0) ((float*)(stage + a.mb * 2048))[mi * 16 + r] = s;
 }
 
 // Work-group barrier once this wave's copies of the next chunk have landed in
@@ -541,7 +523,7 @@ hipError_t launch_wide(const LmHeadFp8Args& a, hipStream_t st) {
 
 hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   const int MBt = (a.M + 15) >> 4, HB = a.H >> 7;
-  hipLaunchKernelGGL(quant_rows_kernel, dim3((unsigned)((HB * MBt + 3) / 4)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(quant_rows_kernel, dim3((unsigned)(HB * MBt)), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (a.mb) {
