@@ -9,12 +9,14 @@
 // tokens and pages start are two prefix sums over the batch (held in 64 bits),
 // so one work-group does them: the whole plan is a few KB and bound by the
 // latency of its dependent loads (idx_map, then the slot's state, then the
-// free list), not by bytes. Tokens are then filled in by the same work-group
-// for small steps, by a second launch for large ones.
+// free list), not by bytes: 32 requests of 8 tokens 4.8 us, 1024 requests with
+// prompts and releases 21 us and 5 us for the tokens. Tokens are filled in by
+// the same work-group for small steps, by a second launch for large ones.
 //
 // Append. Every element is read once and written once, 16 bytes a lane
 // (two reads and one write for an 8-bit cache): bound by HBM for long
-// prompts, by the launch for a decoding step.
+// prompts (16384 tokens of 8 heads of 128: 134 MB in 26.4 us, 5.1 TB/s), by the
+// launch for a decoding step (3.8 us).
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -24,7 +26,8 @@ namespace {
 // Tokens up to which the plan's own work-group writes positions and slots: past that one CU's stores cost more
 // than a launch.
 constexpr int kPlanFillTokens = 4096;
-// Threads of the plan: 256 keep its barriers and scans short (32 requests of 8 tokens: 4.8 us a launch); 1024 take large batches in fewer tiles.
+// Threads of the plan: 256 keep its barriers and scans short (32 requests of 8 tokens: 4.8 us a launch, 12.7 us with
+// 1024 and scans through LDS); 1024 take large batches in fewer tiles.
 constexpr int kPlanSmall = 256, kPlanLarge = 1024;
 
 // Inclusive prefix sum over the wave (its total stays below 2^32): shifts within rows of 16 lanes, then the

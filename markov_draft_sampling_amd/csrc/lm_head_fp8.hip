@@ -19,10 +19,11 @@
 // by chunk with the rows' scales behind, so that a chunk goes into LDS as one
 // linear copy without registers, shared by the waves.
 //
-// For few rows the call is bound by the matrix's V * H bytes (7 rows, V =
-// 200064, H = 4096: 149 us, 5.5 TB/s); at 224 rows by the matrix cores and the
-// operand reads from LDS (382 us, 960 TFLOP/s), which is why a wave takes 64
-// vocabulary rows: every hidden operand serves four products.
+// For few rows the call is bound by the matrix's V * H bytes (7 rows, H = 4096:
+// 149 us and 5.5 TB/s at V = 200064, 26.6 us at V = 32000, 4 of them the hidden
+// rows' launch); at 224 rows by the matrix cores and the operand reads from LDS
+// (V = 200064: 360 us, 1.02 PFLOP/s), which is why a wave takes 64 vocabulary
+// rows: every hidden operand serves four products.
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   store_logits<MB, NBW>(a, acc, mb0, vb0);
 }
 
-// 112 hidden rows by 512 vocabulary rows: eight waves, each with all 7 row blocks and 4 vocabulary blocks of its
+// 112 hidden rows by 64 vocabulary rows a wave, NW waves: each with all 7 row blocks and 4 vocabulary blocks of its
 // own. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS, shared; the wave's part of the
 // matrix (8 KB a chunk) one deep in a part of LDS of its own, widened into registers at the chunk's start, after
 // which the next chunk is copied over it. One barrier a chunk. A chunk's sums are scaled once, since the vector

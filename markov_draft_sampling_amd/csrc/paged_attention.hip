@@ -12,16 +12,25 @@
 // sums the unrounded p.
 //
 // Rows. The G query heads of one key head read the same keys, so a request's
-// rows are its (token, head in group) pairs, token-major: tiles of up to 64
-// rows, and every key and value is read from HBM once per tile.
+// rows are its (token, head in group) pairs, token-major, in tiles of 16, 32,
+// 64 or 128 rows: every key and value is read from HBM once per tile, and a
+// tile's work-group is one (request, rows, key head).
 //
-// Split. Few rows means few work-groups, so the keys are cut into chunks of
-// work-groups as well, whose (m, l, o) a second kernel joins.
+// Waves. A work-group is RG row groups of 32 rows (16 in the smallest tile)
+// by KG key groups of waves. Key group g takes blocks g, g + KG, .. of KB keys.
+// Few rows are bound by the cache's bytes: one row group, four key groups, a
+// work-group to a CU with 128 KB of LDS to keep reads in flight. Up to 64 rows
+// take two by two, a prompt's 128 rows four row groups that share every block;
+// both with two work-groups to a CU, so that one's softmax runs beside the
+// other's products. The key groups' (m, l, o) are joined through LDS at the end.
 //
-// Wave. Four waves of a work-group take the chunk's blocks of 32 keys in turn,
-// each with its own part of LDS and without a barrier: a block's keys and
-// values are copied straight into LDS (16 bytes a lane, no registers), two to
-// four blocks in flight per wave, 16-byte slots XOR-swizzled by row. Both
+// Split. Fewer tiles than CUs: the keys are cut into chunks of work-groups as
+// well, whose (m, l, o) a second kernel joins (attn_plan has the rule). More
+// work-groups than the CUs hold: the longest sequences go first.
+//
+// Block. Keys and values are copied straight into LDS (16 bytes a lane, no
+// registers), two to four blocks ahead, 16-byte slots XOR-swizzled by row. A key
+// group of one wave needs no barrier, one of several has one a block. Both
 // products are computed transposed on the matrix cores (16x16x32 bf16): the
 // scores as S^T = K Q^T, whose result layout (lane: one row, 4 keys of each
 // 16) is the operand layout of P^T once the keys of a block are taken in the
@@ -29,6 +38,14 @@
 // are read column-wise from LDS by the transposing LDS reads in that order.
 // 8-bit caches are widened to bf16 (exactly) after the LDS read; the key scale
 // joins the softmax scale, the value scale the final division.
+//
+// Measured (32 query heads, 8 key heads, D = 128, the reads of each key and
+// value once): one request of 131072 keys 105 us, 5.1 TB/s, bound by HBM; 32
+// requests of 8 tokens over 100 .. 8192 keys 129 us, 4.5 TB/s, the last CUs to
+// finish; 128 requests over an 8-bit cache 133 us, 4.3 TB/s; a chunk of
+// 2048 prompt tokens over 14336 keys 498 us, 1.01 PFLOP/s, bound by the vector
+// unit (the exponentials) and the matrix cores in turn; one token over 1037
+// keys 9.6 us, two launches' latency.
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -50,6 +67,7 @@ struct Tile {
   int lo, hi;                    // keys that some row sees: [lo, hi)
   int base;                      // lo rounded down to a block of 64
   int chunks;                    // chunks with keys (at least 1)
+  int at;                        // number of the tile in the batch's own order: its place in the partials
 };
 
 // keys [lo, hi) that token t of the request sees
@@ -67,16 +85,21 @@ __device__ __forceinline__ int clamp_tok(const PagedAttnArgs& a, int q, uint32_t
   return q;
 }
 
-// The request with the n-th longest sequence (B <= 128; every wave ranks them all, about a microsecond).
-__device__ __forceinline__ int nth_longest(const PagedAttnArgs& a, int n) {
+// The request with the n-th longest sequence (B <= 128; every wave ranks them all, about a microsecond), or -1 if it
+// surely has no key past the first `least` (the quick way out of a chunk that only longer sequences have).
+__device__ __forceinline__ int nth_longest(const PagedAttnArgs& a, int n, long long least) {
   const int lane = threadIdx.x & 63;
   // length above request number: all different (beyond 2^24 keys only the order may suffer)
-  int key[2], rank[2] = {0, 0};
+  constexpr int kTop = (1 << 24) - 1;
+  int key[2], rank[2] = {0, 0}, longer = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int b = lane + 64 * i;
-    key[i] = b < a.B ? min(max(a.seq_lens[b], 0), (1 << 24) - 1) * 128 + 127 - b : -1;
+    const int len = b < a.B ? min(max(a.seq_lens[b], 0), kTop) : 0;
+    key[i] = b < a.B ? len * 128 + 127 - b : -1;
+    longer += __popcll(__ballot(len > least));
   }
+  if (least > 0 && least < kTop && n >= longer) return -1;
   for (int b = 0; b < min(a.B, 64); ++b) {
     const int k = __builtin_amdgcn_readlane(key[0], b);
     rank[0] += k > key[0];
@@ -91,17 +114,25 @@ __device__ __forceinline__ int nth_longest(const PagedAttnArgs& a, int n) {
   return m0 ? __ffsll(m0) - 1 : m1 ? 63 + __ffsll(m1) : 0;
 }
 
+// c: the chunk it is wanted for
 template <int ROWS>
-__device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, uint32_t& bad) {
+__device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, int c, uint32_t& bad) {
   Tile t;
   t.rows = 0;
   if (a.per_req > 0) {
     t.b = tile / a.per_req;
     t.r0 = (tile - t.b * a.per_req) * ROWS;
-    if (a.by_length) t.b = nth_longest(a, t.b);
+    t.at = tile;
+    if (a.by_length) {
+      const int b = nth_longest(a, t.b, (long long)c * a.chunk);
+      if (b < 0) return t;
+      t.at += (b - t.b) * a.per_req;
+      t.b = b;
+    }
   } else {
     // Request b's tiles start at floor(q0 G / ROWS) + b: enough for its rows, since ceil(x) of its rows is at most
     // the step to the next request's start. The last request that starts at or before the tile, 64 probes a round.
+    t.at = tile;
     const int lane = threadIdx.x & 63;
     int step = 1;
     while (step * 64 < a.B) step *= 64;
@@ -295,7 +326,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   const int c = ct / a.tiles, tile = ct - c * a.tiles;
 
   uint32_t bad = 0;
-  const Tile t = find_tile<ROWS>(a, tile, bad);
+  const Tile t = find_tile<ROWS>(a, tile, c, bad);
   if (t.rows <= 0 || c >= t.chunks) {
     if (bad && tid == 0) set_status(a.status, bad);
     return;
@@ -656,7 +687,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
       if (t.chunks == 1) {
         store_row(a, t, row, h, od, o, Mr, L);
       } else {
-        const size_t pr = ((size_t)ct * a.Hkv + h) * ROWS + row;
+        const size_t pr = (((size_t)c * a.tiles + t.at) * a.Hkv + h) * ROWS + row;
         float* po = a.part_o + pr * D + od;
         *(floatx4*)po = floatx4{o[0], o[1], o[2], o[3]};
         *(floatx4*)(po + 4) = floatx4{o[4], o[5], o[6], o[7]};
@@ -667,19 +698,13 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   }
 }
 
-// Joins the chunks of a row tile: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. A wave per row: its lanes read
-// the chunks' (m, l) side by side, then four groups of 16 lanes take the chunks in turn.
+// Joins the chunks of a row: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. A wave's lanes read the chunks' (m, l)
+// side by side, then four groups of 16 lanes take the chunks in turn.
 template <int D, int ROWS>
-__global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
+__device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, int row, int h) {
   const int lane = threadIdx.x & 63;
-  const int h = blockIdx.x % (unsigned)a.Hkv;
-  const int tile = blockIdx.x / (unsigned)a.Hkv;
-  uint32_t bad = 0;
-  const Tile t = find_tile<ROWS>(a, tile, bad);
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 6);
-  if (row >= t.rows || t.chunks <= 1) return;
   const size_t step = (size_t)a.tiles * a.Hkv * ROWS;
-  const size_t pr = ((size_t)tile * a.Hkv + h) * ROWS + row;
+  const size_t pr = ((size_t)t.at * a.Hkv + h) * ROWS + row;
   float M = -INFINITY;
   for (int c = lane; c < t.chunks; c += 64) M = fmaxf(M, a.part_ml[pr + c * step].x);
   M = wave_max_f32(M);
@@ -713,6 +738,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
   if (g == 0) store_row(a, t, row, h, od, o, M, L);
 }
 
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
+  uint32_t bad = 0;
+  const Tile t = find_tile<ROWS>(a, blockIdx.x / (unsigned)a.Hkv, 0, bad);  // (in the batch's own order)
+  int row = blockIdx.y * 4 + (threadIdx.x >> 6);
+  if (row >= t.rows || t.chunks <= 1) return;
+#pragma nounroll
+  do {
+    join_row<D, ROWS>(a, t, row, blockIdx.x % (unsigned)a.Hkv);
+    row += 4 * gridDim.y;
+  } while (row < t.rows);
+}
+
 template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
 hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
   constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG, KB, LB>::kRows;
@@ -720,7 +758,11 @@ hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
-  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)wgs, ROWS / 4), dim3(256), 0, st, a);
+  // few tiles: a wave a row; many, most of which have nothing to join: some rows a wave
+  PagedAttnArgs j = a;
+  j.by_length = 0;
+  const unsigned per_tile = (unsigned)(wgs >= 4096 ? 1 : wgs * (ROWS / 4) <= 4096 ? ROWS / 4 : 4096 / wgs);
+  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)wgs, per_tile), dim3(256), 0, st, j);
   return hipGetLastError();
 }
 
@@ -744,24 +786,34 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   const long long by_rows = (long long)T * G / p.rows + B;
   p.per_req = direct * B <= by_rows ? (int)direct : 0;
   p.tiles = (int)(p.per_req ? direct * B : by_rows);
-  // Keys a tile reads at most. One work-group fits a CU, and a split costs its partials and the join's launch (32
-  // requests of up to 8192 keys in 256 work-groups: 135 us whole, 149 us in two chunks): the keys are cut only as
-  // far as it takes to give every CU a work-group, into chunks of at least 256, and into chunks of at most 16384,
-  // so that one long sequence among short ones does not wait for one CU.
+  // Keys a tile reads at most (a window's first block starts up to 63 keys before it).
   long long span = max_seq_len;
-  if (window > 0) span = span < (long long)window + max_q_len ? span : (long long)window + max_q_len;
+  if (window > 0) span = span < (long long)window + max_q_len + 63 ? span : (long long)window + max_q_len + 63;
+  // Chunks of keys. A split costs its partials and the join's launch, so fewer tiles than CUs are cut only as far as
+  // it takes to give every CU a work-group, into chunks of at least 256 keys. And no chunk is so long that the rest
+  // waits for its CU: with tiles bound by the cache's bytes, 4608 keys of 128 (of 32 requests with 8 key heads, over
+  // 100 to 8192 keys: 129 us, whole 136 us; one of 30000 keys among 500: 87 us, in chunks of 16384 200 us; the price
+  // where all are as long, 8000 keys: 203 us, whole 187 us), as many times longer as a CU has other tiles to run;
+  // with 128-row tiles, whose partials are larger and whose length hides in their products, 16384 (2048
+  // prompt tokens over 14336: 500 us whole, 560 us in chunks of 4096). At most 8
+  // chunks of a guess that is far too long, each of which costs a work-group that finds nothing (128 requests of 2000
+  // 8-bit keys and a guess of 131072: 155 us, without that 181 us).
   const long long wgs = (long long)p.tiles * Hkv;
   const long long want = (256 + wgs - 1) / wgs;
-  long long chunk = (span + 64 + want - 1) / want;
-  if (chunk > 16384) chunk = 16384;
+  long long chunk = (span + want - 1) / want, cap = 16384;
+  if (p.rows <= 64) {
+    cap = 4608 * 128 / D * (wgs > 1024 ? wgs / 1024 : 1);
+    if (cap < span / 8) cap = span / 8;
+  }
+  if (chunk > cap) chunk = cap;
   chunk = (chunk + 127) / 128 * 128;
   if (chunk < 256) chunk = 256;
-  long long n = (span + 63 + chunk - 1) / chunk;
+  long long n = (span + chunk - 1) / chunk;
   if (n < 1) n = 1;
   p.chunk = (int)chunk;
   p.n_chunks = (int)n;
   // more work-groups than the CUs hold at once: the longest sequences go first, so that none starts last
-  // (128 requests of 1 to 4096 keys over an 8-bit cache: 141 us against 167 us in the batch's order)
+  // (128 requests of 1 to 4096 keys over an 8-bit cache: 134 us against 173 us in the batch's order)
   p.by_length = p.per_req > 0 && B > 1 && B <= 128 && wgs * n > 256;
   const size_t rows = (size_t)p.n_chunks * p.tiles * Hkv * p.rows;
   p.part_o = 256;

@@ -205,6 +205,19 @@ def test_longest_first_order(B, Hk):
     _case(ctx, chunk, 2 * Hk, Hk, 64, 16, seed=B, idx=True)
 
 
+@pytest.mark.parametrize("guess", [None, 100, 4700, 40000])
+def test_some_long_sequences_among_many(guess):
+    # chunks that only some requests have, a guess that is too small (the last chunk takes the rest) or too large
+    rng = np.random.default_rng(1)
+    ctx = rng.integers(0, 60, 40).tolist()
+    ctx[3], ctx[17], ctx[30] = 10000, 4605, 4610
+    chunk = rng.choice([0, 1, 2], 40).tolist()
+    chunk[3], chunk[17], chunk[30] = 2, 1, 2
+    _case(ctx, chunk, 16, 8, 128, 16, seed=11, idx=True, max_seq=guess)
+    ctx = rng.integers(0, 700, 100).tolist()
+    _case(ctx, [2] * 100, 8, 4, 64, 16, "e4m3", seed=12, max_seq=guess)
+
+
 @pytest.mark.parametrize("rows", [1, 4, 20, 100])
 @pytest.mark.parametrize("window", [0, 9])
 def test_infinities_and_nan_stay_with_the_rows_that_see_them(rows, window):
