@@ -698,36 +698,55 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   }
 }
 
-// Joins the chunks of a row: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. A wave's lanes read the chunks' (m, l)
-// side by side, then four groups of 16 lanes take the chunks in turn.
+// Joins the chunks of a row: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. Four groups of 16 lanes take the chunks in
+// turn, four of them in flight each, with a running maximum of their own, and are joined at the end.
 template <int D, int ROWS>
 __device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, int row, int h) {
   const int lane = threadIdx.x & 63;
   const size_t step = (size_t)a.tiles * a.Hkv * ROWS;
   const size_t pr = ((size_t)t.at * a.Hkv + h) * ROWS + row;
-  float M = -INFINITY;
-  for (int c = lane; c < t.chunks; c += 64) M = fmaxf(M, a.part_ml[pr + c * step].x);
-  M = wave_max_f32(M);
-  constexpr int NC = D / 16;
+  constexpr int NC = D / 16, NL = 4;
   const int g = lane >> 4, od = (lane & 15) * NC;
-  float L = 0.0f, o[NC];
+  float M = -INFINITY, L = 0.0f, o[NC];
 #pragma unroll
   for (int e = 0; e < NC; ++e) o[e] = 0.0f;
-#pragma unroll 4
-  for (int c = g; c < t.chunks; c += 4) {
-    const float2 ml = a.part_ml[pr + c * step];
-    const float* po = a.part_o + (pr + c * step) * D + od;
-    floatx4 x[NC / 4];
+  auto scale_to = [&](float x) {  // from M to x >= M
+    const float f = M == x ? 1.0f : __builtin_amdgcn_exp2f(M - x);
+    M = x;
+    L *= f;
 #pragma unroll
-    for (int q = 0; q < NC / 4; ++q) x[q] = *(const floatx4*)(po + q * 4);
-    // a chunk without keys of the row has (-inf, 0) and zeros
-    const float f = ml.x == -INFINITY && ml.y == ml.y ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
-    L += ml.y * f;
+    for (int e = 0; e < NC; ++e) o[e] *= f;
+  };
+#pragma nounroll
+  for (int c0 = 0; c0 < t.chunks; c0 += 4 * NL) {
+    float2 ml[NL];
+    floatx4 x[NL][NC / 4];
 #pragma unroll
-    for (int q = 0; q < NC / 4; ++q)
+    for (int i = 0; i < NL; ++i) {
+      const int c = c0 + 4 * i + g;
+      const size_t p = pr + min(c, t.chunks - 1) * step;
+      ml[i] = a.part_ml[p];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[q * 4 + e] += x[q][e] * f;
+      for (int q = 0; q < NC / 4; ++q) x[i][q] = *(const floatx4*)(a.part_o + p * D + od + q * 4);
+      if (c >= t.chunks) ml[i] = make_float2(-INFINITY, 0.0f);
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) top = fmaxf(top, ml[i].x);
+    scale_to(top);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      // a chunk without keys of the row has (-inf, 0)
+      const bool none = ml[i].x == -INFINITY && ml[i].y == ml[i].y;
+      const float f = none ? 0.0f : __builtin_amdgcn_exp2f(ml[i].x - M);
+      L += ml[i].y * f;
+#pragma unroll
+      for (int q = 0; q < NC / 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[q * 4 + e] += none ? 0.0f : x[i][q][e] * f;
+    }
   }
+  scale_to(fmaxf(M, fmaxf(__shfl_xor(M, 16), fmaxf(__shfl_xor(M, 32), __shfl_xor(M, 48)))));
 #pragma unroll
   for (int e = 0; e < NC; ++e) {
     o[e] += __shfl_xor(o[e], 16);
