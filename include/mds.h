@@ -600,8 +600,9 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  *                 mds_kv_page_tables (a slot < 0 or >= n_slots has no keys)
  *   query_start   int32 [B + 1], from 0, not decreasing, at most T
  *   seq_lens      int32 [B]
- *   max_q_len     no request has more new tokens (a host bound: what is
- *                 past it is not computed, MDS_STATUS_BAD_INDEX)
+ *   max_q_len     no request has more new tokens (a host bound: tokens past
+ *                 it may be left out, then with MDS_STATUS_BAD_INDEX; 0: the
+ *                 call does nothing)
  *   max_seq_len   no sequence is longer, as a guess: it steers how the work is
  *                 cut; results do not depend on it beyond float32 rounding
  *   scale         > 0 (1 / sqrt(D))

@@ -295,6 +295,38 @@ def test_out_of_contract_device_data_is_flagged_and_stays_in_bounds():
     assert st in (0, 8)
 
 
+@pytest.mark.parametrize("Hq,Hk,D", [(256, 1, 64), (200, 1, 128), (64, 64, 64), (130, 2, 64)])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_many_heads(Hq, Hk, D, cache):
+    # one token's heads over more than one row tile, and a key head for each
+    _case([50, 0, 333], [2, 1, 1], Hq, Hk, D, 16, cache, seed=Hq)
+
+
+def test_two_calls_at_once_on_two_streams():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(3)
+    kp = torch.randn((400, 16, 2, 128), generator=g).to(torch.bfloat16).cuda()
+    q = [torch.randn((n, 8, 128), generator=g).to(torch.bfloat16).cuda() for n in (300, 9)]
+    table = t(np.random.default_rng(0).permutation(400)[:384].reshape(3, 128))
+    qs, seq = [t([0, 200, 250, 300]), t([0, 8, 8, 9])], t([1900, 700, 2040])
+    mq, ms = (200, 8), 2048
+    want = []
+    for i in range(2):
+        want.append(torch.zeros_like(q[i]))
+        mds.paged_attention(q[i], kp, kp, table, qs[i], seq, want[i], mq[i], ms)
+    got = [torch.zeros_like(x) for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            mds.paged_attention(q[i], kp, kp, table, qs[i], seq, got[i], mq[i], ms, stream=st)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i], want[i])
+
+
 def test_large_scores_and_a_peak_late_in_the_row():
     # scores up to some hundreds: the running maximum has to move many times
     _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
