@@ -205,7 +205,7 @@ __device__ __forceinline__ void store_logits(const LmHeadFp8Args& a, const float
   }
 }
 
-// Up to 64 hidden rows (MB 16-row blocks): four waves, each with all the rows and NBW 16-row blocks of the
+// Up to 32 hidden rows (MB 16-row blocks): four waves, each with all the rows and NBW 16-row blocks of the
 // vocabulary. Bound by the matrix, which each wave reads on its own: four chunks of it are in flight in registers,
 // four of the hidden rows in LDS.
 template <int MB, int NBW>
@@ -299,22 +299,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   store_logits<MB, NBW>(a, acc, mb0, vb0);
 }
 
-// 112 hidden rows by 64 vocabulary rows a wave, NW waves: each with all 7 row blocks and 4 vocabulary blocks of its
-// own. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS, shared; the wave's part of the
-// matrix (8 KB a chunk) one deep in a part of LDS of its own, widened into registers at the chunk's start, after
-// which the next chunk is copied over it. One barrier a chunk. A chunk's sums are scaled once, since the vector
-// unit would be the bound otherwise. The two row tiles of 224 rows run on the same XCD next to each other, so that
-// the second one finds the matrix in the caches.
-template <int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_wide_kernel(
+// More rows: a work-group of four waves has MB 16-row blocks of them, a wave all of these and NBW vocabulary blocks of
+// its own. A chunk (128 columns) at a time: the hidden rows two chunks deep in LDS, shared; the wave's part of the
+// matrix (2 KB a block and chunk) one deep in a part of LDS of its own, widened into registers at the chunk's start,
+// after which the next chunk is copied over it. One barrier a chunk. A chunk's sums are scaled once, since the vector
+// unit would be the bound otherwise. The row tiles of a vocabulary tile run on the same XCD next to each other, so that
+// the later ones find the matrix in the caches. Four waves, two work-groups a CU: against eight waves and one, 77 us to
+// 104 us at V = 32000 and 284 us to 317 us at V = 151936, whose last round would be short of work-groups, and as fast
+// where the rounds come out even (H = 4096, 224 rows, NBW = 4).
+constexpr int kWideWaves = 4;
+template <int MB, int NBW>
+__global__ __launch_bounds__(64 * kWideWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_wide_kernel(
     LmHeadFp8Args a, int v_tiles, int m_tiles) {
-  constexpr int MB = 7, NBW = 4;
+  constexpr int NW = kWideWaves;
+  constexpr int kScales = (NW * NBW + 7) / 8;  // scale blocks (8 vocabulary blocks) of a work-group
   constexpr int kStage = fp8_stage_bytes(MB);
   constexpr int kCopy = kStage / 1024;
   constexpr int kQ = (kCopy + NW - 1) / NW;
   __shared__ __attribute__((aligned(16))) uint8_t s_x[2][kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t s_w[NW][4 * 2048];
-  __shared__ float s_ws[NW / 2][512];  // the scale blocks' scales, by chunk (H <= 65536)
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[NW][NBW * 2048];
+  __shared__ float s_ws[kScales][512];  // the scale blocks' scales, by chunk (H <= 65536)
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15;
@@ -326,7 +330,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int vt0 = vt * NW * NBW;
   const int coff = __builtin_amdgcn_readfirstlane((int)(((unsigned)vt * (unsigned)kStagger) % (unsigned)HB));
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
-  for (int i = tid; i < NW / 2 * HB; i += 64 * NW) {
+  for (int i = tid; i < kScales * HB; i += 64 * NW) {
     const int b = i / HB;
     s_ws[b][i - b * HB] = a.w_scale[(size_t)min((vt0 >> 3) + b, (a.V - 1) >> 7) * HB + i - b * HB];
   }
@@ -368,7 +372,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
         A[nb][2 * p] = widen8(x[0], x[1]);
         A[nb][2 * p + 1] = widen8(x[2], x[3]);
       }
-    const float sw = s_ws[w >> 1][chunk_of(c)];
+    const float sw = s_ws[kScales == 1 ? 0 : w * NBW >> 3][chunk_of(c)];
     // the wave has read its part of the matrix: its next chunk may land on it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (c + 1 < HB) {
@@ -416,7 +420,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
         if (mb + 1 < MB) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 4 * NBW; ++k) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
         }
@@ -508,16 +512,24 @@ hipError_t launch_mb(const LmHeadFp8Args& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// 256 vocabulary rows a work-group, two work-groups a CU: against one of 512 (eight waves) 77 us to 104 us at
-// V = 32000 and 284 us to 317 us at V = 151936, whose last round would be short of work-groups, and as fast where
-// the rounds come out even (H = 4096, 224 rows).
-constexpr int kWideWaves = 4;
+// Vocabulary blocks a wave: four, so that every hidden operand serves four products, where that leaves more than a
+// work-group to a CU; else two, down to half a work-group to a CU, and one below that (H = 4096, us with four / two /
+// one: V = 65536, 224 rows 115 / 137 / 180, 112 rows 82 / 72 / 95; V = 32000, 224 rows 76 / 69 / 88, 66 rows 57 / 40 / 38;
+// V = 4099, 66 rows 55 / 35 / 29).
+constexpr long long kWide4 = 256 * kWideWaves * 4, kWide2 = 256 * kWideWaves * 2;  // 16-row blocks, all row tiles
+
+template <int MB>
 hipError_t launch_wide(const LmHeadFp8Args& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + 6) / 7;
-  const int tiles = (VB + kWideWaves * 4 - 1) / (kWideWaves * 4);
-  hipLaunchKernelGGL(lm_head_fp8_wide_kernel<kWideWaves>, dim3((unsigned)((tiles + 7) / 8 * 8 * mt)),
-                     dim3(64 * kWideWaves), 0, st, a, tiles, mt);
-  return hipGetLastError();
+  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + MB - 1) / MB;
+  auto launch = [&](auto kernel, int nbw) {
+    const int tiles = (VB + kWideWaves * nbw - 1) / (kWideWaves * nbw);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles + 7) / 8 * 8 * mt)), dim3(64 * kWideWaves), 0, st, a, tiles, mt);
+    return hipGetLastError();
+  };
+  const long long blocks = (long long)VB * mt;
+  if (blocks > kWide4) return launch(lm_head_fp8_wide_kernel<MB, 4>, 4);
+  if (blocks >= kWide2) return launch(lm_head_fp8_wide_kernel<MB, 2>, 2);
+  return launch(lm_head_fp8_wide_kernel<MB, 1>, 1);
 }
 
 }  // namespace
@@ -529,15 +541,21 @@ hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   switch (a.mb) {
     case 1: return launch_mb<1, 1>(a, st);
-    case 2: return launch_mb<2, 1>(a, st);
-    case 4: return launch_mb<4, 2>(a, st);
-    default: return launch_wide(a, st);
+    case 2:
+      // 32 rows, H = 4096: 163 us to 172 us at V = 200064, 53 us to 57 us at V = 65536; 31 us to 29 us at V = 32000
+      return (a.V + 15) >> 4 >= kWide2 ? launch_wide<2>(a, st) : launch_mb<2, 1>(a, st);
+    case 3: return launch_wide<3>(a, st);
+    case 4: return launch_wide<4>(a, st);
+    case 5: return launch_wide<5>(a, st);
+    case 6: return launch_wide<6>(a, st);
+    default: return launch_wide<7>(a, st);
   }
 }
 
+// Row tiles of at most 7 blocks, all of one height (126 rows in 4 + 4 blocks, V = 200064: 288 us, in 7 + 1 359 us).
 int lm_head_fp8_blocks(int M) {
-  const int n = (M + 15) >> 4;
-  return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 7;
+  const int n = (M + 15) >> 4, tiles = (n + 6) / 7;
+  return (n + tiles - 1) / tiles;
 }
 
 hipError_t launch_tile_fp8(int V, int H, const uint8_t* codes, uint8_t* tiled, hipStream_t st) {

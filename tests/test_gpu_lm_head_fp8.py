@@ -70,6 +70,12 @@ def test_lm_head_fp8(B, K, V, H, mode):
     _run(B, K, V, H, seed=B + V, mode=mode)
 
 
+@pytest.mark.parametrize("rows", [17, 32, 33, 48, 64, 66, 84, 112, 126, 140, 170, 224])
+@pytest.mark.parametrize("V", [20003, 33003, 65701])
+def test_every_row_tile_and_vocabulary_width(rows, V):
+    _run(rows, 1, V, 128, seed=rows)
+
+
 def test_lm_head_fp8_bf16_out_strided_with_rows_left_alone():
     _run(6, 8, 1003, 256, seed=1, out_dtype="bf16", pad=5, extra=2)
     _run(6, 8, 1003, 256, seed=1, out_dtype="f32", pad=5, extra=2)
