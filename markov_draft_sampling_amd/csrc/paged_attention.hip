@@ -800,30 +800,51 @@ hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
 AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
   AttnPlan p;
   const long long most = (long long)max_q_len * G;  // rows of the longest request
-  p.rows = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
-  const long long direct = (most + p.rows - 1) / p.rows;
-  const long long by_rows = (long long)T * G / p.rows + B;
-  p.per_req = direct * B <= by_rows ? (int)direct : 0;
-  p.tiles = (int)(p.per_req ? direct * B : by_rows);
   // Keys a tile reads at most (a window's first block starts up to 63 keys before it).
   long long span = max_seq_len;
   if (window > 0) span = span < (long long)window + max_q_len + 63 ? span : (long long)window + max_q_len + 63;
-  // Chunks of keys. A split costs its partials and the join's launch, so fewer tiles than CUs are cut only as far as
-  // it takes to give every CU a work-group, into chunks of at least 256 keys. And no chunk is so long that the rest
-  // waits for its CU: with tiles bound by the cache's bytes, 4608 keys of 128 (of 32 requests with 8 key heads, over
-  // 100 to 8192 keys: 129 us, whole 136 us; one of 30000 keys among 500: 87 us, in chunks of 16384 200 us; the price
-  // where all are as long, 8000 keys: 203 us, whole 187 us), as many times longer as a CU has other tiles to run;
-  // with 128-row tiles, whose partials are larger and whose length hides in their products, 16384 (2048
-  // prompt tokens over 14336: 500 us whole, 560 us in chunks of 4096). At most 8
-  // chunks of a guess that is far too long, each of which costs a work-group that finds nothing (128 requests of 2000
-  // 8-bit keys and a guess of 131072: 155 us, without that 181 us).
+  auto direct = [&](int rows) { return (most + rows - 1) / rows; };
+  auto by_rows = [&](int rows) { return (long long)T * G / rows + B; };
+  auto work_groups = [&](int rows) {
+    const long long d = direct(rows) * B, r = by_rows(rows);
+    return (d < r ? d : r) * Hkv;
+  };
+  // Rows of a tile. All of a request's rows, up to 64, so that its keys are read once; for prompts 128 where that fills
+  // the CUs twice, with the keys cut into chunks of 1024 or more, else 64 (8 key heads, 32 heads, 128 / 64 rows: 1024
+  // tokens over 4096 keys 111 / 130 us; 1024 tokens over none 36 / 29 us). Over short sequences, where the
+  // time is that of the longest chain of one work-group, the smallest tile that leaves every work-group its own CU
+  // (128 tokens over none: 7.4 us with 16 rows, 9.7 with 32, 10.5 with 64, 13.3 with 128; 2 times 290 tokens, 4 key
+  // heads, 12 heads: 12.6 us with 32, 17.0 with 16 in two rounds, 18.5 with 64).
+  if (most <= 16 || (span <= 1024 && work_groups(16) <= 256))
+    p.rows = 16;
+  else if (most <= 32 || (span <= 1024 && work_groups(32) <= 256))
+    p.rows = 32;
+  else
+    p.rows = most <= 64 || work_groups(128) * (span < 2048 ? 1 : span / 1024) < 512 ? 64 : 128;
+  p.per_req = direct(p.rows) * B <= by_rows(p.rows) ? (int)direct(p.rows) : 0;
+  p.tiles = (int)(p.per_req ? direct(p.rows) * B : by_rows(p.rows));
+  // Chunks of keys. A split costs its partials and the join's launch, so fewer tiles than CUs are cut only into as many
+  // work-groups as run at once (one a CU with up to 32 rows, two above, the second only for chunks of 1024 or more),
+  // into chunks of at least 256 keys: one more would wait for a second round (217 tiles of 290 keys: 12.6 us
+  // whole, 23.8 us in two chunks). And no chunk is so long that the rest waits for its CU: with tiles bound by
+  // the cache's bytes, 4608 keys of 128 (of 32 requests with 8 key heads, over 100 to 8192 keys: 129 us, whole 136 us;
+  // one of 30000 keys among 500: 87 us, in chunks of 16384 200 us; the price where all are as long, 8000 keys: 203 us,
+  // whole 187 us), as many times longer as a CU has other tiles to run; with 128-row tiles, whose partials are
+  // larger and whose length hides in their products, 16384 (2048 prompt tokens over 14336: 500 us whole, 560 us in
+  // chunks of 4096). At most 8 chunks of a guess that is far too long, each of which costs a work-group that finds
+  // nothing (128 requests of 2000 8-bit keys and a guess of 131072: 155 us, without that 181 us).
   const long long wgs = (long long)p.tiles * Hkv;
-  const long long want = (256 + wgs - 1) / wgs;
-  long long chunk = (span + want - 1) / want, cap = 16384;
+  long long want = wgs < 256 ? 256 / wgs : 1, cap = 16384;
+  if (p.rows > 32) {
+    long long twice = wgs < 512 ? 512 / wgs : 1;
+    if (twice > span / 1024) twice = span / 1024;
+    if (want < twice) want = twice;
+  }
   if (p.rows <= 64) {
     cap = 4608 * 128 / D * (wgs > 1024 ? wgs / 1024 : 1);
     if (cap < span / 8) cap = span / 8;
   }
+  long long chunk = (span + want - 1) / want;
   if (chunk > cap) chunk = cap;
   chunk = (chunk + 127) / 128 * 128;
   if (chunk < 256) chunk = 256;

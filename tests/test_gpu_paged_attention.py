@@ -327,6 +327,54 @@ def test_two_calls_at_once_on_two_streams():
         assert torch.equal(got[i], want[i])
 
 
+# guesses of the longest sequence that lead to tiles of 64 and 128 rows for prompts as short as these
+TALL = {64: 1100, 128: 600000}
+
+
+@pytest.mark.parametrize("rows", sorted(TALL))
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+def test_tall_tiles(rows, D, cache):
+    _case([0, 40, 130], [150, 1, 77], 4, 2, D, 16, cache, seed=9, q_layout="htd", max_seq=TALL[rows])
+    _case([100], [130], 3, 1, D, 32, cache, window=50, seed=1, max_seq=TALL[rows], max_q=TALL[rows])
+    _case([100, 7], [130, 200], 3, 1, D, 16, cache, causal=False, seed=2, max_seq=TALL[rows], idx=True)
+    _case([0], [300], 1, 1, D, 64, cache, window=1, seed=3, max_seq=TALL[rows], max_q=TALL[rows], layout="hnd")
+
+
+def test_tall_tiles_over_split_keys():
+    # chunks of 1536 and of 1152 keys of 128-row tiles, of 1152 of 64-row tiles; some of them a row does not reach
+    _case([4000], [300], 64, 32, 64, 16, seed=4)
+    _case([2100], [100], 256, 64, 64, 16, "e4m3", seed=5, window=2000)
+    _case([2100], [100], 8, 2, 128, 16, seed=6, window=2000)
+
+
+@pytest.mark.parametrize("tall", sorted(TALL))
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinities_and_nan_in_tall_tiles(tall, D):
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    L, n, window = 400, 190, 30
+    g = torch.Generator().manual_seed(tall)
+    q = torch.randn(n, 2, D, generator=g).to(torch.bfloat16)
+    k = torch.randn(25, 16, 1, D, generator=g).to(torch.bfloat16)
+    v = torch.randn(25, 16, 1, D, generator=g).to(torch.bfloat16)
+    kf, vf = k.view(-1, D), v.view(-1, D)
+    inf, nan = float("inf"), float("nan")
+    vf[L - 1, 3], vf[L - 1, 4], vf[L - 1, 5] = inf, nan, -inf
+    vf[300, 7], vf[301, 7], vf[250, 9] = inf, -inf, nan
+    kf[L - 2, 0], kf[320, 1] = nan, nan
+    out = torch.zeros_like(q).cuda()
+    table = t([list(range(25))])
+    mds.paged_attention(q.cuda(), k.cuda(), v.cuda(), table, t([0, n]), t([L]), out, TALL[tall], TALL[tall],
+                        window=window)
+    ref, _, _, _ = sr.attention(q, k, v, table.cpu().numpy(), [0, n], [L], 1 / math.sqrt(D), True, window)
+    o = out.cpu().double()
+    assert torch.equal(torch.isnan(o), torch.isnan(ref))
+    assert torch.equal(torch.isinf(o), torch.isinf(ref)) and torch.equal(o[torch.isinf(o)], ref[torch.isinf(ref)])
+    ok = torch.isfinite(ref)
+    assert ok.any() and ((o - ref).abs()[ok] < 2.0 ** -8 * (ref.abs()[ok] + 4.0)).all()
+
+
 def test_large_scores_and_a_peak_late_in_the_row():
     # scores up to some hundreds: the running maximum has to move many times
     _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
