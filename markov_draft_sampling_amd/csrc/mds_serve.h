@@ -77,7 +77,7 @@ struct PagedAttnArgs {
 };
 // Row tiles, chunks and workspace bytes of a call (host only).
 struct AttnPlan {
-  int rows, tiles, per_req, chunk, n_chunks;
+  int rows, key_groups, tiles, per_req, chunk, n_chunks;
   bool by_length;
   size_t part_o, part_ml, total;  // workspace offsets and size
 };

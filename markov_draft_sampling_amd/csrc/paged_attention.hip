@@ -19,7 +19,8 @@
 // Waves. A work-group is RG row groups of 32 rows (16 in the smallest tile)
 // by KG key groups of waves. Key group g takes blocks g, g + KG, .. of KB keys.
 // Few rows are bound by the cache's bytes: one row group, four key groups, a
-// work-group to a CU with 128 KB of LDS to keep reads in flight. Up to 64 rows
+// work-group to a CU with 128 KB of LDS to keep reads in flight (or, over short
+// sequences of many requests, fewer key groups in two or four work-groups). Up to 64 rows
 // take two by two, a prompt's 128 rows four row groups that share every block;
 // both with two work-groups to a CU, so that one's softmax runs beside the
 // other's products. The key groups' (m, l, o) are joined through LDS at the end.
@@ -303,7 +304,7 @@ struct AttnShape {
 
 template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
 __global__ __launch_bounds__(64 * RG * KG) __attribute__((
-    amdgpu_waves_per_eu(RG * KG / 4 * (LB <= 64 ? 2 : 1), RG * KG / 4 * (LB <= 64 ? 2 : 1)))) void attn_kernel(
+    amdgpu_waves_per_eu(RG > 1 ? 2 : 1, RG > 1 ? 2 : 1))) void attn_kernel(
     PagedAttnArgs a) {
   using Sh = AttnShape<D, E4M3, NB, RG, KG, KB, LB>;
   constexpr int ROWS = Sh::kRows, RB = Sh::RB, kPart = Sh::kPart, kStage = Sh::kStage, NST = Sh::NST;
@@ -786,11 +787,15 @@ hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
 }
 
 template <int D, bool E4M3>
-hipError_t launch_d(const PagedAttnArgs& a, int rows, hipStream_t st) {
-  switch (rows) {
-    case 16: return launch_shape<D, E4M3, 1, 1, 4, 32, 128>(a, st);
-    case 32: return launch_shape<D, E4M3, 2, 1, 4, 32, 128>(a, st);
-    case 64: return launch_shape<D, E4M3, 2, 2, 2, 32, 64>(a, st);
+hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_t st) {
+  switch (rows * 10 + key_groups) {
+    case 161: return launch_shape<D, E4M3, 1, 1, 1, 32, 32>(a, st);
+    case 162: return launch_shape<D, E4M3, 1, 1, 2, 32, 64>(a, st);
+    case 164: return launch_shape<D, E4M3, 1, 1, 4, 32, 128>(a, st);
+    case 321: return launch_shape<D, E4M3, 2, 1, 1, 32, 32>(a, st);
+    case 322: return launch_shape<D, E4M3, 2, 1, 2, 32, 64>(a, st);
+    case 324: return launch_shape<D, E4M3, 2, 1, 4, 32, 128>(a, st);
+    case 642: return launch_shape<D, E4M3, 2, 2, 2, 32, 64>(a, st);
     default: return launch_shape<D, E4M3, 2, 4, 1, 64, 64>(a, st);
   }
 }
@@ -834,6 +839,13 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   // chunks of 4096). At most 8 chunks of a guess that is far too long, each of which costs a work-group that finds
   // nothing (128 requests of 2000 8-bit keys and a guess of 131072: 155 us, without that 181 us).
   const long long wgs = (long long)p.tiles * Hkv;
+  // Key groups of up to 32 rows: four share a long sequence and end together. Over short ones, with more tiles than
+  // CUs, the start and end of a work-group count, and two or four smaller ones to a CU hide them (8 key heads, 128
+  // requests of one token: over 50 keys 13.5 us to 42.3 us with one key group, over 1 to 1024 keys 61 us to 77 us; 64
+  // requests over 1 to 512 keys 21.5 us to 26.5 us with two; 128 over 1 to 4096 keys 243 us to 209 us).
+  p.key_groups = p.rows > 64 ? 1 : p.rows > 32 ? 2 : 4;
+  if (p.rows <= 32 && span <= 1024 && wgs > 512) p.key_groups = 1;
+  if (p.rows <= 32 && span <= 512 && wgs > 256 && wgs <= 512) p.key_groups = 2;
   long long want = wgs < 256 ? 256 / wgs : 1, cap = 16384;
   if (p.rows > 32) {
     long long twice = wgs < 512 ? 512 / wgs : 1;
@@ -863,8 +875,8 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
 }
 
 hipError_t launch_paged_attention(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (a.D == 128) return a.e4m3 ? launch_d<128, true>(a, p.rows, st) : launch_d<128, false>(a, p.rows, st);
-  return a.e4m3 ? launch_d<64, true>(a, p.rows, st) : launch_d<64, false>(a, p.rows, st);
+  if (a.D == 128) return a.e4m3 ? launch_d<128, true>(a, p.rows, p.key_groups, st) : launch_d<128, false>(a, p.rows, p.key_groups, st);
+  return a.e4m3 ? launch_d<64, true>(a, p.rows, p.key_groups, st) : launch_d<64, false>(a, p.rows, p.key_groups, st);
 }
 
 }  // namespace mds

@@ -327,6 +327,17 @@ def test_two_calls_at_once_on_two_streams():
         assert torch.equal(got[i], want[i])
 
 
+@pytest.mark.parametrize("B", [70, 140])
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+@pytest.mark.parametrize("G", [2, 7])
+def test_many_short_sequences(B, D, cache, G):
+    # fewer key groups a work-group: more tiles than CUs over short sequences
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(0, 470, B).tolist()
+    _case(ctx, rng.choice([1, 2, 3, 4], B).tolist(), 4 * G, 4, D, 16, cache, seed=B, idx=True,
+          window=0 if G == 2 else 300)
+
+
 # guesses of the longest sequence that lead to tiles of 64 and 128 rows for prompts as short as these
 TALL = {64: 1100, 128: 600000}
 
