@@ -668,6 +668,20 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
                     const float* scales, void* out, int out_dtype, int64_t out_req_stride, int64_t out_step_stride,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * mds_call_packed - one of the serving calls from an array of its arguments
+ * (all but the stream, in their order, 8 bytes each: integers and pointers as
+ * int64, a float as the bits of a double), for bindings in which every argument
+ * of a call costs time. n: how many there are. Returns what the call returns;
+ * MDS_ERR_INVALID_ARG for an unknown call, another n or an integer out of its
+ * type's range.
+ */
+#define MDS_PACKED_PAGE_TABLES 0     /* mds_kv_page_tables, n = 23 */
+#define MDS_PACKED_APPEND 1          /* mds_kv_append, n = 24 */
+#define MDS_PACKED_ATTENTION 2       /* mds_paged_attention, n = 38 */
+#define MDS_PACKED_LM_HEAD_FP8 3     /* mds_lm_head_fp8, n = 14 */
+int mds_call_packed(int call, const int64_t* args, int n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

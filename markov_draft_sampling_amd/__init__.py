@@ -91,6 +91,7 @@ _SIGS = {
     "mds_quantize_lm_head_fp8": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _vp], _c_int),
     "mds_lm_head_fp8_workspace_bytes": ([_c_int] * 4 + [ctypes.POINTER(_c_sz)], _c_int),
     "mds_lm_head_fp8": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp, _c_sz, _vp], _c_int),
+    "mds_call_packed": ([_c_int, ctypes.c_char_p, _c_int, _vp], _c_int),
     "mds_debug_top_p": ([_c_int, _c_int, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_sz, _vp], _c_int),
 }
 

@@ -392,4 +392,50 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   return e == hipSuccess ? abi_ok() : hip_fail(e);
 }
 
+int mds_call_packed(int call, const int64_t* a, int n, void* stream) {
+  // the calls' argument types: i int, l int64, p pointer, z size, f float
+  static const char* const kTypes[] = {"iiiiiipppippppppppppppp", "iiipllpllppiiillllllpppp",
+                                       "iiiiipllppiiillllllpiipppilfiipppllppz", "iiiiplpppillpz"};
+  if (call < 0 || call > MDS_PACKED_LM_HEAD_FP8) return abi_fail(MDS_ERR_INVALID_ARG, "unknown call");
+  if (!a) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
+  const char* t = kTypes[call];
+  for (int i = 0; i < n || t[i]; ++i) {
+    if (i >= n || !t[i]) return abi_fail(MDS_ERR_INVALID_ARG, "wrong number of arguments");
+    if ((t[i] == 'i' && a[i] != (int)a[i]) || (t[i] == 'z' && a[i] < 0))
+      return abi_fail(MDS_ERR_INVALID_ARG, "an integer is out of its type's range");
+  }
+  auto real = [](int64_t x) {
+    double d;
+    static_assert(sizeof d == sizeof x, "8 bytes");
+    __builtin_memcpy(&d, &x, sizeof d);
+    return (float)d;
+  };
+  switch (call) {
+    case MDS_PACKED_PAGE_TABLES:
+      return mds_kv_page_tables((int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (int)a[5],
+                                (const int32_t*)a[6], (const int32_t*)a[7], (const int32_t*)a[8], (int)a[9],
+                                (const int32_t*)a[10], (int32_t*)a[11], (const int32_t*)a[12], (int32_t*)a[13],
+                                (const int32_t*)a[14], (int32_t*)a[15], (int32_t*)a[16], (int64_t*)a[17],
+                                (int64_t*)a[18], (int32_t*)a[19], (int32_t*)a[20], (int32_t*)a[21],
+                                (uint32_t*)a[22], stream);
+    case MDS_PACKED_APPEND:
+      return mds_kv_append((int)a[0], (int)a[1], (int)a[2], (const void*)a[3], a[4], a[5], (const void*)a[6], a[7],
+                           a[8], (void*)a[9], (void*)a[10], (int)a[11], (int)a[12], (int)a[13], a[14], a[15], a[16],
+                           a[17], a[18], a[19], (const int64_t*)a[20], (const float*)a[21], (const float*)a[22],
+                           (uint32_t*)a[23], stream);
+    case MDS_PACKED_ATTENTION:
+      return mds_paged_attention((int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (const void*)a[5], a[6],
+                                 a[7], (const void*)a[8], (const void*)a[9], (int)a[10], (int)a[11], (int)a[12],
+                                 a[13], a[14], a[15], a[16], a[17], a[18], (const int32_t*)a[19], (int)a[20],
+                                 (int)a[21], (const int32_t*)a[22], (const int32_t*)a[23], (const int32_t*)a[24],
+                                 (int)a[25], a[26], real(a[27]), (int)a[28], (int)a[29], (const float*)a[30],
+                                 (const float*)a[31], (void*)a[32], a[33], a[34], (float*)a[35], (void*)a[36],
+                                 (size_t)a[37], stream);
+    default:
+      return mds_lm_head_fp8((int)a[0], (int)a[1], (int)a[2], (int)a[3], (const void*)a[4], a[5], (const void*)a[6],
+                             (const float*)a[7], (void*)a[8], (int)a[9], a[10], a[11], (void*)a[12],
+                             (size_t)a[13], stream);
+  }
+}
+
 }  // extern "C"

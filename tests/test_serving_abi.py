@@ -127,3 +127,28 @@ def test_unknown_attribute_still_raises():
     with pytest.raises(AttributeError):
         mds.no_such_operator
     assert callable(mds.paged_attention)
+
+
+def _pack(args):
+    import struct
+    return b"".join(struct.pack("d" if isinstance(x, float) else "q", 0 if x is None else x) for x in args)
+
+
+@pytest.mark.parametrize("name,make,bad", [("mds_kv_page_tables", _tables, dict(page_size=24)),
+                                           ("mds_kv_append", _append, dict(D=20)),
+                                           ("mds_paged_attention", _attend, dict(D=96)),
+                                           ("mds_lm_head_fp8", _head, dict(H=100))])
+def test_packed_calls_refuse_as_the_calls_do(lib, name, make, bad):
+    call = ["mds_kv_page_tables", "mds_kv_append", "mds_paged_attention", "mds_lm_head_fp8"].index(name)
+    args = make(**bad)
+    rc = getattr(lib, name)(*args)
+    message = lib.mds_last_error()
+    n = len(args) - 1
+    assert rc < 0 and lib.mds_call_packed(call, _pack(args[:-1]), n, None) == rc
+    assert lib.mds_last_error() == message
+    assert lib.mds_call_packed(call, _pack(args[:-1]), n - 1, None) == -1
+    assert lib.mds_call_packed(call, _pack(args), n + 1, None) == -1
+    assert lib.mds_call_packed(call, _pack([1 << 40] + args[1:-1]), n, None) == -1
+    assert lib.mds_call_packed(9, _pack(args[:-1]), n, None) == -1
+    assert lib.mds_call_packed(call, None, n, None) == -1
+    assert b"NULL" in lib.mds_last_error()
