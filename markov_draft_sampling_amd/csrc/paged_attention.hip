@@ -47,6 +47,8 @@
 // 2048 prompt tokens over 14336 keys 498 us, 1.01 PFLOP/s, bound by the vector
 // unit (the exponentials) and the matrix cores in turn; one token over 1037
 // keys 9.6 us, two launches' latency.
+#include <type_traits>
+
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -700,13 +702,13 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
 }
 
 // Joins the chunks of a row: o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c. Four groups of 16 lanes take the chunks in
-// turn, four of them in flight each, with a running maximum of their own, and are joined at the end.
+// turn, up to four of them in flight each, with a running maximum of their own, and are joined at the end.
 template <int D, int ROWS>
 __device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, int row, int h) {
   const int lane = threadIdx.x & 63;
   const size_t step = (size_t)a.tiles * a.Hkv * ROWS;
   const size_t pr = ((size_t)t.at * a.Hkv + h) * ROWS + row;
-  constexpr int NC = D / 16, NL = 4;
+  constexpr int NC = D / 16;
   const int g = lane >> 4, od = (lane & 15) * NC;
   float M = -INFINITY, L = 0.0f, o[NC];
 #pragma unroll
@@ -718,8 +720,8 @@ __device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, 
 #pragma unroll
     for (int e = 0; e < NC; ++e) o[e] *= f;
   };
-#pragma nounroll
-  for (int c0 = 0; c0 < t.chunks; c0 += 4 * NL) {
+  auto take = [&](auto in_flight, int c0) {
+    constexpr int NL = decltype(in_flight)::value;
     float2 ml[NL];
     floatx4 x[NL][NC / 4];
 #pragma unroll
@@ -746,6 +748,12 @@ __device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[q * 4 + e] += none ? 0.0f : x[i][q][e] * f;
     }
+  };
+  if (t.chunks <= 4) {
+    take(std::integral_constant<int, 1>{}, 0);
+  } else {
+#pragma nounroll
+    for (int c0 = 0; c0 < t.chunks; c0 += 16) take(std::integral_constant<int, 4>{}, c0);
   }
   scale_to(fmaxf(M, fmaxf(__shfl_xor(M, 16), fmaxf(__shfl_xor(M, 32), __shfl_xor(M, 48)))));
 #pragma unroll
