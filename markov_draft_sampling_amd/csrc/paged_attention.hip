@@ -21,7 +21,7 @@
 // Few rows are bound by the cache's bytes: one row group, four key groups, a
 // work-group to a CU with 128 KB of LDS to keep reads in flight (or, over short
 // sequences of many requests, fewer key groups in two or four work-groups). Up to 64 rows
-// take two by two, a prompt's 128 rows four row groups that share every block;
+// take two by two (or by one or four), a prompt's 128 rows four row groups that share every block;
 // both with two work-groups to a CU, so that one's softmax runs beside the
 // other's products. The key groups' (m, l, o) are joined through LDS at the end.
 //
@@ -803,7 +803,9 @@ hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_
     case 321: return launch_shape<D, E4M3, 2, 1, 1, 32, 32>(a, st);
     case 322: return launch_shape<D, E4M3, 2, 1, 2, 32, 64>(a, st);
     case 324: return launch_shape<D, E4M3, 2, 1, 4, 32, 128>(a, st);
+    case 641: return launch_shape<D, E4M3, 2, 2, 1, 32, 32>(a, st);
     case 642: return launch_shape<D, E4M3, 2, 2, 2, 32, 64>(a, st);
+    case 644: return launch_shape<D, E4M3, 2, 2, 4, 32, 128>(a, st);
     default: return launch_shape<D, E4M3, 2, 4, 1, 64, 64>(a, st);
   }
 }
@@ -870,6 +872,11 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   if (chunk < 256) chunk = 256;
   long long n = (span + chunk - 1) / chunk;
   if (n < 1) n = 1;
+  // 64 rows: two key groups and two work-groups a CU, but four and one where there is no second one (512 prompt tokens
+  // over none 15.6 us to 18.1 us; more work-groups than that: 1024 tokens 35 us to 30 us), and one over short
+  // sequences of many requests (128 of 8 tokens and 64 heads over 60 keys: 26 us to 37 us)
+  if (p.rows == 64 && wgs * n <= 256) p.key_groups = 4;
+  if (p.rows == 64 && span <= 1024 && wgs >= 1024) p.key_groups = 1;
   p.chunk = (int)chunk;
   p.n_chunks = (int)n;
   // more work-groups than the CUs hold at once: the longest sequences go first, so that none starts last

@@ -338,6 +338,19 @@ def test_many_short_sequences(B, D, cache, G):
           window=0 if G == 2 else 300)
 
 
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+def test_64_row_tiles_by_work_groups(D, cache):
+    # two key groups: more work-groups than CUs; one: many requests over short sequences
+    rng = np.random.default_rng(D)
+    ctx = rng.integers(0, 300, 130).tolist()
+    chunk = rng.choice([5, 8, 0, 7], 130).tolist()
+    _case(ctx, chunk, 64, 8, D, 16, cache, seed=1, idx=True)
+    _case(ctx[:45], chunk[:45], 64, 8, D, 16, cache, seed=2, max_seq=2000, window=100)
+    _case([0, 60], [150, 77], 64, 32, D, 32, cache, seed=3, max_seq=1100)
+    _case([9, 60], [150, 77], 64, 32, D, 16, cache, seed=4, max_seq=1100, causal=False)
+    _case([900, 60], [150, 77], 64, 32, D, 16, cache, seed=5, window=400, max_q=1200, max_seq=1100)
+
+
 # guesses of the longest sequence that lead to tiles of 64 and 128 rows for prompts as short as these
 TALL = {64: 1100, 128: 600000}
 
