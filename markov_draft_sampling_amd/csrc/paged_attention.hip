@@ -825,8 +825,9 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
     return (d < r ? d : r) * Hkv;
   };
   // Rows of a tile. All of a request's rows, up to 64, so that its keys are read once; for prompts 128 where that fills
-  // the CUs twice, with the keys cut into chunks of 1024 or more, else 64 (8 key heads, 32 heads, 128 / 64 rows: 1024
-  // tokens over 4096 keys 111 / 130 us; 1024 tokens over none 36 / 29 us). Over short sequences, where the
+  // the CUs twice, with the keys cut into chunks of 1024 or more, or where 64 would more than fill them, else 64 (8 key
+  // heads, 32 heads, 128 / 64 rows: 1024 tokens over 4096 keys 111 / 130 us; 1024 tokens over none 36 / 29 us; 4 times 300
+  // tokens over 1000 keys 55 / 64 us). Over short sequences, where the
   // time is that of the longest chain of one work-group, the smallest tile that leaves every work-group its own CU
   // (128 tokens over none: 7.4 us with 16 rows, 9.7 with 32, 10.5 with 64, 13.3 with 128; 2 times 290 tokens, 4 key
   // heads, 12 heads: 12.6 us with 32, 17.0 with 16 in two rounds, 18.5 with 64).
@@ -835,7 +836,7 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   else if (most <= 32 || (span <= 1024 && work_groups(32) <= 256))
     p.rows = 32;
   else
-    p.rows = most <= 64 || work_groups(128) * (span < 2048 ? 1 : span / 1024) < 512 ? 64 : 128;
+    p.rows = most > 64 && (work_groups(64) > 512 || work_groups(128) * (span < 2048 ? 1 : span / 1024) >= 512) ? 128 : 64;
   p.per_req = direct(p.rows) * B <= by_rows(p.rows) ? (int)direct(p.rows) : 0;
   p.tiles = (int)(p.per_req ? direct(p.rows) * B : by_rows(p.rows));
   // Chunks of keys. A split costs its partials and the join's launch, so fewer tiles than CUs are cut only into as many
