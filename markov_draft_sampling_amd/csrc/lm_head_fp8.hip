@@ -112,15 +112,15 @@ __device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t rs, uint8_t* to, 
 }
 // The same as assembly, for the wide kernel, whose waits are all its own: the compiler cannot tell its many
 // copies apart and would wait for all of them before every LDS read. (m0, the LDS address, has no other use in that
-// kernel.) r: a descriptor's four words.
+// kernel; the load may read it one wait state after the scalar write at the earliest.) r: a descriptor's four words.
 template <bool ONCE>
 __device__ __forceinline__ void copy_1k_asm(u32x4 r, const uint8_t* to, int lane_off, int off) {
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)to;
   if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
                  :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
 }
 

@@ -279,9 +279,10 @@ __device__ __forceinline__ void add_nonfinite(bf16x8 v, bf16x8 inf, int key, con
 
 // 16 bytes a lane straight into LDS at `lds` (uniform) + 16 * lane, from base (uniform) + off. As assembly:
 // every wait for these copies is the kernel's own, and the compiler, which cannot tell the copies in flight
-// apart, would wait for all of them before each LDS read. (m0, the LDS address, has no other use here.)
+// apart, would wait for all of them before each LDS read. (m0, the LDS address, has no other use here; the load may read
+// it one wait state after the scalar write at the earliest.)
 __device__ __forceinline__ void copy_1k(const char* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {  // at most N of this wave's copies are still in flight
