@@ -12,15 +12,15 @@
 // the float32 total.
 //
 // The matrix is kept in tiles of 16 rows by 128 columns in operand order
-// (fp8_tile_index): a wave reads its operands as 1 KB runs, straight into
-// registers or its own part of LDS, and widens them there; which columns a
-// lane holds does not matter as long as both operands agree. The quantising
+// (fp8_tile_index): a wave copies its operands as 1 KB runs into its own part
+// of LDS and widens them in registers; which columns a lane holds does not
+// matter as long as both operands agree. The quantising
 // kernel writes the hidden rows' codes in the same order, chunk (128 columns)
 // by chunk with the rows' scales behind, so that a chunk goes into LDS as one
 // linear copy without registers, shared by the waves.
 //
 // For few rows the call is bound by the matrix's V * H bytes (7 rows, H = 4096:
-// 149 us and 5.5 TB/s at V = 200064, 26.6 us at V = 32000, 4 of them the hidden
+// 145 us and 5.7 TB/s at V = 200064, 29.4 us at V = 32000, 4 of them the hidden
 // rows' launch); at 224 rows by the matrix cores and the operand reads from LDS
 // (V = 200064: 360 us, 1.02 PFLOP/s), which is why a wave takes 64 vocabulary
 // rows: every hidden operand serves four products.
@@ -94,25 +94,16 @@ __device__ __forceinline__ void chunk_barrier() {
 }
 
 // buffer descriptor of n bytes from p (raw bytes: word 3), kept in scalar registers
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_at(const uint8_t* p, int n) {
-  const uint64_t q = (uint64_t)p;
-  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)q) |
-                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(q >> 32)) << 32;
-  return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, __builtin_amdgcn_readfirstlane(n), 0x00020000);
-}
 __device__ __forceinline__ u32x4 words_at(const uint8_t* p, int n) {
   const uint64_t q = (uint64_t)p;
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)q),
                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(q >> 32)),
                (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
 }
-// 16 bytes a lane straight into LDS
-__device__ __forceinline__ void copy_1k(__amdgpu_buffer_rsrc_t rs, uint8_t* to, int lane_off, int off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, lane_off, off, 0, 0);
-}
-// The same as assembly, for the wide kernel, whose waits are all its own: the compiler cannot tell its many
-// copies apart and would wait for all of them before every LDS read. (m0, the LDS address, has no other use in that
-// kernel; the load may read it one wait state after the scalar write at the earliest.) r: a descriptor's four words.
+// 16 bytes a lane straight into LDS, as assembly: every wait for these copies is the kernels' own, and the compiler, which
+// cannot tell the copies in flight apart, would wait for all of them before every LDS read. (m0, the LDS address, has no
+// other use in these kernels; the load may read it one wait state after the scalar write at the earliest.) r: a
+// descriptor's four words; ONCE: not kept in the caches.
 template <bool ONCE>
 __device__ __forceinline__ void copy_1k_asm(u32x4 r, const uint8_t* to, int lane_off, int off) {
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)to;
@@ -127,12 +118,12 @@ __device__ __forceinline__ void copy_1k_asm(u32x4 r, const uint8_t* to, int lane
 // acc += (sx of the row * sw) * (A times the hidden operands of 64 columns at xb, a block every 2 KB). One row
 // block after the other, operand reads one block ahead, scaling one block behind (the order is pinned: left alone
 // the compiler holds every block's sums at once).
-template <int MB, int NBW>
-__device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* sx, float sw, const bf16x8 (&A)[NBW][2],
-                                                floatx4 (&acc)[NBW][MB]) {
+template <int MB>
+__device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* sx, float sw, const bf16x8 (&A)[2],
+                                                floatx4 (&acc)[MB]) {
   u32x4 raw = *(const u32x4*)xb;
   float s = sx[0], sp = 0.0f;
-  floatx4 z[NBW], zp[NBW];
+  floatx4 z, zp;
 #pragma unroll
   for (int mb = 0; mb <= MB; ++mb) {
     u32x4 rn = raw;
@@ -143,25 +134,19 @@ __device__ __forceinline__ void scaled_products(const uint8_t* xb, const float* 
     }
     if (mb < MB) {
       const bf16x8 b0 = widen8(raw[0], raw[1]), b1 = widen8(raw[2], raw[3]);
-#pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
-        z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) z[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb][1], b1, z[nb], 0, 0, 0);
+      z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[0], b0, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+      z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[1], b1, z, 0, 0, 0);
     }
     if (mb > 0) {
       const float f = sp * sw;
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nb][mb - 1][i] = __builtin_fmaf(zp[nb][i], f, acc[nb][mb - 1][i]);
+      for (int i = 0; i < 4; ++i) acc[mb - 1][i] = __builtin_fmaf(zp[i], f, acc[mb - 1][i]);
     }
     __builtin_amdgcn_sched_barrier(0);
     raw = rn;
     sp = s;
     s = sn;
-#pragma unroll
-    for (int nb = 0; nb < NBW; ++nb) zp[nb] = z[nb];
+    zp = z;
   }
 }
 
@@ -205,98 +190,73 @@ __device__ __forceinline__ void store_logits(const LmHeadFp8Args& a, const float
   }
 }
 
-// Up to 32 hidden rows (MB 16-row blocks): four waves, each with all the rows and NBW 16-row blocks of the
-// vocabulary. Bound by the matrix, which each wave reads on its own: four chunks of it are in flight in registers,
-// four of the hidden rows in LDS.
-template <int MB, int NBW>
+// Up to 32 hidden rows (MB 16-row blocks): four waves, each with all the rows and a 16-row block of the vocabulary.
+// Bound by the matrix, of which a wave copies its own 2 KB a chunk (128 columns) into LDS; the hidden rows' chunk is
+// shared. Both stand in a ring of NST chunks, NST - 1 of them in flight, two work-groups to a CU or more (7 rows, H = 4096,
+// rings of 4 / 6 / 7 chunks: V = 32000 29.8 / 30.8 / 31.3 us, V = 50017 44.4 / 46.3 / 47.2 us).
+//
+// What the waits count: copies alone. Every load between the first copy and the last barrier is one of copy_1k_asm's,
+// which the compiler can neither drop nor turn into another kind (a plain load counted here once became a scalar one,
+// and others of the last chunks were dropped). The matrix's scales go into LDS ahead of them.
+template <int MB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_fp8_kernel(LmHeadFp8Args a) {
-  static_assert(8 % NBW == 0, "one scale block a wave");
   constexpr int NW = 4, NST = 4;
   constexpr int kStage = fp8_stage_bytes(MB);       // a chunk's hidden rows and their scales
   constexpr int kCopy = kStage / 1024;              // 1 KB copies of it, dealt to the waves in turn
   constexpr int kQ = (kCopy + NW - 1) / NW;
-  constexpr int kLoads = 2 * NBW + 1;               // a wave's loads of a chunk of the matrix
-  // newer operations than the copies of the next chunk: its loads, and all of the chunks after it
-  constexpr int kNewer = kLoads + (NST - 2) * (kQ + kLoads);
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kStage], s_x1[kStage], s_x2[kStage], s_x3[kStage];
+  constexpr int kMine = kQ + 2;                     // copies a wave makes of a chunk, each wave as many
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[NST][kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[NST][NW][2048];
+  __shared__ float s_ws[512];  // the scales of the work-group's rows, by chunk (H <= 65536)
+  static_assert(sizeof s_x + sizeof s_w + sizeof s_ws <= 80 * 1024, "two work-groups a CU");
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15;
   const int HB = a.H >> 7, VB = (a.V + 15) >> 4;
-  const int mb0 = blockIdx.y * MB;
-  const int vb0 = (blockIdx.x * NW + w) * NBW;  // first 16-row block of this wave
+  const int vt0 = blockIdx.x * NW, vb0 = vt0 + w;  // 16-row blocks of the work-group (all in one scale block), of this wave
   const int coff = (int)((blockIdx.x * (unsigned)kStagger) % (unsigned)HB);
   auto chunk_of = [&](int c) { return c + coff >= HB ? c + coff - HB : c + coff; };
-
-  const uint8_t* wp[NBW];
+  for (int i = tid; i < HB; i += 64 * NW) s_ws[i] = a.w_scale[(size_t)min(vt0 >> 3, (a.V - 1) >> 7) * HB + i];
+  const u32x4 xrs = words_at(a.xq + (size_t)blockIdx.y * HB * kStage, HB * kStage);
+  const u32x4 wrs = words_at(a.w + (size_t)min(vb0, VB - 1) * HB * 2048, HB * 2048);  // (past the last: that again)
+  auto copy = [&](int st, int c) {
+    const int j = chunk_of(c);
 #pragma unroll
-  for (int nb = 0; nb < NBW; ++nb) wp[nb] = a.w + (size_t)min(vb0 + nb, VB - 1) * HB * 2048 + lane * 16;
-  const float* wsp = a.w_scale + (size_t)min(vb0 >> 3, (a.V - 1) >> 7) * HB;
-  // copies as buffer loads: the compiler would have the flat form wait for every load in flight
-  const __amdgpu_buffer_rsrc_t xrs = bytes_at(a.xq + (size_t)blockIdx.y * HB * kStage, HB * kStage);
-  auto copy = [&](uint8_t* buf, int c) {
+    for (int p = 0; p < 2; ++p) copy_1k_asm<true>(wrs, s_w[st][w] + p * 1024, lane * 16, j * 2048 + p * 1024);
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-      const int p = min(q * NW + w, kCopy - 1);  // every wave as many: the last piece may be copied twice
-      copy_1k(xrs, buf + p * 1024, lane * 16, chunk_of(c) * kStage + p * 1024);
+      const int p = min(q * NW + w, kCopy - 1);  // the last piece may be copied twice
+      copy_1k_asm<false>(xrs, s_x[st] + p * 1024, lane * 16, j * kStage + p * 1024);
     }
   };
-  u32x4 raw[NST][2][NBW];  // codes of 64 columns each
-  float ws[NST];
-  auto load = [&](int slot, int p, int c) {
+  floatx4 acc[1][MB];
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb)
-      raw[slot][p][nb] = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)chunk_of(c) * 2048 + p * 1024));
-  };
-  floatx4 acc[NBW][MB];
-#pragma unroll
-  for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int mb = 0; mb < MB; ++mb) acc[0][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // chunk c: hidden rows in LDS stage c % 4, matrix in register slot c % 4. At its start the copies of chunk c + 3
-  // go out; each half's registers are loaded with chunk c + 4 once they are widened.
-  auto stage_of = [&](int i) { return i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3; };
 #pragma unroll
-  for (int i = 0; i < NST; ++i) {
-    if (i < NST - 1) copy(stage_of(i), min(i, HB - 1));
-    load(i, 0, min(i, HB - 1));
-    load(i, 1, min(i, HB - 1));
-    ws[i] = wsp[chunk_of(min(i, HB - 1))];
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  // chunk 0 has landed: newer are its loads, two more chunks' copies and loads, and the last loads
-  chunk_barrier<kNewer + kLoads>();
-  auto chunk = [&](int c, int st) {
-    const uint8_t* cur = stage_of(st);
-    const float* sx = (const float*)(cur + MB * 2048) + lr;
-    copy(stage_of((st + NST - 1) % NST), min(c + NST - 1, HB - 1));  // the last chunk again at the end, never used
-    const float sw = ws[st];
+  for (int i = 0; i < NST - 1; ++i)
+    if (i < HB) copy(i, i);
+  int st = 0;
+#pragma nounroll
+  for (int c = 0; c < HB; ++c) {
+    // Chunk c has landed for all waves: of each wave's copies at most those of the NST - 2 chunks after it are in flight
+    // (near the end, where fewer were made: none). And all have read chunk c - 1, whose place is free.
+    if (c + NST - 1 <= HB)
+      chunk_barrier<(NST - 2) * kMine>();
+    else
+      chunk_barrier<0>();
+    if (c + NST - 1 < HB) copy(st == 0 ? NST - 1 : st - 1, c + NST - 1);
+    const uint8_t* cur = s_x[st];
+    const float sw = s_ws[chunk_of(c)];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      bf16x8 A[NBW][2];
-#pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) {
-        const u32x4 x = raw[st][p][nb];
-        A[nb][0] = widen8(x[0], x[1]);
-        A[nb][1] = widen8(x[2], x[3]);
-      }
-      load(st, p, min(c + NST, HB - 1));
-      if (p == 1) ws[st] = wsp[chunk_of(min(c + NST, HB - 1))];
-      __builtin_amdgcn_sched_barrier(0);
-      scaled_products<MB, NBW>(cur + p * 1024 + lane * 16, sx, sw, A, acc);
+      const u32x4 x = *(const u32x4*)(s_w[st][w] + p * 1024 + lane * 16);
+      const bf16x8 A[2] = {widen8(x[0], x[1]), widen8(x[2], x[3])};
+      scaled_products<MB>(cur + p * 1024 + lane * 16, (const float*)(cur + MB * 2048) + lr, sw, A, acc[0]);
     }
-    chunk_barrier<kNewer>();  // chunk c + 1's copies have landed
-  };
-  int c = 0;
-#pragma nounroll
-  for (; c + NST <= HB; c += NST)
-#pragma unroll
-    for (int i = 0; i < NST; ++i) chunk(c + i, i);
-#pragma unroll
-  for (int i = 0; i + 1 < NST; ++i)
-    if (c + i < HB) chunk(c + i, i);
-  store_logits<MB, NBW>(a, acc, mb0, vb0);
+    st = st + 1 == NST ? 0 : st + 1;
+  }
+  store_logits<MB, 1>(a, acc, blockIdx.y * MB, vb0);
 }
 
 // More rows: a work-group of four waves has MB 16-row blocks of them, a wave all of these and NBW vocabulary blocks of
@@ -504,11 +464,11 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(int V, int H, const u
   }
 }
 
-template <int MB, int NBW>
+template <int MB>
 hipError_t launch_mb(const LmHeadFp8Args& a, hipStream_t st) {
   const int VB = (a.V + 15) >> 4, MBt = (a.M + 15) >> 4;
-  const dim3 grid((unsigned)((VB + 4 * NBW - 1) / (4 * NBW)), (unsigned)((MBt + MB - 1) / MB));
-  hipLaunchKernelGGL((lm_head_fp8_kernel<MB, NBW>), grid, dim3(256), 0, st, a);
+  const dim3 grid((unsigned)((VB + 3) / 4), (unsigned)((MBt + MB - 1) / MB));
+  hipLaunchKernelGGL(lm_head_fp8_kernel<MB>, grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -540,10 +500,10 @@ hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (a.mb) {
-    case 1: return launch_mb<1, 1>(a, st);
+    case 1: return launch_mb<1>(a, st);
     case 2:
-      // 32 rows, H = 4096: 163 us to 172 us at V = 200064, 53 us to 57 us at V = 65536; 31 us to 29 us at V = 32000
-      return (a.V + 15) >> 4 >= kWide2 ? launch_wide<2>(a, st) : launch_mb<2, 1>(a, st);
+      // 32 rows, H = 4096, wide / few: V = 32000 32.4 / 32.1 us, 50017 45.7 / 52.4, 65536 57.7 / 58.9, 200064 164 / 162
+      return (a.V + 15) >> 4 >= kWide2 ? launch_wide<2>(a, st) : launch_mb<2>(a, st);
     case 3: return launch_wide<3>(a, st);
     case 4: return launch_wide<4>(a, st);
     case 5: return launch_wide<5>(a, st);

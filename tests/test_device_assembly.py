@@ -97,3 +97,25 @@ def test_copies_into_lds_wait_for_their_base(source, tmp_path):
                 nop = re.match(r"s_nop (\d+)", before)
                 states += int(nop.group(1)) + 1 if nop else 1
                 j -= 1
+
+
+def test_lm_head_fp8_barriers_count_nothing_but_copies(tmp_path):
+    # A wait for all but the newest N operations before a barrier holds if each of those N is one that the source counted:
+    # a copy into LDS written as assembly, of which there are as many in every chunk. A plain load may be dropped by the
+    # compiler, or become a scalar one, which the wait does not count.
+    few = 0
+    for name, code in _kernels("lm_head_fp8.hip", tmp_path).items():
+        copies = [i for i, ins in enumerate(code) if _is_copy(ins)]
+        waits = [re.search(r"vmcnt\((\d+)\)", code[i - 1]) for i, ins in enumerate(code) if ins == "s_barrier" and i]
+        counts = {int(m.group(1)) for m in waits if m}
+        if not copies:
+            continue
+        assert all(waits), name
+        for i, ins in enumerate(code):
+            if re.match(r"(buffer|global|flat|scratch)_load", ins.removeprefix("asm ")):
+                assert i < copies[0] or ins.startswith("asm ") and _is_copy(ins), (name, ins)
+        if counts - {0}:
+            few += 1
+            ring = 4  # chunks; the copies of each but the last are in the code before the loop, of one more in the loop
+            assert len(copies) % ring == 0 and counts == {0, len(copies) // ring * (ring - 2)}, (name, counts)
+    assert few == 2

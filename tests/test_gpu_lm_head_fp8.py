@@ -76,6 +76,13 @@ def test_every_row_tile_and_vocabulary_width(rows, V):
     _run(rows, 1, V, 128, seed=rows)
 
 
+@pytest.mark.parametrize("rows", [1, 7, 16, 17, 32])
+@pytest.mark.parametrize("H", [128, 256, 384, 512, 640, 768, 896, 1664])
+def test_few_rows_over_every_fill_of_the_ring(rows, H):
+    # fewer chunks of 128 columns than the ring has places, as many, and more, once and twice around
+    _run(1 if rows <= 16 else rows, rows if rows <= 16 else 1, 1021, H, seed=rows + H)
+
+
 def test_lm_head_fp8_bf16_out_strided_with_rows_left_alone():
     _run(6, 8, 1003, 256, seed=1, out_dtype="bf16", pad=5, extra=2)
     _run(6, 8, 1003, 256, seed=1, out_dtype="f32", pad=5, extra=2)
