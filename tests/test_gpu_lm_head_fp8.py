@@ -83,6 +83,39 @@ def test_few_rows_over_every_fill_of_the_ring(rows, H):
     _run(1 if rows <= 16 else rows, rows if rows <= 16 else 1, 1021, H, seed=rows + H)
 
 
+@pytest.mark.parametrize("H", [384, 640, 1024])
+@pytest.mark.parametrize("V", [33003, 65701])
+def test_wide_vocabularies_over_several_chunks(V, H):
+    # work-groups of two and of four vocabulary blocks a wave, over an odd and an even number of chunks of 128 columns;
+    # checked at the first, the last and some other vocabulary rows
+    import torch
+    import markov_draft_sampling_amd as mds
+    g = torch.Generator().manual_seed(V + H)
+    codes = torch.randint(0, 127, (V, H), generator=g, dtype=torch.uint8)  # 127 is NaN
+    codes |= torch.randint(0, 2, (V, H), generator=g, dtype=torch.uint8) << 7
+    codes = codes.view(torch.float8_e4m3fn)
+    scales = torch.rand(((V + 127) // 128, H // 128), generator=g) * 1e-3 + 1e-4
+    tiled, sd = mds.tile_lm_head_fp8(codes.cuda()), scales.cuda()
+    at = np.unique(np.concatenate([np.arange(140), np.arange(V - 140, V), np.random.default_rng(V).integers(0, V, 400)]))
+    wq = codes[torch.from_numpy(at)].float().numpy().astype(np.float64)
+    ws = scales.numpy()[at // 128]
+    x = torch.randn((224, H), generator=g).to(torch.bfloat16)
+    xq, xs = sr.quantize_blocks(x.float().numpy(), 1, 128)
+    z = a = 0
+    for j in range(H // 128):
+        c = slice(j * 128, (j + 1) * 128)
+        xj, wj = xq[:, c] * xs[:, j:j + 1].astype(np.float64), wq[:, c] * ws[:, j:j + 1].astype(np.float64)
+        z, a = z + xj @ wj.T, a + np.abs(xj) @ np.abs(wj).T
+    tol = (2 * 128 + H // 128 + 4) * 2.0 ** -24 * a + 2.0 ** -24 * np.abs(z)
+    for rows in (32, 33, 64, 112, 126, 224):
+        print(f"8-bit LM head rows {rows} V {V} H {H}", flush=True)
+        out = torch.full((rows, 1, V), 7.25, device="cuda")
+        mds.lm_head_fp8(x[:rows].cuda(), tiled, sd, out, 1)
+        got = out[:, 0].cpu().numpy()[:, at].astype(np.float64)
+        err = np.abs(got - z[:rows])
+        assert (err <= tol[:rows]).all(), (rows, np.argwhere(err > tol[:rows])[:4])
+
+
 def test_lm_head_fp8_bf16_out_strided_with_rows_left_alone():
     _run(6, 8, 1003, 256, seed=1, out_dtype="bf16", pad=5, extra=2)
     _run(6, 8, 1003, 256, seed=1, out_dtype="f32", pad=5, extra=2)
