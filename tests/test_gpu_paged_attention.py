@@ -295,6 +295,48 @@ def test_out_of_contract_device_data_is_flagged_and_stays_in_bounds():
     assert st in (0, 8)
 
 
+def test_tokens_past_max_q_len_are_flagged_and_left_alone():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(5)
+    kp = torch.randn((4, 16, 1, 64), generator=g).to(torch.bfloat16)
+    q = torch.randn((40, 1, 64), generator=g).to(torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0).cuda(), torch.full((40, 1), 7.0, device="cuda")
+    # one request of 40 rows where 1 was promised: its only tile has 16
+    ws = mds.paged_attention(q.cuda(), kp.cuda(), kp.cuda(), t([[1, 2, 3]]), t([0, 40]), t([45]), out, 1, 64, lse=lse)
+    torch.cuda.synchronize()
+    assert mds.workspace_status(ws) == 8
+    ref = sr.attention(q, kp.float(), kp.float(), np.array([[1, 2, 3]]), [0, 40], [45], 1 / 8)
+    _check(out.cpu()[:16], lse.cpu()[:16], ref, 64, 45, 16)
+    assert (out[16:] == 7.0).all() and (lse[16:] == 7.0).all()
+
+
+@pytest.mark.parametrize("ctx,chunk,Hq,Hk,D", [([0, 5, 30, 100], [8] * 4, 8, 2, 64), ([3000], [1], 32, 8, 128),
+                                               ([900, 20], [130, 40], 16, 8, 128), ([30] * 100, [2] * 100, 16, 8, 64)])
+def test_every_row_is_written_again(ctx, chunk, Hq, Hk, D):
+    # a second call writes every row and nothing else, with the same bits
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(len(ctx))
+    seq = [a + n for a, n in zip(ctx, chunk)]
+    mp = -(-max(seq) // 16)
+    kp = torch.randn((len(ctx) * mp, 16, Hk, D), generator=g).to(torch.bfloat16).cuda()
+    table = torch.arange(len(ctx) * mp, dtype=torch.int32, device="cuda").view(-1, mp)
+    T = sum(chunk)
+    q = torch.randn((T + 3, Hq, D), generator=g).to(torch.bfloat16).cuda()
+    got = []
+    ws = None
+    for fill in (7.0, -3.0):
+        out, lse = torch.full_like(q, fill), torch.full((T + 3, Hq), fill, device="cuda")
+        ws = mds.paged_attention(q, kp, kp, table, t(np.cumsum([0] + chunk)), t(seq), out, max(chunk), max(seq), lse=lse,
+                                 workspace=ws)
+        assert (out[T:] == fill).all() and (lse[T:] == fill).all()
+        got.append((out[:T], lse[:T]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 @pytest.mark.parametrize("Hq,Hk,D", [(256, 1, 64), (200, 1, 128), (64, 64, 64), (130, 2, 64)])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_many_heads(Hq, Hk, D, cache):
