@@ -498,7 +498,8 @@ int mds_debug_gumbel(int n, const uint32_t* words, float* gumbel, void* stream);
  * tables, append, attention) that the scoring of the K + 1 tokens of every
  * request runs over, and an LM head from an 8-bit matrix. Conventions as
  * above; the stream must belong to the current device, and no array may be
- * written by another stream meanwhile.
+ * written by another stream meanwhile. The stride of a dimension of one element
+ * is not looked at.
  *
  * A cache of n_pages pages holds the keys (and one more the values) of
  * page_size tokens a page, page_size a power of two in [16, 1024]: element

@@ -291,7 +291,7 @@ def lm_head_fp8(hidden, lm_head, scales, out, K, workspace=None, stream=None):
     else:
         _check_workspace(workspace, dev)
     _packed("lm_head_fp8", dev, stream,
-          (B, K, V, H, hidden.data_ptr(), hidden.stride(0) if rows > 1 else H, lm_head.data_ptr(),
+          (B, K, V, H, hidden.data_ptr(), hidden.stride(0), lm_head.data_ptr(),
            _vec(scales, _F32, ((V + 127) // 128) * (H // 128), dev, "scales"), out.data_ptr(), code, out.stride(0),
            out.stride(1), workspace.data_ptr(), workspace.numel()))
     return workspace

@@ -13,6 +13,9 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int hip_fail(hipError_t e) { return abi_fail(MDS_ERR_HIP, hipGetErrorString(e)); }
 
+// A dimension of one element is never stepped along: its stride may be anything, and counts as 0.
+int64_t step(int64_t n, int64_t stride) { return n <= 1 ? 0 : stride; }
+
 // log2 of a page size, or -1
 int page_log2(int page_size) {
   for (int s = 4; s <= 10; ++s)
@@ -180,9 +183,12 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
   if ((rc = lm_head_fp8_rows(B, K, &rows)) || (rc = check_lm_head_fp8(V, H))) return rc;
   if (!hidden || !lm_head || !scales || !out || !workspace) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (out_dtype != MDS_F32 && out_dtype != MDS_BF16) return abi_fail(MDS_ERR_INVALID_ARG, "out dtype must be MDS_F32 or MDS_BF16");
+  if (rows == 1) hidden_row_stride = H;
   if (hidden_row_stride < H || hidden_row_stride % 8)
     return abi_fail(MDS_ERR_INVALID_ARG, "hidden_row_stride must be a multiple of 8, at least H");
   if (!aligned(hidden, 16) || !aligned(lm_head, 16)) return abi_fail(MDS_ERR_INVALID_ARG, "hidden and lm_head must be 16-byte aligned");
+  out_req_stride = step(B, out_req_stride);
+  out_step_stride = step(K, out_step_stride);
   Dim dims[2] = {{B, out_req_stride}, {K, out_step_stride}};
   if (out_req_stride < 0 || out_step_stride < 0 || !disjoint(dims, V))
     return abi_fail(MDS_ERR_INVALID_ARG, "out strides make rows overlap or are shorter than V");
@@ -263,6 +269,14 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
   if (!k_pages || !v_pages || (T && (!k || !v || !slot_map)) || (a.e4m3 && (!k_scale || !v_scale)))
     return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   const int es = a.e4m3 ? 1 : 2;
+  k_page_stride = step(n_pages, k_page_stride);
+  v_page_stride = step(n_pages, v_page_stride);
+  k_pages_head_stride = step(Hkv, k_pages_head_stride);
+  v_pages_head_stride = step(Hkv, v_pages_head_stride);
+  k_token_stride = step(T, k_token_stride);
+  v_token_stride = step(T, v_token_stride);
+  k_head_stride = step(Hkv, k_head_stride);
+  v_head_stride = step(Hkv, v_head_stride);
   if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride, page_size)) ||
       (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride, page_size)))
     return rc;
@@ -333,6 +347,14 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   if (!(scale > 0.0f) || !(scale < 1e30f)) return abi_fail(MDS_ERR_INVALID_ARG, "scale must be positive and finite");
   if (causal != 0 && causal != 1) return abi_fail(MDS_ERR_INVALID_ARG, "causal must be 0 or 1");
   const int es = a.e4m3 ? 1 : 2;
+  k_page_stride = step(n_pages, k_page_stride);
+  v_page_stride = step(n_pages, v_page_stride);
+  k_pages_head_stride = step(Hkv, k_pages_head_stride);
+  v_pages_head_stride = step(Hkv, v_pages_head_stride);
+  q_token_stride = step(T, q_token_stride);
+  q_head_stride = step(Hq, q_head_stride);
+  out_token_stride = step(T, out_token_stride);
+  out_head_stride = step(Hq, out_head_stride);
   if ((rc = check_pages(k_pages, es, k_page_stride, k_slot_stride, k_pages_head_stride, page_size)) ||
       (rc = check_pages(v_pages, es, v_page_stride, v_slot_stride, v_pages_head_stride, page_size)))
     return rc;

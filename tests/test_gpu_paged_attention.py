@@ -446,6 +446,27 @@ def test_large_scores_and_a_peak_late_in_the_row():
     _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
 
 
+def test_strides_of_dimensions_of_one():
+    # one token, one head, one page: torch gives such dimensions whatever stride the view was made with
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    D = 64
+    odd = lambda x: x.as_strided(x.shape, [3 if n == 1 else s for n, s in zip(x.shape, x.stride())])  # noqa: E731
+    kv = torch.randn(1, 1, D, device="cuda").to(torch.bfloat16)
+    q = torch.randn(1, 1, D, device="cuda").to(torch.bfloat16)
+    slot = torch.tensor([5], dtype=torch.int64, device="cuda")
+    got = []
+    for view in (lambda x: x, odd):
+        pages = torch.ones(1, 16, 1, D, device="cuda", dtype=torch.bfloat16)
+        mds.kv_append(view(kv), view(kv), view(pages), view(pages.clone()), slot)
+        out = torch.zeros_like(q)
+        mds.paged_attention(view(q), view(pages), view(pages), t([[0]]), t([0, 1]), t([6]), view(out), 1, 6)
+        got.append((pages, out))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.equal(got[1][0][0, 5, 0], kv[0, 0])
+
+
 def test_offsets_past_32_bits():
     # pages whose offset passes 2^31 bytes and 2^31 elements: a strided view over a large buffer
     import torch

@@ -83,6 +83,18 @@ def test_attention_of_nothing_is_ok(lib):
     assert lib.mds_paged_attention(*_attend(T=0, q=None, out=None)) == 0
 
 
+def test_the_stride_of_a_dimension_of_one_is_not_looked_at(lib):
+    # calls that end before any device work: nothing to do, or (the last check) a workspace that is too small
+    one = dict(n_pages=1, kps=7, vps=-3)
+    assert lib.mds_kv_append(*_append(T=0, Hkv=1, k=None, v=None, slot=None, kts=3, vts=-1, khs=-5, vhs=9, kph=-2, vph=5,
+                                      **one)) == 0
+    heads = dict(Hq=1, Hkv=1, qhs=3, ohs=-7, kph=1, vph=-9)
+    assert lib.mds_paged_attention(*_attend(T=1, mq=0, qts=5, ots=-1, **heads, **one)) == 0
+    assert lib.mds_paged_attention(*_attend(T=2, mq=0, qts=5, **heads, **one)) == -2
+    assert lib.mds_lm_head_fp8(*_head(B=1, K=1, hrs=3, rs=-1, ss=7, wsb=16)) == -3
+    assert lib.mds_lm_head_fp8(*_head(B=1, K=2, hrs=3, rs=-1, wsb=16)) == -1
+
+
 def test_attention_workspace_bytes():
     n = mds.paged_attention_workspace_bytes
     assert n(1, 1, 8, 8, 128, 1, 1) >= 256
