@@ -65,7 +65,12 @@ def _on(stream, make, *args, **kw):
 
 
 def _new_workspace(nbytes, index, stream):
-    return _on(stream, torch.zeros, max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{index}")
+    """Memory for a call's partial results, with a cleared status word in front (which is all that has to be)."""
+    def make():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{index}")
+        ws[:256].zero_()
+        return ws
+    return _on(stream, make)
 
 
 def _check_workspace(ws, index):

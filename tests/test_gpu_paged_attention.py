@@ -446,6 +446,29 @@ def test_large_scores_and_a_peak_late_in_the_row():
     _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
 
 
+def test_a_new_workspace_in_used_memory_has_no_status_and_no_other_clearing():
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp = torch.randn(300, 16, 2, 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    table, qs, seq = torch.arange(300, dtype=torch.int32, device="cuda").view(1, 300), t([0, 3]), t([4000])
+    n = mds.paged_attention_workspace_bytes(3, 1, 4, 2, 64, 3, 4000)
+    want, got = torch.zeros_like(q), torch.zeros_like(q)
+    mds.paged_attention(q, kp, kp, table, qs, seq, want, 3, 4000,
+                        workspace=torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    dirty = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    mds.paged_attention(q, kp, kp, table, qs, seq, got, 3, 4000, workspace=dirty)
+    dirty.fill_(255)
+    at = dirty.data_ptr()
+    del dirty
+    again = torch.zeros_like(q)
+    ws = mds.paged_attention(q, kp, kp, table, qs, seq, again, 3, 4000)
+    assert torch.equal(got, want) and torch.equal(again, want) and mds.workspace_status(ws) == 0
+    # two key heads of one 16-row tile: rows past the request's are nobody's, and stay as the memory was
+    assert ws.data_ptr() != at or (ws == 255).any()
+
+
 def test_strides_of_dimensions_of_one():
     # one token, one head, one page: torch gives such dimensions whatever stride the view was made with
     import torch
