@@ -611,9 +611,10 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  *   out           bf16 [T, Hq, D] as q; rows behind query_start[B] are not written
  *   lse           float [T, Hq] contiguous, or NULL
  *   workspace     >= mds_paged_attention_workspace_bytes(...) of this call's
- *                 sizes (fewer tokens may need more: their keys are split),
- *                 256-byte aligned; its first word is a sticky status word (zero it
- *                 once); the rest needs no clearing
+ *                 sizes, or of no smaller T, B, max_q_len and max_seq_len with the
+ *                 same heads, D and window (one workspace serves all steps of a
+ *                 server), 256-byte aligned; its first word is a sticky status
+ *                 word (zero it once); the rest needs no clearing
  * Keys past max_pages*page_size are not seen (MDS_STATUS_BAD_INDEX); a page id
  * outside [0, n_pages) reads page 0 (MDS_STATUS_BAD_PAGE). Cache slots behind
  * a sequence's end and keys that no token of a request sees are never read.

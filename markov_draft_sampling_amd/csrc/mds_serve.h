@@ -82,6 +82,8 @@ struct AttnPlan {
   size_t part_o, part_ml, total;  // workspace offsets and size
 };
 AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window);
+// Workspace bytes of a call of these sizes or smaller ones (host only).
+size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window);
 hipError_t launch_paged_attention(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st);
 
 // ------------------------------------------------------- 8-bit LM head --

@@ -891,6 +891,33 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   return p;
 }
 
+// Bytes that are enough for attn_plan of these sizes and of all smaller ones (its workspace alone is not: fewer tokens
+// may be cut into more chunks). A plan's partials are n_chunks * tiles * Hkv * rows rows. Chunks that fill the CUs have 256
+// keys or more and leave at most 256 work-groups (up to 32 rows) or 512. Chunks that bound a work-group's length are at
+// most nine (an eighth of the keys rounds down) of 4608 * 128 / D keys or more in tiles that hold a request's rows; lower
+// tiles than that are chosen for short sequences or few work-groups, of which such chunks leave 512 at most. 128-row tiles
+// have chunks of 16384 keys.
+size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
+  const long long most = max_q_len > 0 ? (long long)max_q_len * G : G;
+  long long span = max_seq_len, rows = 0;
+  if (window > 0) span = span < (long long)window + max_q_len + 63 ? span : (long long)window + max_q_len + 63;
+  auto chunks = [&](long long keys) { return (span + keys - 1) / keys; };
+  for (int r = 16; r <= 128; r *= 2) {
+    const long long direct = (most + r - 1) / r * r * B, by_rows = (long long)T * G + (long long)r * B;
+    const long long padded = (direct < by_rows ? direct : by_rows) * Hkv;
+    long long fill = (r <= 32 ? 256 : 512) * (long long)r;
+    if (fill > padded * chunks(256)) fill = padded * chunks(256);
+    if (chunks(256) > 1 && rows < fill) rows = fill;
+    long long n = r == 128 ? chunks(16384) : chunks(4608 * 128 / D);
+    if (r < 128 && n > 9) n = 9;
+    const long long bound = n * (r == 128 ? padded : (long long)r * B * Hkv);
+    if (n > 1 && rows < bound) rows = bound;
+    if (most <= r) break;
+  }
+  const size_t o = (size_t)rows * D * 4, ml = (size_t)rows * 8;
+  return 256 + (o + 255) / 256 * 256 + (ml + 255) / 256 * 256;
+}
+
 hipError_t launch_paged_attention(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st) {
   if (a.D == 128) return a.e4m3 ? launch_d<128, true>(a, p.rows, p.key_groups, st) : launch_d<128, false>(a, p.rows, p.key_groups, st);
   return a.e4m3 ? launch_d<64, true>(a, p.rows, p.key_groups, st) : launch_d<64, false>(a, p.rows, p.key_groups, st);

@@ -446,6 +446,29 @@ def test_large_scores_and_a_peak_late_in_the_row():
     _case([700], [4], 2, 1, 128, 16, seed=8, scale=2.0, qgain=3.0)
 
 
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (128, 700)])
+def test_one_workspace_for_the_largest_step_and_smaller_ones(D, window):
+    import torch
+    import markov_draft_sampling_amd as mds
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    rng = np.random.default_rng(D)
+    T, B, Hq, Hk, mq, ms = 300, 8, 16, 4, 200, 6000
+    ws = mds.new_workspace(mds.paged_attention_workspace_bytes(T, B, Hq, Hk, D, mq, ms, window))
+    kp = torch.randn((400, 16, Hk, D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    table = t(rng.integers(0, 400, (B, 375)))
+    for chunk in ([200, 40, 8, 8, 8, 8, 8, 8], [8] * 8, [1] * 8, [1], [8], [17, 3], [130], [64, 1, 1], [1, 0, 5, 2, 2, 2, 1]):
+        for longest in (ms, 900, 300):
+            n, b = sum(chunk), len(chunk)
+            seq = [int(x) for x in rng.integers(longest // 2, longest + 1, b)]
+            q = torch.randn((n, Hq, D), device="cuda").to(torch.bfloat16)
+            args = (q, kp, kp, table[:b], t(np.cumsum([0] + chunk)), t(seq))
+            want, got = torch.zeros_like(q), torch.full_like(q, 7.0)
+            mds.paged_attention(*args, want, max(chunk), longest, window=window)
+            mds.paged_attention(*args, got, max(chunk), longest, window=window, workspace=ws)
+            assert torch.equal(got, want), (chunk, longest)
+    assert mds.workspace_status(ws) == 0
+
+
 def test_a_new_workspace_in_used_memory_has_no_status_and_no_other_clearing():
     import torch
     import markov_draft_sampling_amd as mds

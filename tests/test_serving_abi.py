@@ -106,6 +106,21 @@ def test_attention_workspace_bytes():
         n(1, 1, 8, 3, 128, 1, 64)
 
 
+def test_attention_workspace_of_the_largest_step_serves_smaller_ones():
+    import random
+    rng = random.Random(0)
+    n = mds.paged_attention_workspace_bytes
+    log = lambda hi: int(round(hi ** rng.random()))  # noqa: E731
+    # fewer tokens, whose keys are split, beside a prompt, whose keys are not
+    assert n(2048, 8, 32, 8, 128, 2048, 16384) >= n(8, 8, 32, 8, 128, 1, 16384) > 256
+    for _ in range(20000):
+        hk, g, D = log(64), rng.choice([1, 2, 3, 4, 8, 16]), rng.choice([64, 128])
+        T, B, q, s = log(20000), log(500), log(4000), log(1 << 20)
+        window = rng.choice([0, 0, log(20000)])
+        t, b, r, u = rng.randint(0, T), rng.randint(1, B), rng.randint(0, q), rng.randint(0, s)
+        assert n(t, b, hk * g, hk, D, r, u, window) <= n(T, B, hk * g, hk, D, q, s, window)
+
+
 def _head(**kw):
     a = dict(B=2, K=3, V=1000, H=256, hidden=FAKE, hrs=256, lm=FAKE, sc=FAKE, out=FAKE, dt=0, rs=3000, ss=1000, ws=FAKE,
              wsb=1 << 30, stream=None)
