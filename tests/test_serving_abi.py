@@ -179,3 +179,26 @@ def test_packed_calls_refuse_as_the_calls_do(lib, name, make, bad):
     assert lib.mds_call_packed(9, _pack(args[:-1]), n, None) == -1
     assert lib.mds_call_packed(call, None, n, None) == -1
     assert b"NULL" in lib.mds_last_error()
+
+
+def test_the_three_copies_of_a_signature_agree():
+    # the header's prototype, the binding's ctypes signature and the packed call's type string
+    import ctypes
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(mds.__file__)))
+    with open(os.path.join(root, "include", "mds.h")) as f:
+        header = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    with open(os.path.join(root, "markov_draft_sampling_amd", "csrc", "abi_serve.hip")) as f:
+        strings = re.findall(r'"([iplzf]{10,})"', f.read())
+    ctype = {"i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float}
+    calls = ["mds_kv_page_tables", "mds_kv_append", "mds_paged_attention", "mds_lm_head_fp8"]
+    assert len(strings) == len(calls)
+    for name, packed in zip(calls, strings):
+        args = re.search(name + r"\((.*?)\);", header, re.S).group(1).split(",")
+        kinds = ["p" if "*" in a else {"int": "i", "int64_t": "l", "size_t": "z", "float": "f"}[a.split()[0]] for a in args]
+        assert "".join(kinds) == packed + "p", name  # the stream is not packed
+        types = mds._SIGS[name][0]
+        assert len(types) == len(kinds), name
+        for kind, t in zip(kinds, types):
+            assert t is ctype[kind] or ctypes.sizeof(t) == ctypes.sizeof(ctype[kind]) and t._type_ == ctype[kind]._type_, name
