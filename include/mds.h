@@ -593,7 +593,7 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  *   out = sum_j exp(x_j - lse) v_j (* v_scale)
  * A token that sees no key (also: a padding request's) gets out = 0 and
  * lse = -inf. Sums and the softmax are float32, the probabilities rounded to
- * bf16 for the second product, out rounded to bf16.
+ * bf16 (within 2^-8 of each) for the second product, out rounded to bf16.
  *
  *   q             bf16 [T, Hq, D] (strides as k in mds_kv_append), D 64 or 128
  *                 (else MDS_ERR_UNSUPPORTED), Hq a multiple of Hkv
@@ -605,7 +605,8 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  *                 it may be left out, then with MDS_STATUS_BAD_INDEX; 0: the
  *                 call does nothing)
  *   max_seq_len   no sequence is longer, as a guess: it steers how the work is
- *                 cut; results do not depend on it beyond float32 rounding
+ *                 cut, and so which maximum a probability is taken against
+ *                 before it is rounded: two guesses may differ by that rounding
  *   scale         > 0 (1 / sqrt(D))
  *   k_scale, v_scale  float [Hkv], > 0, or NULL (1): MDS_E4M3 caches
  *   out           bf16 [T, Hq, D] as q; rows behind query_start[B] are not written

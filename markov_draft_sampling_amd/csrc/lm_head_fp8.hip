@@ -8,8 +8,8 @@
 // instruction, whose sums are float32: the 8-bit one, twice as fast, drops low
 // bits of its products before they are added (measured on 16 x 16 x 128 of
 // normal codes: 1.5e-5 of the result's norm off, against 9e-9 here), which
-// a float32 logit shows. Each half block of 64 columns is scaled and added to
-// the float32 total.
+// a float32 logit shows. A block's sum (of up to 32 rows: each half block's, of
+// 64 columns) is scaled and added to the float32 total.
 //
 // The matrix is kept in tiles of 16 rows by 128 columns in operand order
 // (fp8_tile_index): a wave copies its operands as 1 KB runs into its own part
@@ -22,8 +22,9 @@
 // For few rows the call is bound by the matrix's V * H bytes (7 rows, H = 4096:
 // 145 us and 5.7 TB/s at V = 200064, 29.4 us at V = 32000, 4 of them the hidden
 // rows' launch); at 224 rows by the matrix cores and the operand reads from LDS
-// (V = 200064: 360 us, 1.02 PFLOP/s), which is why a wave takes 64 vocabulary
-// rows: every hidden operand serves four products.
+// (V = 200064: 367 to 375 us, 0.98 to 1.0 PFLOP/s), which is why a wave takes 64
+// vocabulary rows: every hidden operand serves four products. (The pairs at the
+// rules below are from one run each; boxes differ by up to 8%.)
 #include "mds_device.h"
 #include "mds_serve.h"
 

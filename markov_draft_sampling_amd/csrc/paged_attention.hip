@@ -8,8 +8,10 @@
 // p = 2^(x - m), l += sum p, o += p v; when a block's maximum passes m by more
 // than 8, o and l are scaled by 2^(m - m') first (below that p stays under
 // 2^8, which costs no precision in floating point). p is rounded to bf16 for
-// the second product (relative 2^-9 each, the products' own input type); l
-// sums the unrounded p.
+// the second product (within 2^-8 of each, the products' own input type, as v
+// has; with the output's rounding 0.0020 to 0.0023 of the outputs' norm from 64
+// bits, where that rounding alone gives 0.0016 to 0.0018; a second bf16 part of p
+// would be one product more for every two); l sums the unrounded p.
 //
 // Rows. The G query heads of one key head read the same keys, so a request's
 // rows are its (token, head in group) pairs, token-major, in tiles of 16, 32,
@@ -42,11 +44,12 @@
 //
 // Measured (32 query heads, 8 key heads, D = 128, the reads of each key and
 // value once): one request of 131072 keys 105 us, 5.1 TB/s, bound by HBM; 32
-// requests of 8 tokens over 100 .. 8192 keys 129 us, 4.5 TB/s, the last CUs to
-// finish; 128 requests over an 8-bit cache 133 us, 4.3 TB/s; a chunk of
-// 2048 prompt tokens over 14336 keys 498 us, 1.01 PFLOP/s, bound by the vector
+// requests of 8 tokens over 100 .. 8192 keys 128 us, 4.5 TB/s, the last CUs to
+// finish; 128 requests over an 8-bit cache 135 us, 4.2 TB/s; a chunk of
+// 2048 prompt tokens over 14336 keys 515 us, 0.98 PFLOP/s, bound by the vector
 // unit (the exponentials) and the matrix cores in turn; one token over 1037
-// keys 9.6 us, two launches' latency.
+// keys 9.6 us, two launches' latency. (The pairs at the rules below are from one
+// run each; boxes differ by up to 8%.)
 #include <type_traits>
 
 #include "mds_device.h"
