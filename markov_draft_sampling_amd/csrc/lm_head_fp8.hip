@@ -24,7 +24,7 @@
 // rows' launch); at 224 rows by the matrix cores and the operand reads from LDS
 // (V = 200064: 367 to 375 us, 0.98 to 1.0 PFLOP/s), which is why a wave takes 64
 // vocabulary rows: every hidden operand serves four products. (The pairs at the
-// rules below are from one run each; boxes differ by up to 8%.)
+// rules below are from one run each; cards differ by up to 8%.)
 #include "mds_device.h"
 #include "mds_serve.h"
 

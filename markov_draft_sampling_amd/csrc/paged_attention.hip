@@ -49,7 +49,7 @@
 // 2048 prompt tokens over 14336 keys 515 us, 0.98 PFLOP/s, bound by the vector
 // unit (the exponentials) and the matrix cores in turn; one token over 1037
 // keys 9.6 us, two launches' latency. (The pairs at the rules below are from one
-// run each; boxes differ by up to 8%.)
+// run each; cards differ by up to 8%.)
 #include <type_traits>
 
 #include "mds_device.h"
