@@ -495,8 +495,8 @@ int mds_debug_gumbel(int n, const uint32_t* words, float* gumbel, void* stream);
 
 /* ------------------------------------------------------------------------
  * The serving operators around the loop: the paged key/value cache (page
- * tables, append, attention) that the scoring of the K + 1 tokens of every
- * request runs over, and an LM head from an 8-bit matrix. Conventions as
+ * tables, norm and rotation, append, attention) that the scoring of the K + 1
+ * tokens of every request runs over, and LM heads from 8-bit and 4-bit matrices. Conventions as
  * above; the stream must belong to the current device, and no array may be
  * written by another stream meanwhile. The stride of a dimension of one element
  * is not looked at.
@@ -582,6 +582,54 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
                   uint32_t* status, void* stream);
 
 /*
+ * mds_qk_norm_rope - the norm of queries and keys head by head and their
+ * rotation by position, for T tokens, in one pass.
+ *
+ * For each head x of D columns (query head: q_weight, key head: k_weight)
+ *   y = x * weight / sqrt(mean(x^2) + eps)      (y = x where the weight is NULL)
+ * and the R / 2 pairs of its first R columns, columns (i, i + R / 2), or
+ * (2 i, 2 i + 1) if interleaved, are turned by a = positions[t] * inv_freq[i]:
+ *   (y1, y2) -> rope_scale * (y1 cos a - y2 sin a, y2 cos a + y1 sin a)
+ * Columns from R on keep y. Float32 throughout (the sum of squares as well), a
+ * in float64, rounded once to bf16 where it is written. Scaled positions come as
+ * frequencies: linear, by another base, or by parts with rope_scale
+ * as its factor on cosine and sine.
+ *   q, k          bf16 [T, Hq, D], [T, Hkv, D] (strides as k in mds_kv_append),
+ *                 D a multiple of 16, at most 256 (else MDS_ERR_UNSUPPORTED)
+ *   R             a multiple of 16 (else MDS_ERR_UNSUPPORTED), 0 <= R <= D (0: the norm alone)
+ *   positions     int64 [T]; inv_freq double [R / 2], radians a position
+ *   q_weight, k_weight  bf16 [D], 16-byte aligned, or NULL
+ *   q_out, k_out  bf16, strides as the inputs; each may be its input itself
+ *                 (the same pointer and strides), and must not overlap anything otherwise
+ * Every row t < T is written, whatever its position. One launch; equal inputs
+ * give equal bits.
+ */
+int mds_qk_norm_rope(int T, int Hq, int Hkv, int D, int R, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const void* k, int64_t k_token_stride, int64_t k_head_stride, const int64_t* positions,
+                     const double* inv_freq, const void* q_weight, const void* k_weight, float eps, float rope_scale,
+                     int interleaved, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                     int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+
+/*
+ * mds_qk_norm_rope_append - mds_qk_norm_rope whose keys, and the values v beside
+ * them, go to the cache's pages as by mds_kv_append: the results are those of
+ * the two calls, but for 8-bit pages, whose keys are not rounded to bf16 between.
+ * Query rows are written for every token, the pages only for those with a slot
+ * (slot_map[t] < 0 skips; a slot past the cache too, with MDS_STATUS_BAD_PAGE).
+ * Arguments as for both. One launch.
+ */
+int mds_qk_norm_rope_append(int T, int Hq, int Hkv, int D, int R, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* positions,
+                            const double* inv_freq, const void* q_weight, const void* k_weight, float eps,
+                            float rope_scale, int interleaved, void* q_out, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, void* k_pages, void* v_pages, int cache_dtype, int page_size,
+                            int n_pages, int64_t k_page_stride, int64_t k_slot_stride, int64_t k_pages_head_stride,
+                            int64_t v_page_stride, int64_t v_slot_stride, int64_t v_pages_head_stride,
+                            const int64_t* slot_map, const float* k_scale, const float* v_scale, uint32_t* status,
+                            void* stream);
+
+/*
  * mds_paged_attention - attention of every request's new tokens over its cache
  * (the new tokens' own keys and values included: append them first).
  *
@@ -635,6 +683,28 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * mds_paged_attention_sinks - mds_paged_attention in which the first tokens stay
+ * visible outside the window: a token at position P sees the keys j <
+ * seq_lens[b] with j <= P if causal and, if window > 0, j > P - window or j <
+ * sinks (0 <= sinks <= 2^29). sinks = 0, and any with window = 0, is
+ * mds_paged_attention. Pages of a request of which none of its tokens sees a key
+ * are not read, nor their entries of the block table: they may
+ * have gone to others. The workspace: as there, for this call's window and sinks.
+ */
+int mds_paged_attention_sinks_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len,
+                                              int window, int sinks, size_t* out_bytes);
+int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
+                              int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
+                              int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
+                              int64_t v_pages_head_stride, const int32_t* block_table, int n_slots, int max_pages,
+                              const int32_t* idx_map, const int32_t* query_start, const int32_t* seq_lens,
+                              int max_q_len, int64_t max_seq_len, float scale, int causal, int window, int sinks,
+                              const float* k_scale, const float* v_scale, void* out, int64_t out_token_stride,
+                              int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
  * The LM head from an 8-bit matrix: lm_head [V, H] in MDS_E4M3 with one
  * float32 scale for each block of 128 rows by 128 columns, scales
  * [ceil(V / 128), H / 128] contiguous (weight = code * scale), H a multiple of
@@ -673,6 +743,48 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The LM head from a microscaled 4-bit matrix: lm_head [V, H] as e2m1 codes
+ * (bit 3 the sign; 0 .. 7: 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one scale byte s for
+ * 32 columns of a row: weight = code * 2^(s - 127), 255: NaN. H a multiple of 128,
+ * 128 <= H <= 65536, 2 <= V < 2^24. A weight past the largest bf16 value (s >= 253)
+ * counts as infinite.
+ *
+ * Row-major form (a checkpoint's): codes [V, H / 2], two a byte, the even column in
+ * the lower half; scales [V, H / 32].
+ * Tiled order: the code of (v, c) is in byte (c % 32) / 2 of the 16 bytes at
+ *   ((v / 16) * (H / 128) + c / 128) * 1024 + ((c % 128) / 32) * 256 + (v % 16) * 16
+ * of 8 * H * ceil(V / 16) bytes, its scale at
+ *   ((v / 16) * ceil(H / 512) + c / 512) * 256 + ((c % 128) / 32) * 64 + (v % 16) * 4 + (c % 512) / 128
+ * of 256 * ceil(V / 16) * ceil(H / 512) bytes (mds_lm_head_mxfp4_bytes gives both); what
+ * lies past V and H is zero.
+ *
+ * mds_tile_lm_head_mxfp4 makes it from the row-major form; mds_quantize_lm_head_mxfp4
+ * from a bf16 matrix [V, H]: s - 127 = floor(log2(max(largest magnitude of the 32, 2^-100)))
+ * - 2, code = weight / 2^(s - 127) rounded to nearest even, past 6 to 6 (the OCP
+ * microscaling formats' rule); 32 columns with an infinity or NaN get s = 255.
+ * mds_unpack_lm_head_mxfp4 gives the weights back in bf16 [V, H], which has them
+ * exactly. All matrices contiguous, 16-byte aligned and not overlapping (tiled scales
+ * 4-byte aligned, row-major ones of any alignment); one launch each.
+ */
+int mds_lm_head_mxfp4_bytes(int V, int H, size_t* code_bytes, size_t* scale_bytes);
+int mds_tile_lm_head_mxfp4(int V, int H, const void* codes, const void* scales, void* tiled, size_t tiled_bytes,
+                           void* tiled_scales, size_t tiled_scale_bytes, void* stream);
+int mds_quantize_lm_head_mxfp4(int V, int H, const void* lm_head, void* tiled, size_t tiled_bytes, void* tiled_scales,
+                               size_t tiled_scale_bytes, void* stream);
+int mds_unpack_lm_head_mxfp4(int V, int H, const void* tiled, const void* tiled_scales, void* lm_head, void* stream);
+
+/*
+ * mds_lm_head_mxfp4 - mds_draft_lm_head with the 4-bit matrix in tiled order:
+ *   out[b, k, v] = sum over c of hidden[b*K + k, c] * weight[v, c]
+ * the bf16 hidden rows as they are, products exact, sums float32. Arguments as
+ * for mds_draft_lm_head, with 1 <= K <= 64 and hidden_row_stride <= 2^22. No workspace;
+ * one launch; equal inputs give equal bits.
+ */
+int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hidden_row_stride, const void* lm_head,
+                      const void* scales, void* out, int out_dtype, int64_t out_req_stride, int64_t out_step_stride,
+                      void* stream);
+
+/*
  * mds_call_packed - one of the serving calls from an array of its arguments
  * (all but the stream, in their order, 8 bytes each: integers and pointers as
  * int64, a float as the bits of a double), for bindings in which every argument
@@ -684,6 +796,10 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
 #define MDS_PACKED_APPEND 1          /* mds_kv_append, n = 24 */
 #define MDS_PACKED_ATTENTION 2       /* mds_paged_attention, n = 38 */
 #define MDS_PACKED_LM_HEAD_FP8 3     /* mds_lm_head_fp8, n = 14 */
+#define MDS_PACKED_ATTENTION_SINKS 4 /* mds_paged_attention_sinks, n = 39 */
+#define MDS_PACKED_ROPE 5            /* mds_qk_norm_rope, n = 24 */
+#define MDS_PACKED_ROPE_APPEND 6     /* mds_qk_norm_rope_append, n = 39 */
+#define MDS_PACKED_LM_HEAD_MXFP4 7   /* mds_lm_head_mxfp4, n = 12 */
 int mds_call_packed(int call, const int64_t* args, int n, void* stream);
 
 #ifdef __cplusplus

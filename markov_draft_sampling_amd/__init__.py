@@ -22,7 +22,9 @@ __all__ = [
     "debug_noise", "debug_gumbel", "debug_top_p", "STATUS_BAD_ANCHOR", "STATUS_BAD_DRAFT", "STATUS_BAD_INDEX", "SALT_DRAFT", "SALT_ACCEPT",
     "SALT_RESAMPLE", "E4M3", "STATUS_BAD_PAGE", "STATUS_NO_PAGES", "kv_page_tables", "kv_append",
     "paged_attention_workspace_bytes", "paged_attention", "lm_head_fp8_tiled_bytes", "tile_lm_head_fp8",
-    "quantize_lm_head_fp8", "lm_head_fp8_workspace_bytes", "lm_head_fp8",
+    "quantize_lm_head_fp8", "lm_head_fp8_workspace_bytes", "lm_head_fp8", "rope_frequencies", "qk_norm_rope",
+    "qk_norm_rope_append", "lm_head_mxfp4_bytes", "tile_lm_head_mxfp4", "quantize_lm_head_mxfp4",
+    "unpack_lm_head_mxfp4", "lm_head_mxfp4",
 ]
 
 F32, BF16, E4M3 = 0, 1, 2
@@ -91,6 +93,19 @@ _SIGS = {
     "mds_quantize_lm_head_fp8": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _vp], _c_int),
     "mds_lm_head_fp8_workspace_bytes": ([_c_int] * 4 + [ctypes.POINTER(_c_sz)], _c_int),
     "mds_lm_head_fp8": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp, _c_sz, _vp], _c_int),
+    "mds_qk_norm_rope": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 2 + [_vp] * 4 + [ctypes.c_float] * 2 + [_c_int]
+                         + [_vp, _c_i64, _c_i64] * 2 + [_vp], _c_int),
+    "mds_qk_norm_rope_append": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 3 + [_vp] * 4 + [ctypes.c_float] * 2 + [_c_int]
+                                + [_vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3 + [_c_i64] * 6 + [_vp] * 5, _c_int),
+    "mds_paged_attention_sinks_workspace_bytes": ([_c_int] * 6 + [_c_i64, _c_int, _c_int, ctypes.POINTER(_c_sz)], _c_int),
+    "mds_paged_attention_sinks": ([_c_int] * 5 + [_vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3 + [_c_i64] * 6
+                                  + [_vp, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_i64, ctypes.c_float, _c_int, _c_int,
+                                     _c_int, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_sz, _vp], _c_int),
+    "mds_lm_head_mxfp4_bytes": ([_c_int, _c_int, ctypes.POINTER(_c_sz), ctypes.POINTER(_c_sz)], _c_int),
+    "mds_tile_lm_head_mxfp4": ([_c_int, _c_int, _vp, _vp, _vp, _c_sz, _vp, _c_sz, _vp], _c_int),
+    "mds_quantize_lm_head_mxfp4": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _c_sz, _vp], _c_int),
+    "mds_unpack_lm_head_mxfp4": ([_c_int, _c_int, _vp, _vp, _vp, _vp], _c_int),
+    "mds_lm_head_mxfp4": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp], _c_int),
     "mds_call_packed": ([_c_int, ctypes.c_char_p, _c_int, _vp], _c_int),
     "mds_debug_top_p": ([_c_int, _c_int, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_sz, _vp], _c_int),
 }
@@ -602,7 +617,8 @@ def debug_top_p(target, temperature, top_p):
 # the serving operators live in a module of their own, which needs torch when it is imported
 _SERVING = ("kv_page_tables", "kv_append", "paged_attention_workspace_bytes", "paged_attention",
             "lm_head_fp8_tiled_bytes", "tile_lm_head_fp8", "quantize_lm_head_fp8", "lm_head_fp8_workspace_bytes",
-            "lm_head_fp8")
+            "lm_head_fp8", "rope_frequencies", "qk_norm_rope", "qk_norm_rope_append", "lm_head_mxfp4_bytes",
+            "tile_lm_head_mxfp4", "quantize_lm_head_mxfp4", "unpack_lm_head_mxfp4", "lm_head_mxfp4")
 
 
 def __getattr__(name):

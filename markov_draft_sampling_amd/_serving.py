@@ -1,6 +1,7 @@
 """Binding of the serving operators: the paged key/value cache (page tables,
-append, attention) and the LM head from an 8-bit matrix. Argument checks and
-marshalling only, as in the package's other functions, which re-exports these.
+norm and rotation, append, attention) and the LM heads from 8-bit and 4-bit
+matrices. Argument checks and marshalling only, as in the package's other
+functions, which re-exports these.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import torch
 from . import _SIGS, BF16, E4M3, F32, MdsError, _check, _lib, _need
 
 _I32, _I64, _F32, _BF16, _E4M3 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_F64, _U8 = torch.float64, torch.uint8
 _c_sz = ctypes.c_size_t
 
 # These calls take a few microseconds on the GPU at decoding sizes, so the checks here are kept cheap: a device is
@@ -42,7 +44,8 @@ def _call(what, fn, index, stream, args):
 
 # mds_call_packed's numbers and the arguments' layout: 8 bytes each, floats as doubles
 _PACKED = {name: (i, struct.Struct("".join("d" if t is ctypes.c_float else "q" for t in _SIGS["mds_" + name][0][:-1])))
-           for i, name in enumerate(("kv_page_tables", "kv_append", "paged_attention", "lm_head_fp8"))}
+           for i, name in enumerate(("kv_page_tables", "kv_append", "paged_attention", "lm_head_fp8",
+                                       "paged_attention_sinks", "qk_norm_rope", "qk_norm_rope_append", "lm_head_mxfp4"))}
 
 
 def _packed(what, index, stream, args):
@@ -172,24 +175,112 @@ def kv_append(k, v, k_pages, v_pages, slot_map, k_scale=None, v_scale=None, stat
            _opt(k_scale, _F32, H, dev, "k_scale"), _opt(v_scale, _F32, H, dev, "v_scale"), _status(status, dev)))
 
 
-def paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window=0) -> int:
+def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
+                     device="cuda"):
+    """(inv_freq float64 [rotary_dim / 2] in radians a position, rope_scale) for qk_norm_rope.
+
+    Pair i turns by base^(-2 i / rotary_dim) a position. scaling, for contexts
+    factor times as long as those trained on: "linear" divides every frequency
+    by factor; "ntk" takes base * factor^(rotary_dim / (rotary_dim - 2)), which
+    divides the slowest one by it and keeps the fastest; "yarn" (Peng et al.,
+    "YaRN", 2023) divides the pairs that turn less than beta_slow times within
+    trained_len positions, keeps those of more than beta_fast, goes over in a
+    ramp between, and gives rope_scale = 0.1 ln(factor) + 1 (1 for the others).
+    """
+    _need(rotary_dim >= 2 and rotary_dim % 2 == 0 and base > 1.0, "rotary_dim must be even, base above 1")
+    _need(factor >= 1.0, "factor must be at least 1")
+    i = torch.arange(rotary_dim // 2, dtype=_F64)
+    if scaling == "ntk":
+        _need(rotary_dim > 2, "ntk scaling needs more than one pair")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f, rope_scale = base ** (-2.0 * i / rotary_dim), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        _need(trained_len >= 1 and beta_fast > beta_slow > 0, "yarn scaling needs trained_len and beta_fast > beta_slow > 0")
+        lo, hi = (rotary_dim * math.log(trained_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+                  for turns in (beta_fast, beta_slow))
+        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
+        ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        f, rope_scale = f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise MdsError(f"unknown scaling {scaling!r}")
+    return f.to(device), rope_scale
+
+
+def _heads(t, shape, index, what):
+    """(pointer, token stride, head stride) of bf16 [T, H, D] with a unit last stride."""
+    st = t.stride()
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or (st[2] != 1 and t.numel()):
+        raise MdsError(f"{what} must be bf16 {list(shape)} with a unit last stride on cuda:{index}")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev):
+    """What the two calls have in common: sizes and inputs up to the keys, the rest up to q_out."""
+    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [T, heads, D]")
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    half = 0 if inv_freq is None else inv_freq.numel()
+    return ((T, Hq, Hk, D, 2 * half, *_heads(q, q.shape, dev, "q"), *_heads(k, (T, Hk, D), dev, "k")),
+            (_vec(positions, _I64, T, dev, "positions"), _opt(inv_freq, _F64, half, dev, "inv_freq"),
+             _opt(q_weight, _BF16, D, dev, "q_weight"), _opt(k_weight, _BF16, D, dev, "k_weight"), eps, rope_scale,
+             1 if interleaved else 0, *_heads(q_out, q.shape, dev, "q_out")))
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 rope_scale=1.0, stream=None) -> None:
+    """Norm and rotation of queries and keys, head by head (mds_qk_norm_rope).
+
+    q, q_out bf16 [T, Hq, D], k, k_out bf16 [T, Hkv, D] (unit last stride; an
+    output may be its input); positions int64 [T]; inv_freq float64 [R / 2]
+    for the first R columns of a head, or None (no rotation); q_weight,
+    k_weight bf16 [D] or None (no norm); interleaved pairs columns (2 i, 2 i +
+    1) instead of (i, i + R / 2); rope_scale multiplies cosine and sine.
+    """
+    dev = _index(q)
+    first, rest = _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev)
+    _packed("qk_norm_rope", dev, stream, (*first, *rest, *_heads(k_out, k.shape, dev, "k_out")))
+
+
+def qk_norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pages, v_pages, slot_map, q_weight=None, k_weight=None,
+                        eps=1e-6, interleaved=False, rope_scale=1.0, k_scale=None, v_scale=None, status=None,
+                        stream=None) -> None:
+    """qk_norm_rope with the keys, and the values v beside them, written into
+    the cache (mds_qk_norm_rope_append).
+
+    q, k, positions to rope_scale as for qk_norm_rope; v bf16 [T, Hkv, D]; the
+    pages, slot_map, scales and status as for kv_append.
+    """
+    dev = _index(q)
+    (NP, P, H, D), code, kp, vp = _pages(k_pages, v_pages, dev)
+    first, rest = _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev)
+    T = first[0]
+    _need(first[2] == H and first[3] == D, "the pages must be [n_pages, page_size, Hkv, D] of the keys' heads")
+    _packed("qk_norm_rope_append", dev, stream,
+            (*first, *_heads(v, k.shape, dev, "v"), *rest, k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, kp[0],
+             kp[1], kp[2], vp[0], vp[1], vp[2], _vec(slot_map, _I64, T, dev, "slot_map"),
+             _opt(k_scale, _F32, H, dev, "k_scale"), _opt(v_scale, _F32, H, dev, "v_scale"), _status(status, dev)))
+
+
+def paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window=0, sinks=0) -> int:
     out = _c_sz()
-    _check(_lib().mds_paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window,
-                                                      ctypes.byref(out)), "paged_attention_workspace_bytes")
+    _check(_lib().mds_paged_attention_sinks_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window, sinks,
+                                                            ctypes.byref(out)), "paged_attention_workspace_bytes")
     return out.value
 
 
 def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len, max_seq_len, scale=None,
                     causal=True, window=0, idx_map=None, k_scale=None, v_scale=None, lse=None, workspace=None,
-                    stream=None):
-    """Attention of every request's new tokens over its paged cache (mds_paged_attention).
+                    stream=None, sinks=0):
+    """Attention of every request's new tokens over its paged cache (mds_paged_attention, mds_paged_attention_sinks).
 
     q, out bf16 [T, Hq, D] (unit last stride; D 64 or 128); the cache as for
     kv_append; block_table int32 [n_slots, max_pages]; query_start int32
     [B+1], seq_lens int32 [B]; idx_map int32 [B] or None; max_q_len bounds
     every request's new tokens, max_seq_len guesses the longest sequence;
-    scale defaults to 1/sqrt(D); lse float32 [T, Hq] or None. Returns the
-    workspace used.
+    scale defaults to 1/sqrt(D); window bounds how far back a token sees, but for
+    the first sinks tokens; lse float32 [T, Hq] or None. Returns the workspace used.
     """
     dev = _index(q)
     (NP, P, Hk, D), code, kp, vp = _pages(k_pages, v_pages, dev)
@@ -203,16 +294,15 @@ def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out
     _need(block_table.dim() == 2, "block_table must be [n_slots, max_pages]")
     N, MP = block_table.shape
     if workspace is None:
-        workspace = _new_workspace(paged_attention_workspace_bytes(T, B, Hq, Hk, D, max_q_len, max_seq_len, window),
-                                   dev, stream)
+        workspace = _new_workspace(paged_attention_workspace_bytes(T, B, Hq, Hk, D, max_q_len, max_seq_len, window, sinks), dev, stream)
     else:
         _check_workspace(workspace, dev)
-    _packed("paged_attention", dev, stream,
+    _packed("paged_attention_sinks" if sinks else "paged_attention", dev, stream,
           (T, B, Hq, Hk, D, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, kp[0], kp[1],
            kp[2], vp[0], vp[1], vp[2], _vec(block_table, _I32, N * MP, dev, "block_table"), N, MP,
            _opt(idx_map, _I32, B, dev, "idx_map"), _vec(query_start, _I32, B + 1, dev, "query_start"),
            _vec(seq_lens, _I32, B, dev, "seq_lens"), max_q_len, max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale,
-           1 if causal else 0, window, _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
+           1 if causal else 0, *((window, sinks) if sinks else (window,)), _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
            out.data_ptr(), os[0], os[1], _opt(lse, _F32, T * Hq, dev, "lse"), workspace.data_ptr(), workspace.numel()))
     return workspace
 
@@ -300,3 +390,113 @@ def lm_head_fp8(hidden, lm_head, scales, out, K, workspace=None, stream=None):
            _vec(scales, _F32, ((V + 127) // 128) * (H // 128), dev, "scales"), out.data_ptr(), code, out.stride(0),
            out.stride(1), workspace.data_ptr(), workspace.numel()))
     return workspace
+
+
+_CODES = tuple(getattr(torch, n) for n in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, n))
+_SCALES = tuple(getattr(torch, n) for n in ("uint8", "float8_e8m0fnu") if hasattr(torch, n))
+
+
+def lm_head_mxfp4_bytes(V, H):
+    """(bytes of the tiled codes, of the tiled scales) of a 4-bit matrix [V, H]."""
+    codes, scales = _c_sz(), _c_sz()
+    _check(_lib().mds_lm_head_mxfp4_bytes(V, H, ctypes.byref(codes), ctypes.byref(scales)), "lm_head_mxfp4_bytes")
+    return codes.value, scales.value
+
+
+def _mx_shapes(V, H):
+    return ((V + 15) // 16, 8 * H), ((V + 15) // 16, 256 * ((H + 511) // 512))
+
+
+def _mx_tiles(lm_head, scales, V, H, dev):
+    """The tiled codes and scales of a matrix [V, H], checked."""
+    cs, ss = _mx_shapes(V, H)
+    _need(lm_head.dtype is _U8 and lm_head.shape == cs and lm_head.is_contiguous() and lm_head.get_device() == dev,
+          "the tiled codes must be contiguous uint8 [ceil(V/16), 8 H]")
+    _need(scales.dtype is _U8 and scales.shape == ss and scales.is_contiguous() and scales.get_device() == dev,
+          "the tiled scales must be contiguous uint8 [ceil(V/16), 256 ceil(H/512)]")
+
+
+def _mx_out(out, scales, V, H, dev, stream):
+    codes, scale_bytes = lm_head_mxfp4_bytes(V, H)
+    cs, ss = _mx_shapes(V, H)
+    if out is None:
+        out = _on(stream, torch.empty, cs, dtype=_U8, device=f"cuda:{dev}")
+    if scales is None:
+        scales = _on(stream, torch.empty, ss, dtype=_U8, device=f"cuda:{dev}")
+    _mx_tiles(out, scales, V, H, dev)
+    return out, codes, scales, scale_bytes
+
+
+def tile_lm_head_mxfp4(codes, scales, out=None, out_scales=None, stream=None):
+    """Codes uint8 (or float4_e2m1fn_x2) [V, H/2] and scales uint8 (or
+    float8_e8m0fnu) [V, H/32] (a matrix that is in 4 bits already) in the tiled
+    order of mds_tile_lm_head_mxfp4: (uint8 [ceil(V/16), 8 H], uint8
+    [ceil(V/16), 256 ceil(H/512)])."""
+    _need(codes.is_cuda and codes.dtype in _CODES and codes.dim() == 2 and codes.is_contiguous(),
+          "codes must be a contiguous uint8 [V, H/2] GPU tensor")
+    dev = _index(codes)
+    V, H = codes.shape[0], 2 * codes.shape[1]
+    _need(scales.dtype in _SCALES and scales.shape == (V, H // 32) and scales.is_contiguous()
+          and scales.get_device() == dev, "scales must be a contiguous uint8 [V, H/32] beside the codes")
+    out, n, out_scales, m = _mx_out(out, out_scales, V, H, dev, stream)
+    _call("tile_lm_head_mxfp4", _lib().mds_tile_lm_head_mxfp4, dev, stream,
+          (V, H, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), n, out_scales.data_ptr(), m))
+    return out, out_scales
+
+
+def quantize_lm_head_mxfp4(lm_head, out=None, scales=None, stream=None):
+    """bf16 [V, H] -> (tiled codes, tiled scales) of tile_lm_head_mxfp4, a scale
+    for 32 columns of a row (mds_quantize_lm_head_mxfp4)."""
+    _need(lm_head.is_cuda and lm_head.dtype is _BF16 and lm_head.dim() == 2 and lm_head.is_contiguous(),
+          "lm_head must be a contiguous bf16 [V, H] GPU tensor")
+    V, H = lm_head.shape
+    dev = _index(lm_head)
+    out, n, scales, m = _mx_out(out, scales, V, H, dev, stream)
+    _call("quantize_lm_head_mxfp4", _lib().mds_quantize_lm_head_mxfp4, dev, stream,
+          (V, H, lm_head.data_ptr(), out.data_ptr(), n, scales.data_ptr(), m))
+    return out, scales
+
+
+def unpack_lm_head_mxfp4(lm_head, scales, V=None, out=None, stream=None):
+    """The weights of a tiled 4-bit matrix in bf16 [V, H], which holds them
+    exactly; V rows of it, out's or all."""
+    dev = _index(lm_head)
+    _need(lm_head.dim() == 2 and lm_head.shape[1] % 8 == 0, "the tiled codes must be [ceil(V/16), 8 H]")
+    H = lm_head.shape[1] // 8
+    if V is None:
+        V = 16 * lm_head.shape[0] if out is None else out.shape[0]
+    _mx_tiles(lm_head, scales, V, H, dev)
+    if out is None:
+        out = _on(stream, torch.empty, (V, H), dtype=_BF16, device=f"cuda:{dev}")
+    _need(out.dtype is _BF16 and out.shape == (V, H) and out.is_contiguous() and out.get_device() == dev,
+          "out must be a contiguous bf16 [V, H]")
+    _call("unpack_lm_head_mxfp4", _lib().mds_unpack_lm_head_mxfp4, dev, stream,
+          (V, H, lm_head.data_ptr(), scales.data_ptr(), out.data_ptr()))
+    return out
+
+
+def lm_head_mxfp4(hidden, lm_head, scales, out, K, stream=None) -> None:
+    """Logits from a 4-bit LM head (mds_lm_head_mxfp4).
+
+    hidden bf16 [B*K, H] (row b*K + k, unit column stride); lm_head and scales
+    from tile_lm_head_mxfp4 / quantize_lm_head_mxfp4; out float32 or bf16
+    [B, >=K, V] with unit column stride (rows k < K are written).
+    """
+    dev = _index(hidden)
+    _need(hidden.dtype is _BF16 and hidden.dim() == 2 and hidden.stride(1) == 1 and K >= 1 and hidden.shape[0] % K == 0,
+          "hidden must be bf16 [B*K, H] with unit column stride")
+    rows, H = hidden.shape
+    B = rows // K
+    _need(out.dim() == 3 and out.shape[0] == B and out.shape[1] >= K and out.stride(2) == 1 and out.get_device() == dev,
+          "out must be [B, >=K, V] with unit column stride")
+    V = out.shape[2]
+    _mx_tiles(lm_head, scales, V, H, dev)
+    if out.dtype is _F32:
+        code = F32
+    elif out.dtype is _BF16:
+        code = BF16
+    else:
+        raise MdsError(f"unsupported dtype {out.dtype}")
+    _packed("lm_head_mxfp4", dev, stream,
+            (B, K, V, H, hidden.data_ptr(), hidden.stride(0), lm_head.data_ptr(), scales.data_ptr(), out.data_ptr(), code,
+             out.stride(0), out.stride(1)))

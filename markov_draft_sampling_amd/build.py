@@ -17,8 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmds.so")
-SOURCES = ("abi.hip", "abi_serve.hip", "draft.hip", "draft_wave.hip", "draft_topk.hip", "kv_cache.hip", "lm_head.hip",
-           "lm_head_fp8.hip", "paged_attention.hip", "verify.hip", "topp.hip")
+SOURCES = ("abi.hip", "abi_layer.hip", "abi_serve.hip", "draft.hip", "draft_wave.hip", "draft_topk.hip", "kv_cache.hip", "lm_head.hip",
+           "lm_head_fp8.hip", "lm_head_mxfp4.hip", "paged_attention.hip", "rope.hip", "verify.hip", "topp.hip")
 ARCH = "gfx950"
 
 FLAGS = [

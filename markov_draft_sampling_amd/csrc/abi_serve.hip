@@ -1,127 +1,15 @@
 // extern "C" entry points of the serving operators (page tables, cache append,
 // paged attention, the 8-bit LM head): argument checks on the host, then the
 // kernels on the caller's stream. See include/mds.h for the contract.
-#include "../../include/mds.h"
-#include "mds_serve.h"
+#include "abi_checks.h"
 
-namespace {
-
+using namespace mds::abi;
 using mds::abi_fail;
 using mds::abi_ok;
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-int hip_fail(hipError_t e) { return abi_fail(MDS_ERR_HIP, hipGetErrorString(e)); }
-
-// A dimension of one element is never stepped along: its stride may be anything, and counts as 0.
-int64_t step(int64_t n, int64_t stride) { return n <= 1 ? 0 : stride; }
-
-// log2 of a page size, or -1
-int page_log2(int page_size) {
-  for (int s = 4; s <= 10; ++s)
-    if (page_size == 1 << s) return s;
-  return -1;
-}
-
-int check_page(int page_size, int n_pages, int* lg) {
-  *lg = page_log2(page_size);
-  if (page_size < 1 || n_pages < 1) return abi_fail(MDS_ERR_INVALID_ARG, "page_size and n_pages must be >= 1");
-  if (*lg < 0) return abi_fail(MDS_ERR_UNSUPPORTED, "page_size must be a power of two in [16, 1024]");
-  if ((long long)n_pages * page_size > 0x7FFFFFFFFFLL) return abi_fail(MDS_ERR_INVALID_ARG, "the cache is too large");
-  return MDS_OK;
-}
-
-// [n_pages][P][Hkv][D] pages of `es`-byte elements with a unit last stride: 16-byte aligned, strides that
-// are whole 16-byte pieces and fit the kernels' 32-bit offsets inside a page
-int check_pages(const void* p, int es, int64_t ps, int64_t ts, int64_t hs, int page_size) {
-  const int64_t e16 = 16 / es;
-  if (!aligned(p, 16) || ps % e16 || ts % e16 || hs % e16)
-    return abi_fail(MDS_ERR_UNSUPPORTED, "pages must be 16-byte aligned with strides that are multiples of 16 bytes");
-  if (ps < 0 || ts < 0 || hs < 0 || ps > (int64_t{1} << 40) || ts > (1 << 30) || hs > (int64_t{1} << 40) ||
-      ts * es * page_size >= (1LL << 31))
-    return abi_fail(MDS_ERR_INVALID_ARG, "page strides must be >= 0, and a page's slots span less than 2 GiB");
-  return MDS_OK;
-}
-
-int check_heads(int Hkv, int D) {
-  if (Hkv < 1 || Hkv > 1024) return abi_fail(MDS_ERR_INVALID_ARG, "key heads must be in [1, 1024]");
-  if (D < 1) return abi_fail(MDS_ERR_INVALID_ARG, "the head dimension must be >= 1");
-  return MDS_OK;
-}
-
-constexpr int kMaxBatch = 65535;
-constexpr int kMaxSlots = 1 << 17;
-
-int check_batch(int B, int n_slots, int max_pages, int lg, bool idx) {
-  if (B < 1 || B > kMaxBatch) return abi_fail(MDS_ERR_INVALID_ARG, "B must be in [1, 65535]");
-  if (n_slots < 1 || n_slots > kMaxSlots) return abi_fail(MDS_ERR_INVALID_ARG, "n_slots must be in [1, 2^17]");
-  if (!idx && n_slots < B) return abi_fail(MDS_ERR_INVALID_ARG, "without idx_map: n_slots >= B");
-  if (max_pages < 1 || ((long long)max_pages << lg) >= (1LL << 30))
-    return abi_fail(MDS_ERR_INVALID_ARG, "max_pages must be >= 1 and max_pages * page_size below 2^30");
-  return MDS_OK;
-}
-
-int check_cache_dtype(int dt) {
-  if (dt != MDS_BF16 && dt != MDS_E4M3) return abi_fail(MDS_ERR_INVALID_ARG, "cache dtype must be MDS_BF16 or MDS_E4M3");
-  return MDS_OK;
-}
-
-int check_attention(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len, int window) {
-  int rc;
-  if (T < 0 || T > (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "T must be in [0, 2^24]");
-  if (B < 1 || B > kMaxBatch) return abi_fail(MDS_ERR_INVALID_ARG, "B must be in [1, 65535]");
-  if ((rc = check_heads(Hkv, D))) return rc;
-  if (Hq < 1 || Hq > 1024 || Hq % Hkv) return abi_fail(MDS_ERR_INVALID_ARG, "query heads must be a multiple of key heads, at most 1024");
-  if (D != 64 && D != 128) return abi_fail(MDS_ERR_UNSUPPORTED, "the head dimension must be 64 or 128");
-  if (max_q_len < 0 || max_q_len > (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "max_q_len must be in [0, 2^24]");
-  if (max_seq_len < 0 || max_seq_len > (1LL << 30)) return abi_fail(MDS_ERR_INVALID_ARG, "max_seq_len must be in [0, 2^30]");
-  if (window < 0 || window > (1 << 30)) return abi_fail(MDS_ERR_INVALID_ARG, "window must be in [0, 2^30] (0: none)");
-  if ((long long)T * (Hq / Hkv) > 0x3FFFFFFF) return abi_fail(MDS_ERR_UNSUPPORTED, "too many query rows");
-  return MDS_OK;
-}
-
-// strides (elements) of a written array keep its elements apart: taken from the smallest stride up, each
-// must step past everything below it
-struct Dim {
-  int64_t n, stride;
-};
-template <int N>
-bool disjoint(Dim (&d)[N], int64_t inner) {
-  for (int i = 1; i < N; ++i)
-    for (int j = i; j > 0 && d[j].stride < d[j - 1].stride; --j) {
-      const Dim t = d[j];
-      d[j] = d[j - 1];
-      d[j - 1] = t;
-    }
-  int64_t extent = inner;
-  for (int i = 0; i < N; ++i) {
-    if (d[i].n <= 1) continue;
-    if (d[i].stride < extent) return false;
-    if (d[i].stride > (int64_t{1} << 62) / d[i].n) return false;
-    extent += (d[i].n - 1) * d[i].stride;
-  }
-  return true;
-}
-
-int check_lm_head_fp8(int V, int H) {
-  if (V < 2 || V >= (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "V must be in [2, 2^24)");
-  if (H < 128 || H > (1 << 16)) return abi_fail(MDS_ERR_INVALID_ARG, "H must be in [128, 65536]");
-  if (H % 128) return abi_fail(MDS_ERR_UNSUPPORTED, "H must be a multiple of 128");
-  return MDS_OK;
-}
+namespace {
 
 size_t tiled_fp8_bytes(int V, int H) { return (size_t)((V + 15) / 16) * 16 * H; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
-}
-
-int lm_head_fp8_rows(int B, int K, int* rows) {
-  if (B < 1 || B > kMaxBatch) return abi_fail(MDS_ERR_INVALID_ARG, "B must be in [1, 65535]");
-  if (K < 1 || K > 64) return abi_fail(MDS_ERR_INVALID_ARG, "K must be in [1, 64]");
-  *rows = B * K;
-  return MDS_OK;
-}
 
 size_t lm_head_fp8_ws(int rows, int H) {
   const int mb = mds::lm_head_fp8_blocks(rows);
@@ -135,7 +23,7 @@ extern "C" {
 
 int mds_lm_head_fp8_tiled_bytes(int V, int H, size_t* out_bytes) {
   int rc;
-  if ((rc = check_lm_head_fp8(V, H))) return rc;
+  if ((rc = check_lm_head_matrix(V, H))) return rc;
   if (!out_bytes) return abi_fail(MDS_ERR_INVALID_ARG, "out_bytes is NULL");
   *out_bytes = tiled_fp8_bytes(V, H);
   return abi_ok();
@@ -143,7 +31,7 @@ int mds_lm_head_fp8_tiled_bytes(int V, int H, size_t* out_bytes) {
 
 int mds_tile_lm_head_fp8(int V, int H, const void* codes, void* tiled, size_t tiled_bytes, void* stream) {
   int rc;
-  if ((rc = check_lm_head_fp8(V, H))) return rc;
+  if ((rc = check_lm_head_matrix(V, H))) return rc;
   if (!codes || !tiled) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(codes, 16) || !aligned(tiled, 16)) return abi_fail(MDS_ERR_INVALID_ARG, "codes and tiled must be 16-byte aligned");
   const size_t need = tiled_fp8_bytes(V, H);
@@ -156,7 +44,7 @@ int mds_tile_lm_head_fp8(int V, int H, const void* codes, void* tiled, size_t ti
 int mds_quantize_lm_head_fp8(int V, int H, const void* lm_head, void* tiled, size_t tiled_bytes, float* scales,
                              void* stream) {
   int rc;
-  if ((rc = check_lm_head_fp8(V, H))) return rc;
+  if ((rc = check_lm_head_matrix(V, H))) return rc;
   if (!lm_head || !tiled || !scales) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(lm_head, 16) || !aligned(tiled, 16))
     return abi_fail(MDS_ERR_INVALID_ARG, "lm_head and tiled must be 16-byte aligned");
@@ -170,7 +58,7 @@ int mds_quantize_lm_head_fp8(int V, int H, const void* lm_head, void* tiled, siz
 
 int mds_lm_head_fp8_workspace_bytes(int B, int K, int V, int H, size_t* out_bytes) {
   int rc, rows;
-  if ((rc = lm_head_fp8_rows(B, K, &rows)) || (rc = check_lm_head_fp8(V, H))) return rc;
+  if ((rc = check_lm_head_rows(B, K, &rows)) || (rc = check_lm_head_matrix(V, H))) return rc;
   if (!out_bytes) return abi_fail(MDS_ERR_INVALID_ARG, "out_bytes is NULL");
   *out_bytes = lm_head_fp8_ws(rows, H);
   return abi_ok();
@@ -180,7 +68,7 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
                     const float* scales, void* out, int out_dtype, int64_t out_req_stride, int64_t out_step_stride,
                     void* workspace, size_t workspace_bytes, void* stream) {
   int rc, rows;
-  if ((rc = lm_head_fp8_rows(B, K, &rows)) || (rc = check_lm_head_fp8(V, H))) return rc;
+  if ((rc = check_lm_head_rows(B, K, &rows)) || (rc = check_lm_head_matrix(V, H))) return rc;
   if (!hidden || !lm_head || !scales || !out || !workspace) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (out_dtype != MDS_F32 && out_dtype != MDS_BF16) return abi_fail(MDS_ERR_INVALID_ARG, "out dtype must be MDS_F32 or MDS_BF16");
   if (rows == 1) hidden_row_stride = H;
@@ -325,17 +213,28 @@ int mds_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, in
   return abi_ok();
 }
 
-int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
-                        int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
-                        int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
-                        int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
-                        int64_t v_pages_head_stride, const int32_t* block_table, int n_slots, int max_pages,
-                        const int32_t* idx_map, const int32_t* query_start, const int32_t* seq_lens, int max_q_len,
-                        int64_t max_seq_len, float scale, int causal, int window, const float* k_scale,
-                        const float* v_scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
-                        void* workspace, size_t workspace_bytes, void* stream) {
+int mds_paged_attention_sinks_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len,
+                                              int window, int sinks, size_t* out_bytes) {
+  int rc;
+  if ((rc = check_attention(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window)) || (rc = check_sinks(sinks))) return rc;
+  if (!out_bytes) return abi_fail(MDS_ERR_INVALID_ARG, "out_bytes is NULL");
+  *out_bytes = mds::attn_workspace(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks));
+  return abi_ok();
+}
+
+int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
+                              int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
+                              int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
+                              int64_t v_pages_head_stride, const int32_t* block_table, int n_slots, int max_pages,
+                              const int32_t* idx_map, const int32_t* query_start, const int32_t* seq_lens,
+                              int max_q_len, int64_t max_seq_len, float scale, int causal, int window, int sinks,
+                              const float* k_scale, const float* v_scale, void* out, int64_t out_token_stride,
+                              int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream) {
   int rc;
   mds::PagedAttnArgs a{};
+  if ((rc = check_sinks(sinks))) return rc;
   if ((rc = check_attention(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window)) ||
       (rc = check_cache_dtype(cache_dtype)) || (rc = check_page(page_size, n_pages, &a.page_log2)) ||
       (rc = check_batch(B, n_slots, max_pages, a.page_log2, idx_map != nullptr)))
@@ -366,7 +265,8 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
     return abi_fail(MDS_ERR_INVALID_ARG, "strides must be >= 0, and those of out keep its rows apart");
   if (!aligned(workspace, 256)) return abi_fail(MDS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (T == 0 || max_q_len == 0) return abi_ok();
-  const mds::AttnPlan p = mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, window);
+  const mds::AttnPlan p =
+      mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks));
   if (workspace_bytes < p.total) return abi_fail(MDS_ERR_WORKSPACE, "workspace too small for paged attention");
   if ((long long)p.tiles * Hkv * p.n_chunks > 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   a.T = T;
@@ -380,6 +280,7 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   a.max_pages = max_pages;
   a.causal = causal;
   a.window = window;
+  a.sinks = window > 0 ? sinks : 0;  // without a window every key is seen anyway
   a.q = (const uint16_t*)q;
   a.q_ts = q_token_stride;
   a.q_hs = q_head_stride;
@@ -414,24 +315,33 @@ int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int
   return e == hipSuccess ? abi_ok() : hip_fail(e);
 }
 
+int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
+                        int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,
+                        int64_t k_pages_head_stride, int64_t v_page_stride, int64_t v_slot_stride,
+                        int64_t v_pages_head_stride, const int32_t* block_table, int n_slots, int max_pages,
+                        const int32_t* idx_map, const int32_t* query_start, const int32_t* seq_lens, int max_q_len,
+                        int64_t max_seq_len, float scale, int causal, int window, const float* k_scale,
+                        const float* v_scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return mds_paged_attention_sinks(T, B, Hq, Hkv, D, q, q_token_stride, q_head_stride, k_pages, v_pages, cache_dtype,
+                                   page_size, n_pages, k_page_stride, k_slot_stride, k_pages_head_stride, v_page_stride,
+                                   v_slot_stride, v_pages_head_stride, block_table, n_slots, max_pages, idx_map,
+                                   query_start, seq_lens, max_q_len, max_seq_len, scale, causal, window, 0, k_scale,
+                                   v_scale, out, out_token_stride, out_head_stride, lse, workspace, workspace_bytes,
+                                   stream);
+}
+
 int mds_call_packed(int call, const int64_t* a, int n, void* stream) {
   // the calls' argument types: i int, l int64, p pointer, z size, f float
   static const char* const kTypes[] = {"iiiiiipppippppppppppppp", "iiipllpllppiiillllllpppp",
                                        "iiiiipllppiiillllllpiipppilfiipppllppz", "iiiiplpppillpz"};
+  if (call > MDS_PACKED_LM_HEAD_FP8 && call <= MDS_PACKED_LM_HEAD_MXFP4)
+    return mds::call_packed_layer(call, a, n, stream);
   if (call < 0 || call > MDS_PACKED_LM_HEAD_FP8) return abi_fail(MDS_ERR_INVALID_ARG, "unknown call");
   if (!a) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
-  const char* t = kTypes[call];
-  for (int i = 0; i < n || t[i]; ++i) {
-    if (i >= n || !t[i]) return abi_fail(MDS_ERR_INVALID_ARG, "wrong number of arguments");
-    if ((t[i] == 'i' && a[i] != (int)a[i]) || (t[i] == 'z' && a[i] < 0))
-      return abi_fail(MDS_ERR_INVALID_ARG, "an integer is out of its type's range");
-  }
-  auto real = [](int64_t x) {
-    double d;
-    static_assert(sizeof d == sizeof x, "8 bytes");
-    __builtin_memcpy(&d, &x, sizeof d);
-    return (float)d;
-  };
+  const int rc = check_packed(kTypes[call], a, n);
+  if (rc) return rc;
   switch (call) {
     case MDS_PACKED_PAGE_TABLES:
       return mds_kv_page_tables((int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (int)a[5],
@@ -450,7 +360,7 @@ int mds_call_packed(int call, const int64_t* a, int n, void* stream) {
                                  a[7], (const void*)a[8], (const void*)a[9], (int)a[10], (int)a[11], (int)a[12],
                                  a[13], a[14], a[15], a[16], a[17], a[18], (const int32_t*)a[19], (int)a[20],
                                  (int)a[21], (const int32_t*)a[22], (const int32_t*)a[23], (const int32_t*)a[24],
-                                 (int)a[25], a[26], real(a[27]), (int)a[28], (int)a[29], (const float*)a[30],
+                                 (int)a[25], a[26], packed_real(a[27]), (int)a[28], (int)a[29], (const float*)a[30],
                                  (const float*)a[31], (void*)a[32], a[33], a[34], (float*)a[35], (void*)a[36],
                                  (size_t)a[37], stream);
     default:

@@ -1,5 +1,6 @@
-// Declarations of the serving operators (page tables, cache append, paged
-// attention, the 8-bit LM head) shared by their kernels and their entry points.
+// Declarations of the serving operators (page tables, norm and rotation, cache
+// append, paged attention, the 8-bit and 4-bit LM heads) shared by their kernels
+// and their entry points.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,8 +50,34 @@ struct KvAppendArgs {
 };
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st);
 
+struct RopeArgs {
+  int T, Hq, Hk, D, R, interleaved, page_log2, n_pages, e4m3;
+  const uint16_t* q;                 // bf16 [T][Hq][D], keys and values [T][Hk][D]
+  const uint16_t* k;
+  const uint16_t* v;                 // null without pages
+  long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+  const long long* positions;        // [T]
+  const double* inv_freq;            // [R / 2], radians a position
+  const uint16_t* q_weight;          // bf16 [D] or null: no norm
+  const uint16_t* k_weight;
+  float eps, rope_scale;
+  uint16_t* q_out;                   // may be q (and k_out k)
+  long long qo_ts, qo_hs;
+  uint16_t* k_out;                   // null with pages
+  long long ko_ts, ko_hs;
+  void* k_pages;                     // null: rows
+  void* v_pages;
+  long long ps[2], ts[2], hs[2];     // keys, values: page, token and head strides (elements)
+  const long long* slot_map;         // [T], < 0: nothing of the token goes to the pages
+  const float* k_scale;              // [Hk] (e4m3 pages)
+  const float* v_scale;
+  uint32_t* status;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
+
 struct PagedAttnArgs {
   int T, B, Hq, Hkv, G, D, page_log2, n_pages, n_slots, max_pages, e4m3, causal, window;
+  int sinks;                         // keys that every row sees beside its window (0: none, or no window)
   const uint16_t* q;                 // bf16 [T][Hq][D]
   long long q_ts, q_hs;
   const void* k_pages;
@@ -113,6 +140,26 @@ int lm_head_fp8_blocks(int M);
 hipError_t launch_lm_head_fp8(const LmHeadFp8Args& a, hipStream_t st);
 hipError_t launch_tile_fp8(int V, int H, const uint8_t* codes, uint8_t* tiled, hipStream_t st);
 hipError_t launch_quantize_fp8(int V, int H, const uint16_t* w, uint8_t* tiled, float* scales, hipStream_t st);
+
+// ------------------------------------------------------- 4-bit LM head --
+// e2m1 codes in tiles of 16 rows by 128 columns, 1 KB each, in column order for a 16-row block: the 32 codes of row r,
+// columns 32 g on, in bytes 16 (r + 16 g) .. + 15 of a tile, the lower column in a byte's lower half. Their scale is byte
+// c % 4 of word r + 16 g of the 256 bytes for tiles 4 (c / 4) .. + 3 of the row of tiles.
+struct LmHeadMxArgs {
+  int M, K, V, H;                // rows M = B*K, H a multiple of 128
+  const uint16_t* hidden;        // bf16 [M][H]
+  long long hidden_rs;
+  const uint8_t* w;              // [ceil(V / 16)][H / 128] tiles
+  const uint8_t* w_scale;        // [ceil(V / 16)][ceil(H / 512)][256]
+  void* out;
+  long long out_rs, out_ss;
+  int out_bf16, vec_out;
+};
+hipError_t launch_lm_head_mx(const LmHeadMxArgs& a, hipStream_t st);
+hipError_t launch_tile_mx(int V, int H, const uint8_t* codes, const uint8_t* scales, uint8_t* tiled, uint8_t* tiled_scales,
+                          hipStream_t st);
+hipError_t launch_quantize_mx(int V, int H, const uint16_t* w, uint8_t* tiled, uint8_t* tiled_scales, hipStream_t st);
+hipError_t launch_unpack_mx(int V, int H, const uint8_t* tiled, const uint8_t* tiled_scales, uint16_t* out, hipStream_t st);
 
 // Error reporting of the extern "C" layer: sets the thread's message, returns code.
 int abi_fail(int code, const char* msg);

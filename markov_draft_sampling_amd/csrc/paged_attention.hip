@@ -71,7 +71,10 @@ struct Tile {
   int b, slot, q0, n, r0, rows;  // request, state slot, first token, tokens, first row, rows (0: nothing to do)
   int seq, lim;                  // sequence length, and that within the block table
   int lo, hi;                    // keys that some row sees: [lo, hi)
-  int base;                      // lo rounded down to a block of 64
+  int base;                      // lo rounded down to a block of 64 (SINKS: 0)
+  // SINKS: the first s keys are seen too. Places of keys, in whose blocks and chunks the tile is worked on, are the keys'
+  // own numbers up to sb, a multiple of 64, and gap (one too) less than those from there on
+  int s, sb, gap;
   int chunks;                    // chunks with keys (at least 1)
   int at;                        // number of the tile in the batch's own order: its place in the partials
 };
@@ -121,7 +124,7 @@ __device__ __forceinline__ int nth_longest(const PagedAttnArgs& a, int n, long l
 }
 
 // c: the chunk it is wanted for
-template <int ROWS>
+template <int ROWS, bool SINKS>
 __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, int c, uint32_t& bad) {
   Tile t;
   t.rows = 0;
@@ -189,7 +192,14 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, int tile, int 
   t.hi = max(t.hi, 0);
   t.lo = min(t.lo, t.hi);
   t.base = t.lo & ~63;
-  t.chunks = min(max((t.hi - t.base + a.chunk - 1) / a.chunk, 1), a.n_chunks);
+  t.s = t.sb = t.gap = 0;
+  if constexpr (SINKS) {
+    t.s = min(a.sinks, t.hi);
+    t.sb = (t.s + 63) & ~63;
+    t.gap = max(t.base - t.sb, 0);
+    t.base = 0;
+  }
+  t.chunks = min(max((t.hi - t.gap - t.base + a.chunk - 1) / a.chunk, 1), a.n_chunks);
   return t;
 }
 
@@ -247,7 +257,7 @@ __device__ __forceinline__ bf16x8 without(bf16x8 v, bf16x8 mask) {
 // is a product of ones; key: the lane's first key, its others follow the block's order.
 template <int NB, int ND>
 __device__ __forceinline__ void add_nonfinite(bf16x8 v, bf16x8 inf, int key, const int (&mlo)[NB], const int (&mhi)[NB],
-                                              floatx4 (&O)[NB][ND], int db) {
+                                              int sinks, floatx4 (&O)[NB][ND], int db) {
   const u32x4 x = __builtin_bit_cast(u32x4, v), f = __builtin_bit_cast(u32x4, inf);
   u32x4 pos, neg;
 #pragma unroll
@@ -269,7 +279,7 @@ __device__ __forceinline__ void add_nonfinite(bf16x8 v, bf16x8 inf, int key, con
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int k = key + (e & 3) + 16 * (e >> 2);
-      seen[e] = (__bf16)(((k >= mlo[nb]) & (k < mhi[nb])) ? 1.0f : 0.0f);
+      seen[e] = (__bf16)((((k >= mlo[nb]) | (k < sinks)) & (k < mhi[nb])) ? 1.0f : 0.0f);
     }
     const floatx4 zero = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     const floatx4 np = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), seen, zero, 0, 0, 0);
@@ -308,7 +318,8 @@ struct AttnShape {
   static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
 };
 
-template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
+// SINKS: the first a.sinks keys are seen outside the window too
+template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB, bool SINKS>
 __global__ __launch_bounds__(64 * RG * KG) __attribute__((
     amdgpu_waves_per_eu(RG > 1 ? 2 : 1, RG > 1 ? 2 : 1))) void attn_kernel(
     PagedAttnArgs a) {
@@ -333,14 +344,23 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   const int c = ct / a.tiles, tile = ct - c * a.tiles;
 
   uint32_t bad = 0;
-  const Tile t = find_tile<ROWS>(a, tile, c, bad);
+  const Tile t = find_tile<ROWS, SINKS>(a, tile, c, bad);
   if (t.rows <= 0 || c >= t.chunks) {
     if (bad && tid == 0) set_status(a.status, bad);
     return;
   }
   const int c0 = t.base + c * a.chunk;
-  const int lo = max(t.lo, c0), hi = c == a.n_chunks - 1 ? t.hi : min(t.hi, c0 + a.chunk);
-  const int nblk = hi > lo ? (hi - c0 + KB - 1) / KB : 0;
+  // SINKS: lo and hi are the tile's, and end is the chunk's last place
+  const int end = c == a.n_chunks - 1 ? t.hi - t.gap : min(t.hi - t.gap, c0 + a.chunk);
+  const int lo = SINKS ? t.lo : max(t.lo, c0), hi = SINKS ? t.hi : end;
+  const int nblk = end > (SINKS ? c0 : lo) ? (end - c0 + KB - 1) / KB : 0;
+  const int sinks = SINKS ? t.s : 0;
+  auto key_at = [&](int place) { return SINKS && place >= t.sb ? place + t.gap : place; };  // (of a block, or a piece of it)
+  // Keys that a copy of the 16 keys from k on may read, [lo, hi) without SINKS. Those outside repeat the nearest inside:
+  // what lies behind a sequence's end, or in a page of which no row sees a key, is never read. Their probability is zero.
+  auto piece_lo = [&](int k) { return SINKS && k < sinks ? 0 : lo; };
+  auto piece_hi = [&](int k) { return SINKS && k < sinks && k + 16 <= lo ? sinks : hi; };
+  auto nearest = [&](int k, int of) { return min(max(k, piece_lo(of)), piece_hi(of) - 1); };
   const int nit = (nblk + KG - 1) / KG;                 // rounds; key group kg takes blocks kg, kg + KG, ..
   const int nmy = nblk > kg ? (nblk - kg + KG - 1) / KG : 0;  // of them, its own
 
@@ -393,12 +413,10 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   }
   // Page ids of the key group's blocks i0 .. i0 + NP - 1: lane NH (i - i0) + j has the page of 16-key piece j of
   // block i.
-  // Keys outside [lo, hi) repeat the nearest one inside: what lies behind a sequence's end is never read, and
-  // their probability is zero.
   int pages = 0;
   auto load_pages = [&](int i0) {
-    const int kh = c0 + (kg + KG * (i0 + lane / NH)) * KB + 16 * (lane % NH);
-    pages = trow[min(max(kh, lo), hi - 1) >> a.page_log2];
+    const int kh = key_at(c0 + (kg + KG * (i0 + lane / NH)) * KB + 16 * (lane % NH));
+    pages = trow[nearest(kh, kh) >> a.page_log2];
     if ((unsigned)pages >= (unsigned)a.n_pages) {
       pages = 0;
       bad |= kStatusBadPage;
@@ -406,20 +424,20 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   };
   auto copy_block = [&](int i, int st) {
     if (i && i % NP == 0) load_pages(i);
-    const int k0 = c0 + (kg + KG * i) * KB;
-    const bool inside = k0 >= lo && k0 + KB <= hi;
+    const int k0 = key_at(c0 + (kg + KG * i) * KB);
+    const bool inside = (k0 >= lo && k0 + KB <= hi) || (SINKS && k0 + KB <= sinks);
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
       const int p = rg + RG * m, j = p * RPI / 16;  // copy p lies in 16-key piece j
       if (NI % RG != 0 && p >= NI) break;
-      const int kc = min(max(k0 + 16 * j, lo), hi - 1);
+      const int kc = nearest(k0 + 16 * j, k0 + 16 * j);
       const int pg = __builtin_amdgcn_readlane(pages, NH * (i % NP) + j);
       const char* kp = kb_h + pg * a.k_ps + (kc & pmask) * (int)a.k_ts;
       const char* vp = vb_h + pg * a.v_ps + (kc & pmask) * (int)a.v_ts;
       uint32_t kof = ko[m], vof = vo[m];
       if (!inside) {
         const int r = (p * RPI + lrow) & 15;
-        const int d = min(max(k0 + 16 * j + r, lo), hi - 1) - kc - r;  // from the row's own place to the key copied
+        const int d = nearest(k0 + 16 * j + r, k0 + 16 * j) - kc - r;  // from the row's own place to the key copied
         kof = (uint32_t)((int)kof + d * (int)a.k_ts);
         vof = (uint32_t)((int)vof + d * (int)a.v_ts);
       }
@@ -482,7 +500,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
   };
   constexpr int NK = KB / 16;
   auto block = [&](int st, int i) {
-    const int k0 = c0 + (kg + KG * i) * KB;
+    const int k0 = key_at(c0 + (kg + KG * i) * KB);
     const unsigned char* buf = s_kv + (kg * NST + st) * kStage;
     floatx4 S[NK][NB];
 #pragma unroll
@@ -512,7 +530,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
     }
     high();
     // lane: row lr of each nb, keys k0 + 16 kb + 4 lg + i
-    const bool masked = k0 < all_lo || k0 + KB > all_hi;
+    const bool masked = (k0 < all_lo && !(SINKS && k0 + KB <= sinks)) || k0 + KB > all_hi;
     if (masked) {
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb)
@@ -521,7 +539,8 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = k0 + 16 * kb + 4 * lg + e;
-            S[kb][nb][e] = ((key >= mlo[nb]) & (key < mhi[nb])) ? S[kb][nb][e] : -INFINITY;
+            const bool late = SINKS ? (key >= mlo[nb]) | (key < sinks) : key >= mlo[nb];
+            S[kb][nb][e] = (late & (key < mhi[nb])) ? S[kb][nb][e] : -INFINITY;
           }
     }
     float top[NB];
@@ -582,7 +601,7 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
         for (int db = 0; db < ND; ++db) {
           const bf16x8 inf = nonfinite(V[db]);
           if (__any(any_bits(inf))) {
-            add_nonfinite<NB, ND>(V[db], inf, k0 + 32 * k2 + 4 * lg, mlo, mhi, O, db);
+            add_nonfinite<NB, ND>(V[db], inf, k0 + 32 * k2 + 4 * lg, mlo, mhi, sinks, O, db);
             V[db] = without(V[db], inf);
           }
         }
@@ -636,8 +655,8 @@ __global__ __launch_bounds__(64 * RG * KG) __attribute__((
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (i + NST - 1 < nmy) copy_block(i + NST - 1, st == 0 ? NST - 1 : st - 1);
       if (i < nmy) {
-        const int k0 = c0 + (kg + KG * i) * KB;
-        if (k0 < any_hi && k0 + KB > any_lo) block(st, i);  // else no row of this wave sees a key of it
+        const int k0 = key_at(c0 + (kg + KG * i) * KB);
+        if (k0 < any_hi && (k0 + KB > any_lo || (SINKS && k0 < sinks))) block(st, i);  // else no row of this wave sees a key of it
       }
       st = st + 1 == NST ? 0 : st + 1;
     }
@@ -770,10 +789,10 @@ __device__ __forceinline__ void join_row(const PagedAttnArgs& a, const Tile& t, 
   if (g == 0) store_row(a, t, row, h, od, o, M, L);
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, bool SINKS>
 __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
   uint32_t bad = 0;
-  const Tile t = find_tile<ROWS>(a, blockIdx.x / (unsigned)a.Hkv, 0, bad);  // (in the batch's own order)
+  const Tile t = find_tile<ROWS, SINKS>(a, blockIdx.x / (unsigned)a.Hkv, 0, bad);  // (in the batch's own order)
   int row = blockIdx.y * 4 + (threadIdx.x >> 6);
   if (row >= t.rows || t.chunks <= 1) return;
 #pragma nounroll
@@ -783,34 +802,35 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
   } while (row < t.rows);
 }
 
-template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB>
+template <int D, bool E4M3, bool SINKS, int NB, int RG, int KG, int KB, int LB>
 hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
   constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG, KB, LB>::kRows;
   const long long wgs = (long long)a.tiles * a.Hkv;
-  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0, st, a);
+  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB, SINKS>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0,
+                     st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
   // few tiles: a wave a row; many, most of which have nothing to join: some rows a wave
   PagedAttnArgs j = a;
   j.by_length = 0;
   const unsigned per_tile = (unsigned)(wgs >= 4096 ? 1 : wgs * (ROWS / 4) <= 4096 ? ROWS / 4 : 4096 / wgs);
-  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)wgs, per_tile), dim3(256), 0, st, j);
+  hipLaunchKernelGGL((attn_join_kernel<D, ROWS, SINKS>), dim3((unsigned)wgs, per_tile), dim3(256), 0, st, j);
   return hipGetLastError();
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool SINKS>
 hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_t st) {
   switch (rows * 10 + key_groups) {
-    case 161: return launch_shape<D, E4M3, 1, 1, 1, 32, 32>(a, st);
-    case 162: return launch_shape<D, E4M3, 1, 1, 2, 32, 64>(a, st);
-    case 164: return launch_shape<D, E4M3, 1, 1, 4, 32, 128>(a, st);
-    case 321: return launch_shape<D, E4M3, 2, 1, 1, 32, 32>(a, st);
-    case 322: return launch_shape<D, E4M3, 2, 1, 2, 32, 64>(a, st);
-    case 324: return launch_shape<D, E4M3, 2, 1, 4, 32, 128>(a, st);
-    case 641: return launch_shape<D, E4M3, 2, 2, 1, 32, 32>(a, st);
-    case 642: return launch_shape<D, E4M3, 2, 2, 2, 32, 64>(a, st);
-    case 644: return launch_shape<D, E4M3, 2, 2, 4, 32, 128>(a, st);
-    default: return launch_shape<D, E4M3, 2, 4, 1, 64, 64>(a, st);
+    case 161: return launch_shape<D, E4M3, SINKS, 1, 1, 1, 32, 32>(a, st);
+    case 162: return launch_shape<D, E4M3, SINKS, 1, 1, 2, 32, 64>(a, st);
+    case 164: return launch_shape<D, E4M3, SINKS, 1, 1, 4, 32, 128>(a, st);
+    case 321: return launch_shape<D, E4M3, SINKS, 2, 1, 1, 32, 32>(a, st);
+    case 322: return launch_shape<D, E4M3, SINKS, 2, 1, 2, 32, 64>(a, st);
+    case 324: return launch_shape<D, E4M3, SINKS, 2, 1, 4, 32, 128>(a, st);
+    case 641: return launch_shape<D, E4M3, SINKS, 2, 2, 1, 32, 32>(a, st);
+    case 642: return launch_shape<D, E4M3, SINKS, 2, 2, 2, 32, 64>(a, st);
+    case 644: return launch_shape<D, E4M3, SINKS, 2, 2, 4, 32, 128>(a, st);
+    default: return launch_shape<D, E4M3, SINKS, 2, 4, 1, 64, 64>(a, st);
   }
 }
 
@@ -921,9 +941,16 @@ size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long l
   return 256 + (o + 255) / 256 * 256 + (ml + 255) / 256 * 256;
 }
 
+template <bool SINKS>
+static hipError_t launch(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if (a.D == 128)
+    return a.e4m3 ? launch_d<128, true, SINKS>(a, p.rows, p.key_groups, st)
+                  : launch_d<128, false, SINKS>(a, p.rows, p.key_groups, st);
+  return a.e4m3 ? launch_d<64, true, SINKS>(a, p.rows, p.key_groups, st)
+                : launch_d<64, false, SINKS>(a, p.rows, p.key_groups, st);
+}
 hipError_t launch_paged_attention(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (a.D == 128) return a.e4m3 ? launch_d<128, true>(a, p.rows, p.key_groups, st) : launch_d<128, false>(a, p.rows, p.key_groups, st);
-  return a.e4m3 ? launch_d<64, true>(a, p.rows, p.key_groups, st) : launch_d<64, false>(a, p.rows, p.key_groups, st);
+  return a.sinks > 0 ? launch<true>(a, p, st) : launch<false>(a, p, st);
 }
 
 }  // namespace mds
