@@ -209,7 +209,7 @@ int mds_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, in
   int rc;
   if ((rc = check_attention(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window))) return rc;
   if (!out_bytes) return abi_fail(MDS_ERR_INVALID_ARG, "out_bytes is NULL");
-  *out_bytes = mds::attn_workspace(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, window);
+  *out_bytes = mds::attn_workspace(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, window, false);
   return abi_ok();
 }
 
@@ -218,7 +218,8 @@ int mds_paged_attention_sinks_workspace_bytes(int T, int B, int Hq, int Hkv, int
   int rc;
   if ((rc = check_attention(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window)) || (rc = check_sinks(sinks))) return rc;
   if (!out_bytes) return abi_fail(MDS_ERR_INVALID_ARG, "out_bytes is NULL");
-  *out_bytes = mds::attn_workspace(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks));
+  *out_bytes = mds::attn_workspace(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks),
+                                   window > 0 && sinks > 0);
   return abi_ok();
 }
 
@@ -265,8 +266,8 @@ int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* 
     return abi_fail(MDS_ERR_INVALID_ARG, "strides must be >= 0, and those of out keep its rows apart");
   if (!aligned(workspace, 256)) return abi_fail(MDS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (T == 0 || max_q_len == 0) return abi_ok();
-  const mds::AttnPlan p =
-      mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks));
+  const mds::AttnPlan p = mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks),
+                                         window > 0 && sinks > 0, a.e4m3);
   if (workspace_bytes < p.total) return abi_fail(MDS_ERR_WORKSPACE, "workspace too small for paged attention");
   if ((long long)p.tiles * Hkv * p.n_chunks > 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   a.T = T;

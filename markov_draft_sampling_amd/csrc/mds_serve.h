@@ -108,9 +108,11 @@ struct AttnPlan {
   bool by_length;
   size_t part_o, part_ml, total;  // workspace offsets and size
 };
-AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window);
+// sinks: first tokens are seen beside the window, which then counts them in.
+AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window, bool sinks,
+                   bool e4m3);
 // Workspace bytes of a call of these sizes or smaller ones (host only).
-size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window);
+size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window, bool sinks);
 hipError_t launch_paged_attention(const PagedAttnArgs& a, const AttnPlan& p, hipStream_t st);
 
 // ------------------------------------------------------- 8-bit LM head --

@@ -318,10 +318,9 @@ struct AttnShape {
   static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
 };
 
-// SINKS: the first a.sinks keys are seen outside the window too
-template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB, bool SINKS>
-__global__ __launch_bounds__(64 * RG * KG) __attribute__((
-    amdgpu_waves_per_eu(RG > 1 ? 2 : 1, RG > 1 ? 2 : 1))) void attn_kernel(
+// SINKS: the first a.sinks keys are seen outside the window too; EU: waves of a SIMD at once
+template <int D, bool E4M3, int NB, int RG, int KG, int KB, int LB, bool SINKS, int EU>
+__global__ __launch_bounds__(64 * RG * KG) __attribute__((amdgpu_waves_per_eu(EU, EU))) void attn_kernel(
     PagedAttnArgs a) {
   using Sh = AttnShape<D, E4M3, NB, RG, KG, KB, LB>;
   constexpr int ROWS = Sh::kRows, RB = Sh::RB, kPart = Sh::kPart, kStage = Sh::kStage, NST = Sh::NST;
@@ -802,11 +801,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedAttnArgs a) {
   } while (row < t.rows);
 }
 
-template <int D, bool E4M3, bool SINKS, int NB, int RG, int KG, int KB, int LB>
+template <int D, bool E4M3, bool SINKS, int NB, int RG, int KG, int KB, int LB, int EU = (RG > 1 ? 2 : 1)>
 hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
   constexpr int ROWS = AttnShape<D, E4M3, NB, RG, KG, KB, LB>::kRows;
   const long long wgs = (long long)a.tiles * a.Hkv;
-  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB, SINKS>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0,
+  hipLaunchKernelGGL((attn_kernel<D, E4M3, NB, RG, KG, KB, LB, SINKS, EU>), dim3((unsigned)(wgs * a.n_chunks)), dim3(64 * RG * KG), 0,
                      st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_chunks == 1) return e;
@@ -818,15 +817,30 @@ hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// With first tokens, up to 32 rows over an 8-bit cache: half the LDS and two work-groups to a CU, since a block is half as
+// long in bytes and its chain of LDS reads, widening, exponentials and products is not (8 key heads, windows over twice
+// their keys at most, against one work-group to a CU: 128 requests of one token, window 2000 58 us to 82 us, 4000 129 to
+// 146; 32 requests of 8 tokens, 4000 47 to 53; the other way 32 requests of one token, 8000 72 to 61).
 template <int D, bool E4M3, bool SINKS>
 hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_t st) {
+  if constexpr (E4M3 && SINKS) {
+    switch (rows * 10 + key_groups) {
+      case 162: return launch_shape<D, E4M3, SINKS, 1, 1, 2, 32, 32, 2>(a, st);
+      case 164: return launch_shape<D, E4M3, SINKS, 1, 1, 4, 32, 64, 2>(a, st);
+      case 322: return launch_shape<D, E4M3, SINKS, 2, 1, 2, 32, 32, 2>(a, st);
+      case 324: return launch_shape<D, E4M3, SINKS, 2, 1, 4, 32, 64, 2>(a, st);
+    }
+  } else {
+    switch (rows * 10 + key_groups) {
+      case 161: return launch_shape<D, E4M3, SINKS, 1, 1, 1, 32, 32>(a, st);
+      case 162: return launch_shape<D, E4M3, SINKS, 1, 1, 2, 32, 64>(a, st);
+      case 164: return launch_shape<D, E4M3, SINKS, 1, 1, 4, 32, 128>(a, st);
+      case 321: return launch_shape<D, E4M3, SINKS, 2, 1, 1, 32, 32>(a, st);
+      case 322: return launch_shape<D, E4M3, SINKS, 2, 1, 2, 32, 64>(a, st);
+      case 324: return launch_shape<D, E4M3, SINKS, 2, 1, 4, 32, 128>(a, st);
+    }
+  }
   switch (rows * 10 + key_groups) {
-    case 161: return launch_shape<D, E4M3, SINKS, 1, 1, 1, 32, 32>(a, st);
-    case 162: return launch_shape<D, E4M3, SINKS, 1, 1, 2, 32, 64>(a, st);
-    case 164: return launch_shape<D, E4M3, SINKS, 1, 1, 4, 32, 128>(a, st);
-    case 321: return launch_shape<D, E4M3, SINKS, 2, 1, 1, 32, 32>(a, st);
-    case 322: return launch_shape<D, E4M3, SINKS, 2, 1, 2, 32, 64>(a, st);
-    case 324: return launch_shape<D, E4M3, SINKS, 2, 1, 4, 32, 128>(a, st);
     case 641: return launch_shape<D, E4M3, SINKS, 2, 2, 1, 32, 32>(a, st);
     case 642: return launch_shape<D, E4M3, SINKS, 2, 2, 2, 32, 64>(a, st);
     case 644: return launch_shape<D, E4M3, SINKS, 2, 2, 4, 32, 128>(a, st);
@@ -836,7 +850,8 @@ hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_
 
 }  // namespace
 
-AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
+AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window, bool sinks,
+                   bool e4m3) {
   AttnPlan p;
   const long long most = (long long)max_q_len * G;  // rows of the longest request
   // Keys a tile reads at most (a window's first block starts up to 63 keys before it).
@@ -879,8 +894,21 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   // requests of one token: over 50 keys 13.5 us to 42.3 us with one key group, over 1 to 1024 keys 61 us to 77 us; 64
   // requests over 1 to 512 keys 21.5 us to 26.5 us with two; 128 over 1 to 4096 keys 243 us to 209 us).
   p.key_groups = p.rows > 64 ? 1 : p.rows > 32 ? 2 : 4;
-  if (p.rows <= 32 && span <= 1024 && wgs > 512) p.key_groups = 1;
-  if (p.rows <= 32 && span <= 512 && wgs > 256 && wgs <= 512) p.key_groups = 2;
+  if (p.rows <= 32 && !sinks) {
+    if (span <= 1024 && wgs > 512) p.key_groups = 1;
+    if (span <= 512 && wgs > 256 && wgs <= 512) p.key_groups = 2;
+  }
+  // With first tokens beside a window all sequences beyond it are as long, so the places beside a work-group matter up
+  // to longer ones (one token, 8 key heads, a window over twice its keys at most; us with one / two / four key groups:
+  // 64 requests, window 300 30 / 22 / 27, 1000 57 / 42 / 48, 4000 172 / 162 / 163; 128 requests, 300 35 / 39 / 59,
+  // 2000 165 / 164 / 166, 4000 293 / 301 / 287; over 8-bit caches, whose work-groups are two to a CU already, 128
+  // requests with two / four, 300 25 / 31, 1000 48 / 48, 2000 108 / 101).
+  if (p.rows <= 32 && sinks) {
+    if (e4m3)
+      p.key_groups = wgs > 512 && span <= 1280 ? 2 : 4;
+    else if (wgs > 256)
+      p.key_groups = wgs <= 512 ? 2 : span <= 2560 ? 1 : 4;
+  }
   long long want = wgs < 256 ? 256 / wgs : 1, cap = 16384;
   if (p.rows > 32) {
     long long twice = wgs < 512 ? 512 / wgs : 1;
@@ -894,7 +922,9 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
   long long chunk = (span + want - 1) / want;
   if (chunk > cap) chunk = cap;
   chunk = (chunk + 127) / 128 * 128;
-  if (chunk < 256) chunk = 256;
+  // (with first tokens 128 keys where every chunk then has a CU: one token, window 1000 10.3 us to 11.4 us)
+  const long long least = sinks && p.rows <= 32 && span > 256 && wgs * ((span + 127) / 128) <= 256 ? 128 : 256;
+  if (chunk < least) chunk = least;
   long long n = (span + chunk - 1) / chunk;
   if (n < 1) n = 1;
   // 64 rows: two key groups and two work-groups a CU, but four and one where there is no second one (512 prompt tokens
@@ -916,11 +946,11 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
 
 // Bytes that are enough for attn_plan of these sizes and of all smaller ones (its workspace alone is not: fewer tokens
 // may be cut into more chunks). A plan's partials are n_chunks * tiles * Hkv * rows rows. Chunks that fill the CUs have 256
-// keys or more and leave at most 256 work-groups (up to 32 rows) or 512. Chunks that bound a work-group's length are at
+// keys (128 with first tokens) or more and leave at most 256 work-groups (up to 32 rows) or 512. Chunks that bound a work-group's length are at
 // most nine (an eighth of the keys rounds down) of 4608 * 128 / D keys or more in tiles that hold a request's rows; lower
 // tiles than that are chosen for short sequences or few work-groups, of which such chunks leave 512 at most. 128-row tiles
 // have chunks of 16384 keys.
-size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window) {
+size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long long max_seq_len, int window, bool sinks) {
   const long long most = max_q_len > 0 ? (long long)max_q_len * G : G;
   long long span = max_seq_len, rows = 0;
   if (window > 0) span = span < (long long)window + max_q_len + 63 ? span : (long long)window + max_q_len + 63;
@@ -929,8 +959,9 @@ size_t attn_workspace(int T, int B, int Hkv, int G, int D, int max_q_len, long l
     const long long direct = (most + r - 1) / r * r * B, by_rows = (long long)T * G + (long long)r * B;
     const long long padded = (direct < by_rows ? direct : by_rows) * Hkv;
     long long fill = (r <= 32 ? 256 : 512) * (long long)r;
-    if (fill > padded * chunks(256)) fill = padded * chunks(256);
-    if (chunks(256) > 1 && rows < fill) rows = fill;
+    const long long most_chunks = chunks(sinks ? 128 : 256);
+    if (fill > padded * most_chunks) fill = padded * most_chunks;
+    if (most_chunks > 1 && rows < fill) rows = fill;
     long long n = r == 128 ? chunks(16384) : chunks(4608 * 128 / D);
     if (r < 128 && n > 9) n = 9;
     const long long bound = n * (r == 128 ? padded : (long long)r * B * Hkv);

@@ -188,10 +188,14 @@ def test_without_a_window_or_first_tokens_it_is_the_call_without():
     table = torch.randperm(40, generator=g).view(2, 20).int().cuda()
     call = (q, kp, vp, table, t([0, 8, 16]), t([300, 317]))
     outs = []
-    for kw in (dict(), dict(sinks=7), dict(sinks=7, window=400), dict(window=400)):
+    for kw in (dict(), dict(sinks=7), dict(window=400), dict(sinks=7, window=400)):
         outs.append(torch.zeros_like(q))
         mds.paged_attention(*call, outs[-1], 8, 317, **kw)
-    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and torch.equal(outs[0], outs[3])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    # a window that holds every key: the work may be cut another way, which moves the maximum that a probability is taken
+    # against before it is rounded: each of the two is within 2^-8 of the value and 2^-8 of sum p |v| <= max |v| off
+    r = outs[0].double()
+    assert ((outs[3].double() - r).abs() <= 2.01 * (2.0 ** -8 * r.abs() + 2.0 ** -8 * vp.abs().max().double())).all()
     a, b = torch.zeros_like(q), torch.zeros_like(q)
     mds.paged_attention(*call, a, 8, 317, window=50)
     mds.paged_attention(*call, b, 8, 317, window=50, sinks=0)
