@@ -14,6 +14,8 @@
 // Which columns a matrix instruction takes together does not matter as long as both
 // operands agree: its slice s has columns 32 g + 8 s .. + 7 of each g. Scales of
 // four tiles in a row of tiles are the bytes of a lane's word.
+#include <type_traits>
+
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -34,49 +36,83 @@ __device__ __forceinline__ bf16x8 widen(uint32_t codes, float scale) {
 // Byte i of a lane's word of scales, as the float whose exponent it is
 __device__ __forceinline__ float scale_of(uint32_t word, int i) { return __uint_as_float((word >> (8 * i) & 0xFFu) << 23); }
 
-// lane: vocabulary rows 4 lg + (0 .. 3) of 16-row block vb for hidden row lr of row block mb
-__device__ __forceinline__ void store_block(const LmHeadMxArgs& a, floatx4 z, int mb, int vb) {
-  const int lane = threadIdx.x & 63, m = mb * 16 + (lane & 15), v = vb * 16 + (lane >> 4) * 4;
-  if (m >= a.M || v >= a.V) return;
-  const int b = m / a.K, k = m - b * a.K;
-  const long long off = (long long)b * a.out_rs + (long long)k * a.out_ss + v;
-  if (a.out_bf16) {
-    uint16_t* o = (uint16_t*)a.out + off;
-    uint32_t h[4];
+// Logits go out by way of LDS, as rows of consecutive columns (four floats of padding keep rows apart in the banks): a
+// row's run of them in one piece, also where rows are not aligned and every logit is a store of its own (224 rows, V = 100003,
+// H = 1024: PLACEHOLDER).
+template <int COLS>
+constexpr int kOutStride = COLS + 4;
+
+// Where a hidden row's logits start
+__device__ __forceinline__ long long row_at(const LmHeadMxArgs& a, int m) {
+  const int b = m / a.K;
+  return (long long)b * a.out_rs + (long long)(m - b * a.K) * a.out_ss;
+}
+
+// The i-th of n threads stores its part of `rows` rows of COLS logits from column v0 on. at(r): where row r starts;
+// z(r, c): a pointer to NC logits in LDS.. their sums are the caller's.
+template <int COLS, typename At, typename Z>
+__device__ __forceinline__ void store_rows(const LmHeadMxArgs& a, int i, int n, int rows, int v0, At at, Z z) {
+  if (a.vec_out) {
+    for (int e = i; e < rows * (COLS / 4); e += n) {
+      const int r = e / (COLS / 4), c = e % (COLS / 4) * 4, v = v0 + c;
+      if (v >= a.V) continue;
+      const floatx4 x = z(r, c, std::integral_constant<int, 4>{});
+      const long long off = at(r) + v;
+      if (a.out_bf16) {
+        uint16_t* o = (uint16_t*)a.out + off;
+        uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_bits(z[i]);
-    if (a.vec_out && v + 3 < a.V) {
-      *(u32x2*)o = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-    } else {
+        for (int k = 0; k < 4; ++k) h[k] = f32_to_bf16_bits(x[k]);
+        if (v + 3 < a.V) {
+          *(u32x2*)o = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+        } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (v + i < a.V) o[i] = (uint16_t)h[i];
+          for (int k = 0; k < 4; ++k)
+            if (v + k < a.V) o[k] = (uint16_t)h[k];
+        }
+      } else {
+        float* o = (float*)a.out + off;
+        if (v + 3 < a.V) {
+          *(floatx4*)o = x;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (v + k < a.V) o[k] = x[k];
+        }
+      }
     }
   } else {
-    float* o = (float*)a.out + off;
-    if (a.vec_out && v + 3 < a.V) {
-      *(f32x4*)o = f32x4{z[0], z[1], z[2], z[3]};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (v + i < a.V) o[i] = z[i];
+    for (int e = i; e < rows * COLS; e += n) {
+      const int r = e / COLS, c = e % COLS, v = v0 + c;
+      if (v >= a.V) continue;
+      const float x = z(r, c, std::integral_constant<int, 1>{});
+      const long long off = at(r) + v;
+      if (a.out_bf16)
+        ((uint16_t*)a.out)[off] = (uint16_t)f32_to_bf16_bits(x);
+      else
+        ((float*)a.out)[off] = x;
     }
   }
 }
 
-// Few hidden rows (MB 16-row blocks): the four waves of a work-group have the same NBW vocabulary blocks and divide the
-// columns, 512 (four tiles, a word of scales) at a time; their sums are joined through LDS at the end. So a
-// hidden row is read once a work-group, no wave waits for another before the end, and both operands go from memory into
-// registers, NP tiles ahead.
-template <int MB, int NBW>
+// Few hidden rows, up to 4 NG: the four waves of a work-group have the same NBW vocabulary blocks and divide the columns,
+// 512 (four tiles, a word of scales) at a time; their sums are joined through LDS at the end. So a hidden row is read once
+// a work-group, no wave waits for another before the end, and both operands go from memory into registers, NP tiles
+// ahead. The hidden rows are read along themselves (a wave 4 rows of 256 bytes at a time: as operands, 16 bytes of
+// every row at a time, four times as many cache lines are touched) and change places in a part of LDS of the wave's own.
+template <int NG, int NBW>
 __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
-  constexpr int NP = 2;
-  __shared__ floatx4 s_z[4][NBW * MB][64];
+  constexpr int MB = (NG + 3) / 4;
+  constexpr int NP = 2;  // (three, four: 16 rows, V = 200064, H = 4096 109 and 107 us against 93: fewer waves a CU)
+  constexpr int kOut = kOutStride<NBW * 16>;
+  constexpr int kX = NG * 1024, kZ = NG * 4 * kOut * 4;  // a wave's hidden rows of a tile; in the end its sums
+  __shared__ __attribute__((aligned(16))) unsigned char s[4 * (kX > kZ ? kX : kZ)];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int HB = a.H >> 7, G = (HB + 3) >> 2, VB = (a.V + 15) >> 4;
-  const int vb0 = blockIdx.x * NBW, mb0 = blockIdx.y * MB;
+  unsigned char* s_x = s + w * kX;
+  const int vb0 = blockIdx.x * NBW;
   // the wave's tiles: words w, w + 4, .. of each row of tiles, of which only the last may be short
   const int words = G > w ? (G - w + 3) >> 2 : 0;
   const int n = words ? 4 * words - ((words - 1) * 4 + w == G - 1 ? 4 * G - HB : 0) : 0;
@@ -85,33 +121,39 @@ __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb) {
     const size_t vb = (size_t)min(vb0 + nb, VB - 1);
-    wp[nb] = a.w + vb * HB * 1024 + lane * 16;
-    sp[nb] = a.w_scale + vb * G * 256 + lane * 4;
+    wp[nb] = a.w + vb * HB * 1024;
+    sp[nb] = a.w_scale + vb * G * 256;
   }
-  const uint16_t* xp[MB];
+  const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+  // rows past the last repeat it; row r's 16-byte slot p stands at slot p ^ (r % 16)
+  const uint16_t* xp[NG];
+  uint32_t put[NG], get[MB];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) xp[mb] = a.hidden + (long long)min((mb0 + mb) * 16 + lr, a.M - 1) * a.hidden_rs + 32 * lg;
+  for (int i = 0; i < NG; ++i) {
+    const int r = 4 * i + lg;
+    xp[i] = a.hidden + (long long)min(r, a.M - 1) * a.hidden_rs + 8 * lr;
+    put[i] = r * 256 + (lr ^ (r & 15)) * 16;
+  }
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) get[mb] = min(mb * 16 + lr, NG * 4 - 1);
   floatx4 acc[NBW][MB];
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  u32x4 W[NP][NBW];
+  u32x4 W[NP][NBW], X[NP][NG];
   uint32_t S[NP][NBW];
-  bf16x8 X[NP][MB][4];
-  auto tile_of = [&](int i) { return ((i >> 2) * 4 + w) * 4 + (i & 3); };
   auto load = [&](int p, int i) {
-    const int c = tile_of(min(i, n - 1));
+    const int c = min(i, n - 1);
+    const int t = ((c >> 2) * 4 + w) * 4 + (c & 3);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) X[p][j] = *(const u32x4*)(xp[j] + t * 128);
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb) {
-      W[p][nb] = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)c * 1024));
-      S[p][nb] = *(const uint32_t*)(sp[nb] + (c >> 2) * 256);
+      W[p][nb] = __builtin_nontemporal_load((const u32x4*)(wp[nb] + (size_t)t * 1024 + lane16));
+      S[p][nb] = *(const uint32_t*)(sp[nb] + (t >> 2) * 256 + lane4);
     }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) X[p][mb][s] = *(const bf16x8*)(xp[mb] + c * 128 + 8 * s);
   };
   if (n > 0) {
 #pragma unroll
@@ -123,14 +165,22 @@ __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
         const int i = i0 + p;
         if (i < n) {
 #pragma unroll
-          for (int nb = 0; nb < NBW; ++nb) {
-            const float sc = scale_of(S[p][nb], i & 3);
+          for (int j = 0; j < NG; ++j) *(u32x4*)(s_x + put[j]) = X[p][j];
+          float sc[NBW];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const bf16x8 A = widen(W[p][nb][s], sc);
+          for (int nb = 0; nb < NBW; ++nb) sc[nb] = scale_of(S[p][nb], i & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            bf16x8 x[MB];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+              x[mb] = *(const bf16x8*)(s_x + get[mb] * 256 + ((4 * lg + k) ^ (get[mb] & 15)) * 16);
+#pragma unroll
+            for (int nb = 0; nb < NBW; ++nb) {
+              const bf16x8 A = widen(W[p][nb][k], sc[nb]);
 #pragma unroll
               for (int mb = 0; mb < MB; ++mb)
-                acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, X[p][mb][s], acc[nb][mb], 0, 0, 0);
+                acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, x[mb], acc[nb][mb], 0, 0, 0);
             }
           }
         }
@@ -138,15 +188,21 @@ __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
       }
     }
   }
+  __syncthreads();  // all waves have read their hidden rows
+  auto z_of = [&](int wave, int r, int c) { return s + wave * kZ + (r * kOut + c) * 4; };
 #pragma unroll
-  for (int nb = 0; nb < NBW; ++nb)
+  for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) s_z[w][nb * MB + mb][lane] = acc[nb][mb];
+    for (int nb = 0; nb < NBW; ++nb)
+      if (mb * 16 + lr < NG * 4) *(floatx4*)z_of(w, mb * 16 + lr, nb * 16 + lg * 4) = acc[nb][mb];
   __syncthreads();
-  for (int u = w; u < NBW * MB; u += 4) {
-    const floatx4 z = (s_z[0][u][lane] + s_z[1][u][lane]) + (s_z[2][u][lane] + s_z[3][u][lane]);
-    store_block(a, z, mb0 + u % MB, vb0 + u / MB);
-  }
+  store_rows<NBW * 16>(
+      a, threadIdx.x, 256, a.M, vb0 * 16, [&](int r) { return row_at(a, r); },
+      [&](int r, int c, auto cols) {
+        using T = typename std::conditional<decltype(cols)::value == 4, floatx4, float>::type;
+        auto part = [&](int k) { return *(const T*)z_of(k, r, c); };
+        return (part(0) + part(1)) + (part(2) + part(3));
+      });
 }
 
 // 16 bytes a lane straight into LDS at `lds` (uniform) + 16 * lane, from base (uniform) + off, as assembly: the waits for
@@ -157,15 +213,23 @@ __device__ __forceinline__ void copy_1k(const char* base, uint32_t off, uint32_t
 }
 
 // More rows: a work-group of four waves has MB 16-row blocks of them, a wave all of these and NBW vocabulary blocks of
-// its own. A tile's columns (128) at a time: the hidden rows in LDS, two of these deep and shared, 16-byte slots
-// XOR-swizzled by row; the matrix in registers, loaded one ahead. The row tiles of a vocabulary tile run on
-// the same XCD next to each other, so that the later ones find the matrix in the caches.
+// its own; two work-groups a CU. A tile's columns (128) at a time: the hidden rows in LDS, two of these deep and shared,
+// 16-byte slots XOR-swizzled by row; the matrix in registers, asked for one ahead. The row tiles of a vocabulary tile run
+// on the same XCD next to each other, so that the later ones find the matrix in the caches. (Not kept: eight waves that
+// share three stages, and runs of the vocabulary in uneven passes that fill every CU, 239 us against 223 for 224 rows,
+// V = 151936: a pass costs as much as one more block; one work-group of four waves with eight blocks a wave, 256 us.)
 template <int MB, int NBW>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_head_mx_wide_kernel(
     LmHeadMxArgs a, int v_tiles, int m_tiles) {
   constexpr int NW = 4;
   constexpr int kStage = MB * 4096;  // the hidden rows' 128 columns
-  __shared__ __attribute__((aligned(16))) unsigned char s_x[2][kStage];
+  // The order within a tile: operand reads one row block ahead, the next slice's widening between this one's products (224
+  // rows, V = 131072, H = 4096: 185 us against 210 as the compiler has it). With five blocks there are no registers for it.
+  constexpr bool kPinned = NBW <= 4;
+  constexpr int kOut = kOutStride<NBW * 16>;
+  constexpr int kOutWave = 16 * kOut * 4;  // a wave's logits of 16 rows, in the same place in the end
+  __shared__ __attribute__((aligned(16))) unsigned char s_x[2 * kStage > NW * kOutWave ? 2 * kStage : NW * kOutWave];
+  __shared__ long long s_at[MB * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
@@ -175,6 +239,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int vt = grp * 8 + (in & 7), mt = in >> 3;
   if (vt >= v_tiles) return;
   const int vb0 = (vt * NW + w) * NBW, m0 = mt * MB * 16;
+  if (tid < MB * 16) s_at[tid] = row_at(a, min(m0 + tid, a.M - 1));
   const uint8_t* wp[NBW];
   const uint8_t* sp[NBW];
 #pragma unroll
@@ -228,25 +293,69 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       copy_x((c + 1) & 1, c + 1);
       load_w(c + 1);
     }
-    const unsigned char* cur = s_x[c & 1] + lr * 256;
+    const unsigned char* cur = s_x + (c & 1) * kStage + lr * 256;
+    auto operand = [&](int mb, int s) { return *(const bf16x8*)(cur + mb * 4096 + ((4 * lg + s) ^ lr) * 16); };
+    __builtin_amdgcn_s_setprio(1);
+    if constexpr (kPinned) {
+      bf16x8 A[2][NBW];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      bf16x8 A[NBW];
+      for (int nb = 0; nb < NBW; ++nb) A[0][nb] = widen(cw[nb][0], sc[nb]);
+      bf16x8 x = operand(0, 0);
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) A[nb] = widen(cw[nb][s], sc[nb]);
+      for (int s = 0; s < 4; ++s) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        const bf16x8 x = *(const bf16x8*)(cur + mb * 4096 + ((4 * lg + s) ^ lr) * 16);
+        for (int mb = 0; mb < MB; ++mb) {
+          bf16x8 xn = x;
+          const bool more = s < 3 || mb + 1 < MB;
+          if (more) xn = mb + 1 < MB ? operand(mb + 1, s) : operand(0, s + 1);
+          if (s < 3) {
 #pragma unroll
-        for (int nb = 0; nb < NBW; ++nb)
-          acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb], x, acc[nb][mb], 0, 0, 0);
+            for (int nb = 0; nb < NBW; ++nb)
+              if (nb * MB / NBW == mb) A[(s + 1) & 1][nb] = widen(cw[nb][s + 1], sc[nb]);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+            acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[s & 1][nb], x, acc[nb][mb], 0, 0, 0);
+          if (more) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          x = xn;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        bf16x8 A[NBW];
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb) A[nb] = widen(cw[nb][s], sc[nb]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const bf16x8 x = operand(mb, s);
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb)
+            acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[nb], x, acc[nb][mb], 0, 0, 0);
+        }
       }
     }
+    __builtin_amdgcn_s_setprio(0);
   }
+  __syncthreads();  // the hidden rows have been read
+  float* so = (float*)(s_x + w * kOutWave);
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
+  for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb) store_block(a, acc[nb][mb], mt * MB + mb, vb0 + nb);
+    for (int nb = 0; nb < NBW; ++nb) *(floatx4*)(so + lr * kOut + nb * 16 + lg * 4) = acc[nb][mb];
+    store_rows<NBW * 16>(
+        a, lane, 64, min(16, a.M - m0 - mb * 16), vb0 * 16, [&](int r) { return s_at[mb * 16 + r]; },
+        [&](int r, int c, auto cols) {
+          using T = typename std::conditional<decltype(cols)::value == 4, floatx4, float>::type;
+          return *(const T*)(so + r * kOut + c);
+        });
+  }
 }
 
 // Row-major codes [V][H / 2] and scales [V][H / 32] into the tiles: a thread per 16 codes' bytes; rows past V and
@@ -349,35 +458,94 @@ __global__ __launch_bounds__(256) void unpack_mx_kernel(int V, int H, const uint
   }
 }
 
-template <int MB, int NBW>
+template <int NG, int NBW>
 hipError_t launch_few(const LmHeadMxArgs& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, MBt = (a.M + 15) >> 4;
-  hipLaunchKernelGGL((lm_head_mx_kernel<MB, NBW>), dim3((unsigned)((VB + NBW - 1) / NBW), (unsigned)((MBt + MB - 1) / MB)),
-                     dim3(256), 0, st, a);
+  const int VB = (a.V + 15) >> 4;
+  hipLaunchKernelGGL((lm_head_mx_kernel<NG, NBW>), dim3((unsigned)((VB + NBW - 1) / NBW)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
+// Vocabulary blocks of a work-group: four, so that the hidden rows are read less often, but fewer where that leaves CUs
+// without one, and for up to 4 rows, which cost little (H = 4096, us with one / two / four: 16 rows, V = 4099 8.5 / 9.6 /
+// 12.0, V = 32000 28 / 22 / 20; H = 2048, 4 rows, V = 151936 33 / 32 / 33, one row 33 / 29 / 32).
+template <int NG>
+hipError_t launch_few_rows(const LmHeadMxArgs& a, hipStream_t st) {
+  const int VB = (a.V + 15) >> 4;
+  if (VB <= 512) return launch_few<NG, 1>(a, st);
+  if constexpr (NG == 1) return launch_few<NG, 2>(a, st);
+  return VB <= 1024 ? launch_few<NG, 2>(a, st) : launch_few<NG, 4>(a, st);
+}
+
 template <int MB, int NBW>
-hipError_t launch_wide(const LmHeadMxArgs& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, mt = (((a.M + 15) >> 4) + MB - 1) / MB;
-  const int tiles = (VB + 4 * NBW - 1) / (4 * NBW);
-  hipLaunchKernelGGL((lm_head_mx_wide_kernel<MB, NBW>), dim3((unsigned)((tiles + 7) / 8 * 8 * mt)), dim3(256), 0, st, a,
-                     tiles, mt);
+hipError_t launch_wide(const LmHeadMxArgs& a, int tiles, int mt, hipStream_t st) {
+  hipLaunchKernelGGL((lm_head_mx_wide_kernel<MB, NBW>), dim3((unsigned)((tiles + 7) / 8 * 8 * mt)), dim3(256), 0, st, a, tiles,
+                     mt);
   return hipGetLastError();
+}
+
+// What a launch of the wide kernel takes, in units that a pass over a row of the matrix with one more block would add: the
+// CUs take 512 work-groups a round, each of a time that grows with its blocks of the vocabulary beside what a tile of the
+// hidden rows costs (as much as one of them); 256 or fewer at the end have a CU each and take about 0.7 of it.
+// (H = 4096, us with 1 / 2 / 3 / 4 / 5 blocks a wave, the rule's choice last: 112 rows, V = 100003 144 / 118 / 126 / 104 / 124,
+// 4; 32 rows, V = 151936 105 / 83 / 75 / 92 / 65, 5; 32 rows, V = 200064 143 / 110 / 107 / 104 / 106, 4; 112 rows,
+// V = 32000 41 / 39 / 44 / 54 / 66, 1; 224 rows, V = 200064 455 / 332 / 312 / 297 / 289, 5.)
+float wide_cost(int VB, int mt, int nbw) {
+  const int wgs = (VB + 4 * nbw - 1) / (4 * nbw) * mt, rest = wgs % 512;
+  return (float)(wgs / 512) * (float)(1 + nbw) + (rest == 0 ? 0.0f : rest <= 256 ? 0.7f : 1.0f) * (float)(1 + nbw);
+}
+int wide_blocks(int VB, int mt, int mb) {
+  int best = 1;
+  for (int nbw = 2; nbw <= (mb <= 4 ? 7 : 5); ++nbw)  // (what the registers hold)
+    if (wide_cost(VB, mt, nbw) < wide_cost(VB, mt, best)) best = nbw;
+  return best;
+}
+// Row tiles of at most 7 blocks, all of one height; lower ones while every work-group keeps a CU to itself (112 rows,
+// V = 4099, H = 4096: 28 us in one tile, three of 3 blocks 19 us).
+int wide_row_tiles(int VB, int n) {
+  const int least = (n + 6) / 7, alone = 256 / ((VB + 3) / 4);
+  return alone > n ? n : alone > least ? alone : least;
+}
+
+template <int MB>
+hipError_t launch_rows(const LmHeadMxArgs& a, int mt, hipStream_t st) {
+  const int VB = (a.V + 15) >> 4;
+  const int nbw = wide_blocks(VB, mt, MB), tiles = (VB + 4 * nbw - 1) / (4 * nbw);
+  if constexpr (MB <= 4) {
+    if (nbw == 6) return launch_wide<MB, 6>(a, tiles, mt, st);
+    if (nbw == 7) return launch_wide<MB, 7>(a, tiles, mt, st);
+  }
+  switch (nbw) {
+    case 1: return launch_wide<MB, 1>(a, tiles, mt, st);
+    case 2: return launch_wide<MB, 2>(a, tiles, mt, st);
+    case 3: return launch_wide<MB, 3>(a, tiles, mt, st);
+    case 4: return launch_wide<MB, 4>(a, tiles, mt, st);
+    default: return launch_wide<MB, 5>(a, tiles, mt, st);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_lm_head_mx(const LmHeadMxArgs& a, hipStream_t st) {
-  // row tiles of at most 7 blocks, all of one height
-  const int n = (a.M + 15) >> 4, tiles = (n + 6) / 7, mb = (n + tiles - 1) / tiles;
+  const int VB = (a.V + 15) >> 4, n = (a.M + 15) >> 4;
+  const int tiles = wide_row_tiles(VB, n), mb = (n + tiles - 1) / tiles, mt = (n + mb - 1) / mb;
+  // Up to 32 rows either kernel: the few rows' takes a start and a time by the vocabulary that grows with the rows, in
+  // wide_cost's units (H = 4096, us few / wide: 7 rows, V = 200064 81 / 95, V = 151936 63 / 59; 16 rows, V = 100003 54 / 48,
+  // V = 32000 20 / 24; 32 rows, V = 200064 117 / 104, V = 4099 12.5 / 16.7).
+  if (a.M <= 32) {
+    const float few = 0.5f + (a.M <= 4 ? 0.55e-3f : a.M <= 8 ? 0.61e-3f : a.M <= 16 ? 0.71e-3f : 0.88e-3f) * (float)VB;
+    if (few < wide_cost(VB, mt, wide_blocks(VB, mt, mb))) {
+      if (a.M <= 4) return launch_few_rows<1>(a, st);
+      if (a.M <= 8) return launch_few_rows<2>(a, st);
+      return a.M <= 16 ? launch_few_rows<4>(a, st) : launch_few_rows<8>(a, st);
+    }
+  }
   switch (mb) {
-    case 1: return launch_few<1, 4>(a, st);
-    case 2: return launch_few<2, 4>(a, st);
-    case 3: return launch_wide<3, 4>(a, st);
-    case 4: return launch_wide<4, 4>(a, st);
-    case 5: return launch_wide<5, 4>(a, st);
-    case 6: return launch_wide<6, 4>(a, st);
-    default: return launch_wide<7, 4>(a, st);
+    case 1: return launch_rows<1>(a, mt, st);
+    case 2: return launch_rows<2>(a, mt, st);
+    case 3: return launch_rows<3>(a, mt, st);
+    case 4: return launch_rows<4>(a, mt, st);
+    case 5: return launch_rows<5>(a, mt, st);
+    case 6: return launch_rows<6>(a, mt, st);
+    default: return launch_rows<7>(a, mt, st);
   }
 }
 
