@@ -27,11 +27,12 @@ def _current_stream(index):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # (there are tensors on the GPU already)
 
 
 def _call(what, fn, index, stream, args):
     """fn(*args, stream) on the tensors' device and the given (or that device's current) stream."""
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         if stream is not None and stream.device.index != index:

@@ -230,6 +230,7 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
     return abi_fail(MDS_ERR_INVALID_ARG, "hidden_row_stride must be a multiple of 8, at least H");
   // (112 rows are addressed with 32-bit offsets)
   if (hidden_row_stride > (1 << 22)) return abi_fail(MDS_ERR_UNSUPPORTED, "hidden_row_stride must be at most 2^22");
+  if ((int64_t)((V + 63) / 64) * ((rows + 15) / 16) > (1 << 30)) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   if (!aligned(hidden, 16) || !aligned(lm_head, 16) || !aligned(scales, 4))
     return abi_fail(MDS_ERR_INVALID_ARG, "hidden and lm_head must be 16-byte aligned, scales 4-byte aligned");
   out_req_stride = step(B, out_req_stride);

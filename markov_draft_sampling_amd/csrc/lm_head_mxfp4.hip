@@ -14,6 +14,12 @@
 // Which columns a matrix instruction takes together does not matter as long as both
 // operands agree: its slice s has columns 32 g + 8 s .. + 7 of each g. Scales of
 // four tiles in a row of tiles are the bytes of a lane's word.
+//
+// Up to some 50 rows the call is bound by the matrix's 17 / 32 V H bytes (H = 4096: one row, V = 200064 73 us and 6.0
+// TB/s; 7 rows, V = 151936 57 us; 32 rows, V = 200064 90 us), above by the matrix cores, the widening and the operand
+// reads from LDS (224 rows: V = 200064 280 us and 1.31 PFLOP/s, V = 151936 221 us). Small vocabularies take a
+// work-group's start and its chain of loads (7 rows, V = 4099 8 us). (Pairs at the rules below are from one run each;
+// cards differ by up to 8%.)
 #include <type_traits>
 
 #include "mds_device.h"
@@ -37,8 +43,8 @@ __device__ __forceinline__ bf16x8 widen(uint32_t codes, float scale) {
 __device__ __forceinline__ float scale_of(uint32_t word, int i) { return __uint_as_float((word >> (8 * i) & 0xFFu) << 23); }
 
 // Logits go out by way of LDS, as rows of consecutive columns (four floats of padding keep rows apart in the banks): a
-// row's run of them in one piece, also where rows are not aligned and every logit is a store of its own (224 rows, V = 100003,
-// H = 1024: PLACEHOLDER).
+// row's run of them in one piece, also where rows are not aligned and every logit is a store of its own (224 rows, V = 100003:
+// 163 us, by stores of a lane's own four logits 201; V = 151936 221 and 228).
 template <int COLS>
 constexpr int kOutStride = COLS + 4;
 
@@ -49,7 +55,7 @@ __device__ __forceinline__ long long row_at(const LmHeadMxArgs& a, int m) {
 }
 
 // The i-th of n threads stores its part of `rows` rows of COLS logits from column v0 on. at(r): where row r starts;
-// z(r, c): a pointer to NC logits in LDS.. their sums are the caller's.
+// z(r, c, n): its n logits from column c on (n: 4 or 1, as a type).
 template <int COLS, typename At, typename Z>
 __device__ __forceinline__ void store_rows(const LmHeadMxArgs& a, int i, int n, int rows, int v0, At at, Z z) {
   if (a.vec_out) {
@@ -486,8 +492,8 @@ hipError_t launch_wide(const LmHeadMxArgs& a, int tiles, int mt, hipStream_t st)
 // CUs take 512 work-groups a round, each of a time that grows with its blocks of the vocabulary beside what a tile of the
 // hidden rows costs (as much as one of them); 256 or fewer at the end have a CU each and take about 0.7 of it.
 // (H = 4096, us with 1 / 2 / 3 / 4 / 5 blocks a wave, the rule's choice last: 112 rows, V = 100003 144 / 118 / 126 / 104 / 124,
-// 4; 32 rows, V = 151936 105 / 83 / 75 / 92 / 65, 5; 32 rows, V = 200064 143 / 110 / 107 / 104 / 106, 4; 112 rows,
-// V = 32000 41 / 39 / 44 / 54 / 66, 1; 224 rows, V = 200064 455 / 332 / 312 / 297 / 289, 5.)
+// 4; 32 rows, V = 151936 105 / 83 / 75 / 92 / 65, 5; V = 200064 143 / 110 / 107 / 104 / 106, and 90 with the rule's 7; 112
+// rows, V = 32000 41 / 39 / 44 / 54 / 66, 1; 224 rows, V = 200064 455 / 332 / 312 / 297 / 289, 5.)
 float wide_cost(int VB, int mt, int nbw) {
   const int wgs = (VB + 4 * nbw - 1) / (4 * nbw) * mt, rest = wgs % 512;
   return (float)(wgs / 512) * (float)(1 + nbw) + (rest == 0 ? 0.0f : rest <= 256 ? 0.7f : 1.0f) * (float)(1 + nbw);

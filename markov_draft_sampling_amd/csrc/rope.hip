@@ -16,6 +16,10 @@
 // and R / 2 + 8 j on, or 16 j on), so that no lane needs another's columns and
 // the sum of squares is the only exchange. The 64 lanes compute the token's
 // sines and cosines once, a pair each, and read their eight pairs from LDS.
+//
+// Bound by HBM for prompts, every element read and written once (16384 tokens of
+// 32 query and 8 key heads of 128 with their values, 403 MB: 76 us, 5.3 TB/s),
+// by the launch for a decoding step (one token 3.0 us, 256 tokens 3.8 us).
 #include "mds_device.h"
 #include "mds_serve.h"
 
@@ -215,6 +219,9 @@ hipError_t launch_lanes(const RopeArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, a, per_token);
     return hipGetLastError();
   };
+  // Two heads a lane once the waves fill the CUs: sines, cosines and positions serve two, and twice the bytes are in flight
+  // (32 + 2 x 8 heads of 128, us with one / two / three: 16384 tokens 86 / 76 / 79, 1024 8.4 / 8.3 / 8.7, 256 3.8 / 4.3 / 5.3).
+  if ((long long)a.T * waves > 8192) return launch(rope_kernel<LPH, 2, TO>, 2);
   return launch(rope_kernel<LPH, 1, TO>, 1);
 }
 

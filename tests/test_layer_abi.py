@@ -108,7 +108,8 @@ def _head(**kw):
                                    (dict(lm=None), -1), (dict(out=None), -1), (dict(dt=2), -1), (dict(hrs=248), -1),
                                    (dict(hrs=260), -1), (dict(hrs=(1 << 22) + 8), -2), (dict(lm=FAKE + 8), -1),
                                    (dict(sc=FAKE + 2), -1), (dict(hidden=FAKE + 8), -1), (dict(ss=999), -1),
-                                   (dict(rs=2000), -1)])
+                                   (dict(rs=2000), -1),
+                                   (dict(B=65535, K=64, V=(1 << 24) - 1, rs=1 << 30, ss=1 << 24), -2)])
 def test_lm_head_mxfp4_refusals(lib, kw, rc):
     assert lib.mds_lm_head_mxfp4(*_head(**kw)) == rc
     assert lib.mds_last_error()
