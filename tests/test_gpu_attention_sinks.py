@@ -145,6 +145,42 @@ def test_prompts_over_128_rows_and_split():
     _case([300, 2000], [600, 520], 16, 1, 64, 16, 700, 64, seed=3)
 
 
+def test_a_prompt_beside_single_tokens():
+    # tiles numbered by their rows instead of by request
+    _case([3000] + list(range(10, 1000, 50)), [260] + [1] * 20, 4, 2, 64, 16, 200, 20, idx=True)
+    _case(list(range(10, 1000, 50)) + [900], [0, 3] * 10 + [150], 8, 2, 128, 32, 100, 70, cache="e4m3")
+
+
+def test_more_work_groups_than_cus_longest_first():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(1, 7000, 70).tolist()
+    _case(lens, [1] * 70, 4, 4, 64, 64, 5000, 10, seed=5)
+    _case(lens, [2] * 70, 8, 4, 64, 64, 5000, 10, cache="e4m3", seed=6, idx=True)
+
+
+def test_pages_past_32_bits():
+    import torch
+    import markov_draft_sampling_amd as mds
+    NP, P, H, D = 140000, 16, 8, 128  # 32 KB a page: the last one is 4.6 GB in
+    kp, vp = (torch.zeros((NP, P, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(0)
+    mine = [NP - 1, 5, NP - 70, 70000]
+    k, v = (torch.randn((64, H, D), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((64, H, D), generator=g).to(torch.bfloat16)
+    slot = torch.tensor([mine[i // P] * P + i % P for i in range(64)], device="cuda")
+    pos, qo = torch.zeros(64, dtype=torch.int64, device="cuda"), torch.zeros((64, H, D), dtype=torch.bfloat16, device="cuda")
+    mds.qk_norm_rope_append(q.cuda(), k.cuda(), v.cuda(), pos, None, qo, kp, vp, slot)
+    assert torch.equal(qo.cpu(), q) and torch.equal(kp[mine].cpu().view(64, H, D), k) and torch.equal(vp[mine].cpu().view(64, H, D), v)
+    assert int((kp != 0).any(-1).any(-1).sum()) == 64
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.zeros((1, H, D), dtype=torch.bfloat16, device="cuda")
+    mds.paged_attention(qo[:1], kp, vp, t([mine]), t([0, 1]), t([63]), out, 1, 63, window=20, sinks=3)
+    r, _, A, S, _ = lr.attention_sinks(q[:1], k.float().view(4, P, H, D), v.float().view(4, P, H, D), [[0, 1, 2, 3]], [0, 1],
+                                       [63], 1 / math.sqrt(D), True, 20, 3)
+    tol, _ = sr.attention_tolerance(r, A, S, D, 63)
+    assert ((out.cpu().double() - r).abs() <= tol).all()
+
+
 def test_the_edges_of_both_parts():
     # every distance of the window from the first tokens, over two blocks of 64 keys
     for ctx in range(60, 200, 7):

@@ -107,6 +107,30 @@ def test_wide_vocabulary_and_rows():
         _check(out[:, 0].cpu().numpy()[:, at].astype(np.float64), x[:rows].double().numpy(), w)
 
 
+def test_a_matrix_past_32_bits():
+    # 4.5 GB of codes: checked at the first and the last rows
+    import torch
+    import markov_draft_sampling_amd as mds
+    V, H = 1100003, 8192
+    g = torch.Generator(device="cuda").manual_seed(2)
+    codes = torch.randint(0, 256, (V, H // 2), generator=g, dtype=torch.uint8, device="cuda")
+    scales = torch.randint(116, 121, (V, H // 32), generator=g, dtype=torch.uint8, device="cuda")
+    tiled, ts = mds.tile_lm_head_mxfp4(codes, scales)
+    at = torch.cat([torch.arange(40), torch.arange(V - 40, V)])
+    c = codes[at.cuda()].cpu().numpy()
+    w = lr.mx_values(np.stack([c & 15, c >> 4], -1).reshape(80, H), scales[at.cuda()].cpu().numpy())
+    del codes, scales
+    x = torch.randn((40, H), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    for rows in (3, 40):
+        out = torch.full((rows, 1, V), 7.25, device="cuda")
+        mds.lm_head_mxfp4(x[:rows].cuda(), tiled, ts, out, 1)
+        _check(out[:, 0, at.cuda()].cpu().numpy().astype(np.float64), x[:rows].double().numpy(), w)
+    back = mds.unpack_lm_head_mxfp4(tiled, ts, V)
+    assert torch.equal(back[at.cuda()].cpu().double(), torch.from_numpy(w))
+    t2, s2 = mds.quantize_lm_head_mxfp4(back)  # (values of the format come back as they are, with scales that fit)
+    assert torch.equal(mds.unpack_lm_head_mxfp4(t2, s2, V), back)
+
+
 def test_outputs_strided_with_rows_left_alone():
     _run(6, 8, 1003, 256, seed=1, out_dtype="bf16", pad=5, extra=2)
     _run(6, 8, 1003, 256, seed=1, pad=5, extra=2)
