@@ -796,10 +796,6 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
 #define MDS_PACKED_APPEND 1          /* mds_kv_append, n = 24 */
 #define MDS_PACKED_ATTENTION 2       /* mds_paged_attention, n = 38 */
 #define MDS_PACKED_LM_HEAD_FP8 3     /* mds_lm_head_fp8, n = 14 */
-#define MDS_PACKED_ATTENTION_SINKS 4 /* mds_paged_attention_sinks, n = 39 */
-#define MDS_PACKED_ROPE 5            /* mds_qk_norm_rope, n = 24 */
-#define MDS_PACKED_ROPE_APPEND 6     /* mds_qk_norm_rope_append, n = 39 */
-#define MDS_PACKED_LM_HEAD_MXFP4 7   /* mds_lm_head_mxfp4, n = 12 */
 int mds_call_packed(int call, const int64_t* args, int n, void* stream);
 
 #ifdef __cplusplus

@@ -13,13 +13,22 @@ import torch
 
 from . import _SIGS, BF16, E4M3, F32, MdsError, _check, _lib, _need
 
+_lib()
+try:
+    from . import _calls
+except ImportError as e:
+    raise MdsError(f"the package's compiled calls do not load ({e}): build them with "
+                   "`python -m markov_draft_sampling_amd.build`") from None
+_calls.set_error(MdsError)
+
 _I32, _I64, _F32, _BF16, _E4M3 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _F64, _U8 = torch.float64, torch.uint8
 _c_sz = ctypes.c_size_t
 
 # These calls take a few microseconds on the GPU at decoding sizes, so the checks here are kept cheap: a device is
 # compared by its index, pointers are plain integers (0: NULL), the stream is asked for once, and the arguments of the
-# calls of a step go over packed (attention's 39 ctypes arguments cost 3.6 us, packed 0.9).
+# calls of a step go over packed (39 ctypes arguments cost 3.6 us, packed 0.9). Those whose checks would
+# outlast their kernels all the same are checked and called by _calls, which is compiled.
 
 
 def _current_stream(index):
@@ -45,8 +54,7 @@ def _call(what, fn, index, stream, args):
 
 # mds_call_packed's numbers and the arguments' layout: 8 bytes each, floats as doubles
 _PACKED = {name: (i, struct.Struct("".join("d" if t is ctypes.c_float else "q" for t in _SIGS["mds_" + name][0][:-1])))
-           for i, name in enumerate(("kv_page_tables", "kv_append", "paged_attention", "lm_head_fp8",
-                                       "paged_attention_sinks", "qk_norm_rope", "qk_norm_rope_append", "lm_head_mxfp4"))}
+           for i, name in ((0, "kv_page_tables"), (1, "kv_append"), (3, "lm_head_fp8"))}
 
 
 def _packed(what, index, stream, args):
@@ -57,6 +65,17 @@ def _packed(what, index, stream, args):
     except struct.error as e:
         raise MdsError(f"{what}: an argument is no integer or out of range: {e}") from None
     _call(what, _lib().mds_call_packed, index, stream, (call, data, len(args)))
+
+
+def _compiled(fn, index, stream, *args):
+    """fn(*args, stream) of _calls, as _call."""
+    if stream is None and _current_device() == index:
+        fn(*args, _raw_stream(index))
+        return
+    if stream is not None and stream.device.index != index:
+        raise MdsError("the stream belongs to another device than the tensors")
+    with torch.cuda.device(index):
+        fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 def _on(stream, make, *args, **kw):
@@ -209,26 +228,6 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, train
     return f.to(device), rope_scale
 
 
-def _heads(t, shape, index, what):
-    """(pointer, token stride, head stride) of bf16 [T, H, D] with a unit last stride."""
-    st = t.stride()
-    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or (st[2] != 1 and t.numel()):
-        raise MdsError(f"{what} must be bf16 {list(shape)} with a unit last stride on cuda:{index}")
-    return t.data_ptr(), st[0], st[1]
-
-
-def _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev):
-    """What the two calls have in common: sizes and inputs up to the keys, the rest up to q_out."""
-    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [T, heads, D]")
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    half = 0 if inv_freq is None else inv_freq.numel()
-    return ((T, Hq, Hk, D, 2 * half, *_heads(q, q.shape, dev, "q"), *_heads(k, (T, Hk, D), dev, "k")),
-            (_vec(positions, _I64, T, dev, "positions"), _opt(inv_freq, _F64, half, dev, "inv_freq"),
-             _opt(q_weight, _BF16, D, dev, "q_weight"), _opt(k_weight, _BF16, D, dev, "k_weight"), eps, rope_scale,
-             1 if interleaved else 0, *_heads(q_out, q.shape, dev, "q_out")))
-
-
 def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                  rope_scale=1.0, stream=None) -> None:
     """Norm and rotation of queries and keys, head by head (mds_qk_norm_rope).
@@ -239,9 +238,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weigh
     k_weight bf16 [D] or None (no norm); interleaved pairs columns (2 i, 2 i +
     1) instead of (i, i + R / 2); rope_scale multiplies cosine and sine.
     """
-    dev = _index(q)
-    first, rest = _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev)
-    _packed("qk_norm_rope", dev, stream, (*first, *rest, *_heads(k_out, k.shape, dev, "k_out")))
+    _compiled(_calls.qk_norm_rope, _index(q), stream, q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps,
+              interleaved, rope_scale)
 
 
 def qk_norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pages, v_pages, slot_map, q_weight=None, k_weight=None,
@@ -253,15 +251,8 @@ def qk_norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pages, v_pages, s
     q, k, positions to rope_scale as for qk_norm_rope; v bf16 [T, Hkv, D]; the
     pages, slot_map, scales and status as for kv_append.
     """
-    dev = _index(q)
-    (NP, P, H, D), code, kp, vp = _pages(k_pages, v_pages, dev)
-    first, rest = _rotation(q, k, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved, q_out, dev)
-    T = first[0]
-    _need(first[2] == H and first[3] == D, "the pages must be [n_pages, page_size, Hkv, D] of the keys' heads")
-    _packed("qk_norm_rope_append", dev, stream,
-            (*first, *_heads(v, k.shape, dev, "v"), *rest, k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, kp[0],
-             kp[1], kp[2], vp[0], vp[1], vp[2], _vec(slot_map, _I64, T, dev, "slot_map"),
-             _opt(k_scale, _F32, H, dev, "k_scale"), _opt(v_scale, _F32, H, dev, "v_scale"), _status(status, dev)))
+    _compiled(_calls.qk_norm_rope_append, _index(q), stream, q, k, v, positions, inv_freq, q_out, k_pages, v_pages,
+              slot_map, q_weight, k_weight, eps, interleaved, rope_scale, k_scale, v_scale, status)
 
 
 def paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window=0, sinks=0) -> int:
@@ -284,27 +275,14 @@ def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out
     the first sinks tokens; lse float32 [T, Hq] or None. Returns the workspace used.
     """
     dev = _index(q)
-    (NP, P, Hk, D), code, kp, vp = _pages(k_pages, v_pages, dev)
-    shape = q.shape
-    _need(q.dtype is _BF16 and out.dtype is _BF16 and len(shape) == 3 and out.shape == shape and shape[2] == D
-          and out.get_device() == dev, "q and out must be bf16 [T, Hq, D] on one device")
-    T, Hq, _ = shape
-    qs, os = q.stride(), out.stride()
-    _need(T == 0 or (qs[2] == 1 and os[2] == 1), "q and out must have a unit last stride")
-    B = seq_lens.numel()
-    _need(block_table.dim() == 2, "block_table must be [n_slots, max_pages]")
-    N, MP = block_table.shape
     if workspace is None:
-        workspace = _new_workspace(paged_attention_workspace_bytes(T, B, Hq, Hk, D, max_q_len, max_seq_len, window, sinks), dev, stream)
-    else:
-        _check_workspace(workspace, dev)
-    _packed("paged_attention_sinks" if sinks else "paged_attention", dev, stream,
-          (T, B, Hq, Hk, D, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, kp[0], kp[1],
-           kp[2], vp[0], vp[1], vp[2], _vec(block_table, _I32, N * MP, dev, "block_table"), N, MP,
-           _opt(idx_map, _I32, B, dev, "idx_map"), _vec(query_start, _I32, B + 1, dev, "query_start"),
-           _vec(seq_lens, _I32, B, dev, "seq_lens"), max_q_len, max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale,
-           1 if causal else 0, *((window, sinks) if sinks else (window,)), _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
-           out.data_ptr(), os[0], os[1], _opt(lse, _F32, T * Hq, dev, "lse"), workspace.data_ptr(), workspace.numel()))
+        _need(q.dim() == 3 and k_pages.dim() == 4, "q must be [T, Hq, D], the pages [n_pages, page_size, Hkv, D]")
+        T, Hq, D = q.shape
+        nbytes = paged_attention_workspace_bytes(T, seq_lens.numel(), Hq, k_pages.shape[2], D, max_q_len, max_seq_len,
+                                                 window, sinks)
+        workspace = _new_workspace(nbytes, dev, stream)
+    _compiled(_calls.paged_attention, dev, stream, q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len,
+              max_seq_len, scale, causal, window, sinks, idx_map, k_scale, v_scale, lse, workspace)
     return workspace
 
 
@@ -483,21 +461,4 @@ def lm_head_mxfp4(hidden, lm_head, scales, out, K, stream=None) -> None:
     from tile_lm_head_mxfp4 / quantize_lm_head_mxfp4; out float32 or bf16
     [B, >=K, V] with unit column stride (rows k < K are written).
     """
-    dev = _index(hidden)
-    _need(hidden.dtype is _BF16 and hidden.dim() == 2 and hidden.stride(1) == 1 and K >= 1 and hidden.shape[0] % K == 0,
-          "hidden must be bf16 [B*K, H] with unit column stride")
-    rows, H = hidden.shape
-    B = rows // K
-    _need(out.dim() == 3 and out.shape[0] == B and out.shape[1] >= K and out.stride(2) == 1 and out.get_device() == dev,
-          "out must be [B, >=K, V] with unit column stride")
-    V = out.shape[2]
-    _mx_tiles(lm_head, scales, V, H, dev)
-    if out.dtype is _F32:
-        code = F32
-    elif out.dtype is _BF16:
-        code = BF16
-    else:
-        raise MdsError(f"unsupported dtype {out.dtype}")
-    _packed("lm_head_mxfp4", dev, stream,
-            (B, K, V, H, hidden.data_ptr(), hidden.stride(0), lm_head.data_ptr(), scales.data_ptr(), out.data_ptr(), code,
-             out.stride(0), out.stride(1)))
+    _compiled(_calls.lm_head_mxfp4, _index(hidden), stream, hidden, lm_head, scales, out, K)

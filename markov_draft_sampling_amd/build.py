@@ -4,7 +4,8 @@
 
 Each source is compiled by hipcc in parallel, then linked into a shared
 library next to this file. Packed fp32 instructions are disabled for device
-code.
+code. The binding's compiled calls (csrc/calls.cpp, against torch's headers)
+become the module _calls beside it.
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmds.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ("abi.hip", "abi_layer.hip", "abi_serve.hip", "draft.hip", "draft_wave.hip", "draft_topk.hip", "kv_cache.hip", "lm_head.hip",
            "lm_head_fp8.hip", "lm_head_mxfp4.hip", "paged_attention.hip", "rope.hip", "verify.hip", "topp.hip")
 ARCH = "gfx950"
@@ -39,8 +41,20 @@ def _hipcc() -> str:
     return exe
 
 
+def _calls_command(out: str):
+    """How the module of the binding's compiled calls is built."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = os.path.join(torch, "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-o", out, os.path.join(CSRC, "calls.cpp"),
+            "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-L", HERE, "-L", os.path.join(torch, "lib"), "-l:libmds.so",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libmds.so; returns its path."""
+    """Compile every source, link libmds.so and the module of calls; returns the library's path."""
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
     procs = []
@@ -68,6 +82,13 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
+    cmd = _calls_command(CALLS + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building the binding's calls failed:\n" + r.stdout + r.stderr)
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 

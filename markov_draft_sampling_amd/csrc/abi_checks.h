@@ -6,10 +6,6 @@
 #include "mds_serve.h"
 
 namespace mds {
-
-// mds_call_packed for the calls of abi_layer.hip
-int call_packed_layer(int call, const int64_t* a, int n, void* stream);
-
 namespace abi {
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -134,23 +130,6 @@ inline int sinks_window(int window, int sinks) {
 inline int check_sinks(int sinks) {
   if (sinks < 0 || sinks > (1 << 29)) return abi_fail(MDS_ERR_INVALID_ARG, "sinks must be in [0, 2^29]");
   return MDS_OK;
-}
-
-// The arguments of a packed call against their types: i int, l int64, p pointer, z size, f float
-inline int check_packed(const char* t, const int64_t* a, int n) {
-  for (int i = 0; i < n || t[i]; ++i) {
-    if (i >= n || !t[i]) return abi_fail(MDS_ERR_INVALID_ARG, "wrong number of arguments");
-    if ((t[i] == 'i' && a[i] != (int)a[i]) || (t[i] == 'z' && a[i] < 0))
-      return abi_fail(MDS_ERR_INVALID_ARG, "an integer is out of its type's range");
-  }
-  return MDS_OK;
-}
-
-inline float packed_real(int64_t x) {
-  double d;
-  static_assert(sizeof d == sizeof x, "8 bytes");
-  __builtin_memcpy(&d, &x, sizeof d);
-  return (float)d;
 }
 
 }  // namespace abi

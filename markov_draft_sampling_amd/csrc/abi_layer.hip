@@ -1,8 +1,7 @@
 // extern "C" entry points of a layer's step between its projections and the
-// logits (norm and rotation, with the append; the 4-bit LM head) and the packed
-// forms of these and of attention with first tokens: argument checks on the
-// host, then the kernels on the caller's stream. See include/mds.h for the
-// contract.
+// logits (norm and rotation, with the append; the 4-bit LM head): argument
+// checks on the host, then the kernels on the caller's stream. See
+// include/mds.h for the contract.
 #include <math.h>
 
 #include "abi_checks.h"
@@ -257,40 +256,3 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
 }
 
 }  // extern "C"
-
-namespace mds {
-
-int call_packed_layer(int call, const int64_t* a, int n, void* stream) {
-  static const char* const kTypes[] = {"iiiiipllppiiillllllpiipppilfiiipppllppz", "iiiiipllpllppppffipllpll",
-                                       "iiiiipllpllpllppppffipllppiiillllllpppp", "iiiiplpppill"};
-  if (!a) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
-  const int rc = check_packed(kTypes[call - MDS_PACKED_ATTENTION_SINKS], a, n);
-  if (rc) return rc;
-  switch (call) {
-    case MDS_PACKED_ATTENTION_SINKS:
-      return mds_paged_attention_sinks(
-          (int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (const void*)a[5], a[6], a[7], (const void*)a[8],
-          (const void*)a[9], (int)a[10], (int)a[11], (int)a[12], a[13], a[14], a[15], a[16], a[17], a[18],
-          (const int32_t*)a[19], (int)a[20], (int)a[21], (const int32_t*)a[22], (const int32_t*)a[23],
-          (const int32_t*)a[24], (int)a[25], a[26], packed_real(a[27]), (int)a[28], (int)a[29], (int)a[30],
-          (const float*)a[31], (const float*)a[32], (void*)a[33], a[34], a[35], (float*)a[36], (void*)a[37],
-          (size_t)a[38], stream);
-    case MDS_PACKED_ROPE:
-      return mds_qk_norm_rope((int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (const void*)a[5], a[6], a[7],
-                              (const void*)a[8], a[9], a[10], (const int64_t*)a[11], (const double*)a[12],
-                              (const void*)a[13], (const void*)a[14], packed_real(a[15]), packed_real(a[16]), (int)a[17],
-                              (void*)a[18], a[19], a[20], (void*)a[21], a[22], a[23], stream);
-    case MDS_PACKED_ROPE_APPEND:
-      return mds_qk_norm_rope_append(
-          (int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)a[4], (const void*)a[5], a[6], a[7], (const void*)a[8], a[9],
-          a[10], (const void*)a[11], a[12], a[13], (const int64_t*)a[14], (const double*)a[15], (const void*)a[16],
-          (const void*)a[17], packed_real(a[18]), packed_real(a[19]), (int)a[20], (void*)a[21], a[22], a[23],
-          (void*)a[24], (void*)a[25], (int)a[26], (int)a[27], (int)a[28], a[29], a[30], a[31], a[32], a[33], a[34],
-          (const int64_t*)a[35], (const float*)a[36], (const float*)a[37], (uint32_t*)a[38], stream);
-    default:
-      return mds_lm_head_mxfp4((int)a[0], (int)a[1], (int)a[2], (int)a[3], (const void*)a[4], a[5], (const void*)a[6],
-                               (const void*)a[7], (void*)a[8], (int)a[9], a[10], a[11], stream);
-  }
-}
-
-}  // namespace mds

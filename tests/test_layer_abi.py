@@ -5,6 +5,7 @@ import ctypes
 import math
 import os
 import re
+import sys
 
 import numpy as np
 import pytest
@@ -142,49 +143,44 @@ def test_mxfp4_matrix_sizes_and_refusals(lib):
     assert unpack(1000, 256, t, s, s + 16, None) == -1
 
 
-def _pack(args):
-    import struct
-    return b"".join(struct.pack("d" if isinstance(x, float) else "q", 0 if x is None else x) for x in args)
-
-
-_CALLS = [("mds_paged_attention_sinks", _attend, dict(D=96), 4), ("mds_qk_norm_rope", _rope, dict(R=24), 5),
-          ("mds_qk_norm_rope_append", _rope_append, dict(dt=0), 6), ("mds_lm_head_mxfp4", _head, dict(H=100), 7)]
-
-
-@pytest.mark.parametrize("name,make,bad,call", _CALLS)
-def test_packed_calls_refuse_as_the_calls_do(lib, name, make, bad, call):
-    args = make(**bad)
-    rc = getattr(lib, name)(*args)
-    message = lib.mds_last_error()
-    n = len(args) - 1
-    assert rc < 0 and lib.mds_call_packed(call, _pack(args[:-1]), n, None) == rc
-    assert lib.mds_last_error() == message
-    assert lib.mds_call_packed(call, _pack(args[:-1]), n - 1, None) == -1
-    assert lib.mds_call_packed(call, _pack(args), n + 1, None) == -1
-    assert lib.mds_call_packed(call, _pack([1 << 40] + args[1:-1]), n, None) == -1
-    assert lib.mds_call_packed(8, _pack(args[:-1]), n, None) == -1
-    assert lib.mds_call_packed(-1, _pack(args[:-1]), n, None) == -1
-    assert lib.mds_call_packed(call, None, n, None) == -1
-    assert b"NULL" in lib.mds_last_error()
+_CALLS = [("mds_paged_attention_sinks", _attend), ("mds_qk_norm_rope", _rope), ("mds_qk_norm_rope_append", _rope_append),
+          ("mds_lm_head_mxfp4", _head)]
 
 
 def test_the_copies_of_a_signature_agree():
-    # the header's prototype and packed number, the binding's ctypes signature and the packed call's type string
+    # the header's prototype and the binding's ctypes signature
     root = os.path.dirname(os.path.dirname(os.path.abspath(mds.__file__)))
     with open(os.path.join(root, "include", "mds.h")) as f:
-        text = f.read()
-    header = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    with open(os.path.join(root, "markov_draft_sampling_amd", "csrc", "abi_layer.hip")) as f:
-        strings = re.findall(r'"([iplzf]{10,})"', f.read())
+        header = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
     ctype = {"i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float}
-    assert len(strings) == len(_CALLS)
-    for (name, make, _, call), packed in zip(_CALLS, strings):
+    for name, make in _CALLS:
         args = re.search(name + r"\((.*?)\);", header, re.S).group(1).split(",")
         kinds = ["p" if "*" in a else {"int": "i", "int64_t": "l", "size_t": "z", "float": "f"}[a.split()[0]] for a in args]
-        assert "".join(kinds) == packed + "p", name  # the stream is not packed
         assert [t._type_ for t in mds._SIGS[name][0]] == [ctype[k]._type_ for k in kinds], name
         assert len(make()) == len(kinds)
-        assert re.search(rf"#define MDS_PACKED_\w+ {call}\s+/\* {name}, n = {len(packed)} \*/", text), name
+
+
+def test_the_compiled_calls_check_their_arguments():
+    import torch
+    from markov_draft_sampling_amd import _serving
+    calls = _serving._calls
+    x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    for fn, n in ((calls.qk_norm_rope, 12), (calls.qk_norm_rope_append, 18), (calls.paged_attention, 19),
+                  (calls.lm_head_mxfp4, 6)):
+        with pytest.raises(mds.MdsError, match="number of arguments"):
+            fn(*[x] * (n - 1))
+        with pytest.raises(mds.MdsError, match="number of arguments"):
+            fn()
+        with pytest.raises(mds.MdsError, match="GPU"):
+            fn(*[x] * n)
+        for bad in (None, 3, "q", [x]):
+            with pytest.raises(mds.MdsError, match="must be a tensor"):
+                fn(*[bad] * n)
+    held = sys.getrefcount(x)
+    for _ in range(100):
+        with pytest.raises(mds.MdsError):
+            calls.lm_head_mxfp4(x, x, x, x, None, None)
+    assert sys.getrefcount(x) == held
 
 
 def test_frequencies():
