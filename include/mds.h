@@ -590,10 +590,11 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  * and the R / 2 pairs of its first R columns, columns (i, i + R / 2), or
  * (2 i, 2 i + 1) if interleaved, are turned by a = positions[t] * inv_freq[i]:
  *   (y1, y2) -> rope_scale * (y1 cos a - y2 sin a, y2 cos a + y1 sin a)
- * Columns from R on keep y. Float32 throughout (the sum of squares as well), a
- * in float64, rounded once to bf16 where it is written. Scaled positions come as
- * frequencies: linear, by another base, or by parts with rope_scale
- * as its factor on cosine and sine.
+ * Columns from R on keep y. Float32 throughout (the sum of squares as well), each
+ * operation of the rotation rounded by itself; a, its sine and its cosine in
+ * float64; rounded once to bf16 where it is written. Scaled positions come as
+ * frequencies: linear, by another base, or by parts with rope_scale as its factor
+ * on cosine and sine.
  *   q, k          bf16 [T, Hq, D], [T, Hkv, D] (strides as k in mds_kv_append),
  *                 D a multiple of 16, at most 256 (else MDS_ERR_UNSUPPORTED)
  *   R             a multiple of 16 (else MDS_ERR_UNSUPPORTED), 0 <= R <= D (0: the norm alone)
@@ -606,7 +607,7 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  */
 int mds_qk_norm_rope(int T, int Hq, int Hkv, int D, int R, const void* q, int64_t q_token_stride, int64_t q_head_stride,
                      const void* k, int64_t k_token_stride, int64_t k_head_stride, const int64_t* positions,
-                     const double* inv_freq, const void* q_weight, const void* k_weight, float eps, float rope_scale,
+                     const double* inv_freq, const void* q_weight, const void* k_weight, float eps, double rope_scale,
                      int interleaved, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
                      int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
 
@@ -622,7 +623,7 @@ int mds_qk_norm_rope_append(int T, int Hq, int Hkv, int D, int R, const void* q,
                             int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
                             const void* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* positions,
                             const double* inv_freq, const void* q_weight, const void* k_weight, float eps,
-                            float rope_scale, int interleaved, void* q_out, int64_t q_out_token_stride,
+                            double rope_scale, int interleaved, void* q_out, int64_t q_out_token_stride,
                             int64_t q_out_head_stride, void* k_pages, void* v_pages, int cache_dtype, int page_size,
                             int n_pages, int64_t k_page_stride, int64_t k_slot_stride, int64_t k_pages_head_stride,
                             int64_t v_page_stride, int64_t v_slot_stride, int64_t v_pages_head_stride,

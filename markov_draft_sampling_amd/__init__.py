@@ -93,9 +93,9 @@ _SIGS = {
     "mds_quantize_lm_head_fp8": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _vp], _c_int),
     "mds_lm_head_fp8_workspace_bytes": ([_c_int] * 4 + [ctypes.POINTER(_c_sz)], _c_int),
     "mds_lm_head_fp8": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp, _c_sz, _vp], _c_int),
-    "mds_qk_norm_rope": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 2 + [_vp] * 4 + [ctypes.c_float] * 2 + [_c_int]
+    "mds_qk_norm_rope": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 2 + [_vp] * 4 + [ctypes.c_float, ctypes.c_double, _c_int]
                          + [_vp, _c_i64, _c_i64] * 2 + [_vp], _c_int),
-    "mds_qk_norm_rope_append": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 3 + [_vp] * 4 + [ctypes.c_float] * 2 + [_c_int]
+    "mds_qk_norm_rope_append": ([_c_int] * 5 + [_vp, _c_i64, _c_i64] * 3 + [_vp] * 4 + [ctypes.c_float, ctypes.c_double, _c_int]
                                 + [_vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3 + [_c_i64] * 6 + [_vp] * 5, _c_int),
     "mds_paged_attention_sinks_workspace_bytes": ([_c_int] * 6 + [_c_i64, _c_int, _c_int, ctypes.POINTER(_c_sz)], _c_int),
     "mds_paged_attention_sinks": ([_c_int] * 5 + [_vp, _c_i64, _c_i64, _vp, _vp] + [_c_int] * 3 + [_c_i64] * 6

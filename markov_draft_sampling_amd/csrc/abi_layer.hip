@@ -30,7 +30,7 @@ int check_out(const void* p, int T, int64_t ts, int H, int64_t hs, int D) {
 // What both calls have in common; fills a
 int check_rope(mds::RopeArgs& a, int T, int Hq, int Hk, int D, int R, const void* q, int64_t q_ts, int64_t q_hs,
                const void* k, int64_t k_ts, int64_t k_hs, const int64_t* positions, const double* inv_freq,
-               const void* q_weight, const void* k_weight, float eps, float rope_scale, int interleaved, void* q_out,
+               const void* q_weight, const void* k_weight, float eps, double rope_scale, int interleaved, void* q_out,
                int64_t qo_ts, int64_t qo_hs, int per_key_head) {
   int rc;
   if (T < 0 || T > (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "T must be in [0, 2^24]");
@@ -42,7 +42,7 @@ int check_rope(mds::RopeArgs& a, int T, int Hq, int Hk, int D, int R, const void
   if ((T && (!q || !k || !q_out || !positions)) || (R && !inv_freq))
     return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!(eps >= 0.0f) || !(eps < 1e30f)) return abi_fail(MDS_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  if (!(fabsf(rope_scale) < 1e30f)) return abi_fail(MDS_ERR_INVALID_ARG, "rope_scale must be finite");
+  if (!(fabs(rope_scale) < 1e30)) return abi_fail(MDS_ERR_INVALID_ARG, "rope_scale must be finite");
   if (interleaved != 0 && interleaved != 1) return abi_fail(MDS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8))
     return abi_fail(MDS_ERR_INVALID_ARG, "weights must be 16-byte aligned, positions and frequencies 8-byte aligned");
@@ -98,7 +98,7 @@ extern "C" {
 
 int mds_qk_norm_rope(int T, int Hq, int Hkv, int D, int R, const void* q, int64_t q_token_stride, int64_t q_head_stride,
                      const void* k, int64_t k_token_stride, int64_t k_head_stride, const int64_t* positions,
-                     const double* inv_freq, const void* q_weight, const void* k_weight, float eps, float rope_scale,
+                     const double* inv_freq, const void* q_weight, const void* k_weight, float eps, double rope_scale,
                      int interleaved, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
                      int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream) {
   int rc;
@@ -121,7 +121,7 @@ int mds_qk_norm_rope_append(int T, int Hq, int Hkv, int D, int R, const void* q,
                             int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
                             const void* v, int64_t v_token_stride, int64_t v_head_stride, const int64_t* positions,
                             const double* inv_freq, const void* q_weight, const void* k_weight, float eps,
-                            float rope_scale, int interleaved, void* q_out, int64_t q_out_token_stride,
+                            double rope_scale, int interleaved, void* q_out, int64_t q_out_token_stride,
                             int64_t q_out_head_stride, void* k_pages, void* v_pages, int cache_dtype, int page_size,
                             int n_pages, int64_t k_page_stride, int64_t k_slot_stride, int64_t k_pages_head_stride,
                             int64_t v_page_stride, int64_t v_slot_stride, int64_t v_pages_head_stride,

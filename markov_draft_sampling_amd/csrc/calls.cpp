@@ -38,13 +38,13 @@ int64_t whole(PyObject* o, const char* name, int64_t lo = INT32_MIN, int64_t hi 
   }
   return x;
 }
-float real(PyObject* o, const char* name) {
+double real(PyObject* o, const char* name) {
   const double x = PyFloat_AsDouble(o);
   if (x == -1.0 && PyErr_Occurred()) {
     PyErr_Clear();
     throw Refused(std::string(name) + " must be a number");
   }
-  return (float)x;
+  return x;
 }
 bool truth(PyObject* o, const char* name) {
   const int x = PyObject_IsTrue(o);
@@ -151,7 +151,8 @@ struct Rotation {
   const int64_t* positions;
   const double* freq;
   void *q_weight, *k_weight;
-  float eps, scale;
+  float eps;
+  double scale;
   int interleaved;
 };
 Rotation rotation(PyObject* q, PyObject* k, PyObject* positions, PyObject* freq, PyObject* q_out, PyObject* q_weight,
@@ -174,7 +175,7 @@ Rotation rotation(PyObject* q, PyObject* k, PyObject* positions, PyObject* freq,
   r.freq = (const double*)opt(freq, at::kDouble, half, r.dev, "inv_freq");
   r.q_weight = opt(q_weight, at::kBFloat16, r.D, r.dev, "q_weight");
   r.k_weight = opt(k_weight, at::kBFloat16, r.D, r.dev, "k_weight");
-  r.eps = real(eps, "eps");
+  r.eps = (float)real(eps, "eps");
   r.scale = real(scale, "rope_scale");
   r.interleaved = truth(interleaved, "interleaved");
   return r;
@@ -229,7 +230,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
          "workspace must be a contiguous uint8 tensor on the tensors' device");
     void* work = ws.data_ptr();
     const size_t work_bytes = (size_t)ws.numel();
-    const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)p.dim)) : real(a[9], "scale");
+    const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)p.dim)) : (float)real(a[9], "scale");
     auto* tables = (const int32_t*)vec(a[3], at::kInt, (int64_t)N * MP, dev, "block_table");
     auto* map = (const int32_t*)opt(a[13], at::kInt, B, dev, "idx_map");
     auto* start = (const int32_t*)vec(a[4], at::kInt, (int64_t)B + 1, dev, "query_start");

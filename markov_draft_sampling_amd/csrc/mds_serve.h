@@ -60,7 +60,8 @@ struct RopeArgs {
   const double* inv_freq;            // [R / 2], radians a position
   const uint16_t* q_weight;          // bf16 [D] or null: no norm
   const uint16_t* k_weight;
-  float eps, rope_scale;
+  float eps;
+  double rope_scale;
   uint16_t* q_out;                   // may be q (and k_out k)
   long long qo_ts, qo_hs;
   uint16_t* k_out;                   // null with pages

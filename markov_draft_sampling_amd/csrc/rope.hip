@@ -7,9 +7,18 @@
 // (2 i, 2 i + 1), at the angle a = position * inv_freq[i],
 //   (y1, y2) -> s (y1 cos a - y2 sin a, y2 cos a + y1 sin a);
 // columns from R on keep y. All in float32 from the bf16 inputs, rounded once
-// where it is written (bf16, or e4m3 of the quotient by the head's scale). The
-// angle alone is float64, with whole turns taken off before it is rounded to
-// float32: at position 10^6 a float32 product is a sixteenth of a radian off.
+// where it is written (bf16, or e4m3 of the quotient by the head's scale).
+// Angles, sines and cosines are float64 until they are rounded to float32: at
+// position 10^6 a float32 angle is a sixteenth of a radian off.
+//
+// An e4m3 code is a sixteenth of its value: where the quotient is next to the
+// border of two codes, the last bit of float32 decides. So that float32 decides
+// alike wherever a key is computed, every factor here is the float32 nearest to
+// its exact value (sine and cosine, 1 / sqrt), products are rounded one by one and
+// squares are summed in the columns' order, fours in turn and then neighbours.
+// (With float32 sines and fused products three codes in a million fell on the
+// other side than by separate operations, now none of 43 million; the prompt
+// below takes 76.1 us and took 75.3.)
 //
 // A wave takes some heads of one token, LPH lanes a head and 16 columns a lane:
 // two pieces of 16 bytes, which in either layout are whole pairs (columns 8 j
@@ -95,6 +104,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
   const bool split = turned && !a.interleaved;   // the lane's pieces are R / 2 columns apart
   const int c0 = split ? 8 * j : 16 * j, c1 = split ? 8 * j + (a.R >> 1) : 16 * j + 8;
 
+  const bool halves = a.R == a.D && !a.interleaved;  // every lane's pieces are half a head apart
+
   const double pos = (double)a.positions[t];
   u32x4 x[U][2];
 #pragma unroll
@@ -112,10 +123,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
   for (int i = lane; i < a.R >> 1; i += 64) {
     // turns of the angle without the whole ones, at most half a turn either way
     const double turns = pos * a.inv_freq[i] * 0.15915494309189535;
-    const float f = (float)(turns - __builtin_rint(turns));
-    float s, c;
-    sincospif(2.0f * f, &s, &c);
-    s_turn[w][i] = make_float2(c * a.rope_scale, s * a.rope_scale);
+    double s, c;
+    sincospi(2.0 * (turns - __builtin_rint(turns)), &s, &c);
+    s_turn[w][i] = make_float2((float)(c * a.rope_scale), (float)(s * a.rope_scale));
   }
   // (a wave's LDS operations keep their order)
   asm volatile("" ::: "memory");
@@ -154,12 +164,20 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
     }
     const uint16_t* weight = is_q ? a.q_weight : a.k_weight;
     if (a.q_weight || a.k_weight) {
-      float ss = 0.0f;
+      float sum[4];  // of four columns each, whose squares float32 holds exactly
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(y[i], y[i], ss);
-      ss = group_sum<LPH>(ss);
+      for (int i = 0; i < 4; ++i) {
+        const float* z = y + 4 * i;
+        sum[i] = ((z[0] * z[0] + z[1] * z[1]) + z[2] * z[2]) + z[3] * z[3];
+      }
+      float lo = sum[0] + sum[1], hi = sum[2] + sum[3];
+      if (!halves) {
+        lo += hi;
+        hi = 0.0f;
+      }
+      const float ss = group_sum<LPH>(lo) + group_sum<LPH>(hi);
       if (here && weight && !is_v) {
-        const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+        const float r = (float)rsqrt((double)(ss / (float)a.D + a.eps));
         float f[16];
         unpack8(*(const u32x4*)(weight + c0), f);
         unpack8(*(const u32x4*)(weight + c1), f + 8);
@@ -169,6 +187,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
     }
     if (!here) continue;
     if (turned && !is_v) {
+#pragma clang fp contract(off)
       if (a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

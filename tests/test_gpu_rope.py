@@ -202,6 +202,38 @@ def test_the_append_in_the_same_pass(T, Hq, Hk, D, R, interleaved, norm, P, layo
     assert torch.equal(got[rest], before[0][rest])
 
 
+@pytest.mark.parametrize("D,interleaved,norm", [(64, False, True), (128, False, True), (128, True, True), (256, True, True),
+                                                (96, False, False), (128, True, False)])
+def test_codes_are_those_of_separate_operations(D, interleaved, norm):
+    # The float32 factors nearest to their exact values, each operation rounded by itself, squares in the columns' order:
+    # the codes are equal but where a float64 sine or root lies within 2^-50 of the middle of two float32s (one in 10^4
+    # sines at these positions) and the code within 2^-23 of the border of two (one in 10^6): 10^-5 in all for 10^5 keys.
+    import torch
+    import markov_draft_sampling_amd as mds
+    T, Hk = 96, 8
+    s = _inputs(T, 4, Hk, D, D, norm, seed=D)
+    scale = torch.linspace(0.003, 0.03, Hk)
+    kp, vp = (torch.zeros((T // 16, 16, Hk, D), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    mds.qk_norm_rope_append(s["q"], s["k"], s["v"], s["pos"], s["freq"], torch.empty_like(s["q"]), kp, vp,
+                            torch.arange(T).cuda(), q_weight=s["qw"], k_weight=s["kw"], interleaved=interleaved,
+                            rope_scale=1.2079441541679836, k_scale=scale.cuda(), v_scale=scale.cuda())
+    k = s["k"].cpu().float()
+    if norm:
+        z = (k * k).view(T, Hk, D // 4, 4)
+        z = ((z[..., 0] + z[..., 1]) + z[..., 2]) + z[..., 3]
+        while z.shape[-1] > 1:
+            z = z[..., 0::2] + z[..., 1::2]
+        k = k * (z / D + 1e-6).double().rsqrt().float() * s["kw"].cpu().float()
+    a = s["pos"].cpu().double()[:, None] * s["freq"].cpu()
+    c, n = ((f(a) * 1.2079441541679836).float()[:, None] for f in (torch.cos, torch.sin))
+    p, q = (k[..., 0::2], k[..., 1::2]) if interleaved else (k[..., :D // 2], k[..., D // 2:])
+    y, z = p * c - q * n, q * c + p * n
+    k = torch.stack([y, z], -1).flatten(-2) if interleaved else torch.cat([y, z], -1)
+    for got, x in ((kp, k), (vp, s["v"].cpu().float())):
+        want = (x / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert torch.equal(got.view(torch.uint8).cpu().view(T, Hk, D), want.view(torch.uint8))
+
+
 def test_slots_past_the_cache_are_flagged_and_skipped():
     import torch
     import markov_draft_sampling_amd as mds

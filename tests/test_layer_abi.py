@@ -152,10 +152,10 @@ def test_the_copies_of_a_signature_agree():
     root = os.path.dirname(os.path.dirname(os.path.abspath(mds.__file__)))
     with open(os.path.join(root, "include", "mds.h")) as f:
         header = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
-    ctype = {"i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float}
+    ctype = {"i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float, "d": ctypes.c_double}
     for name, make in _CALLS:
         args = re.search(name + r"\((.*?)\);", header, re.S).group(1).split(",")
-        kinds = ["p" if "*" in a else {"int": "i", "int64_t": "l", "size_t": "z", "float": "f"}[a.split()[0]] for a in args]
+        kinds = ["p" if "*" in a else {"int": "i", "int64_t": "l", "size_t": "z", "float": "f", "double": "d"}[a.split()[0]] for a in args]
         assert [t._type_ for t in mds._SIGS[name][0]] == [ctype[k]._type_ for k in kinds], name
         assert len(make()) == len(kinds)
 
