@@ -13,14 +13,6 @@ import torch
 
 from . import _SIGS, BF16, E4M3, F32, MdsError, _check, _lib, _need
 
-_lib()
-try:
-    from . import _calls
-except ImportError as e:
-    raise MdsError(f"the package's compiled calls do not load ({e}): build them with "
-                   "`python -m markov_draft_sampling_amd.build`") from None
-_calls.set_error(MdsError)
-
 _I32, _I64, _F32, _BF16, _E4M3 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _F64, _U8 = torch.float64, torch.uint8
 _c_sz = ctypes.c_size_t
@@ -65,6 +57,24 @@ def _packed(what, index, stream, args):
     except struct.error as e:
         raise MdsError(f"{what}: an argument is no integer or out of range: {e}") from None
     _call(what, _lib().mds_call_packed, index, stream, (call, data, len(args)))
+
+
+_CALLS = None
+
+
+def _calls():
+    """The module of the compiled calls."""
+    global _CALLS
+    if _CALLS is None:
+        _lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise MdsError(f"the compiled calls do not load ({e}): build them with "
+                           "`python -m markov_draft_sampling_amd.build`") from None
+        m.set_error(MdsError)
+        _CALLS = m
+    return _CALLS
 
 
 def _compiled(fn, index, stream, *args):
@@ -238,7 +248,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weigh
     k_weight bf16 [D] or None (no norm); interleaved pairs columns (2 i, 2 i +
     1) instead of (i, i + R / 2); rope_scale multiplies cosine and sine.
     """
-    _compiled(_calls.qk_norm_rope, _index(q), stream, q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps,
+    _compiled(_calls().qk_norm_rope, _index(q), stream, q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps,
               interleaved, rope_scale)
 
 
@@ -251,7 +261,7 @@ def qk_norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pages, v_pages, s
     q, k, positions to rope_scale as for qk_norm_rope; v bf16 [T, Hkv, D]; the
     pages, slot_map, scales and status as for kv_append.
     """
-    _compiled(_calls.qk_norm_rope_append, _index(q), stream, q, k, v, positions, inv_freq, q_out, k_pages, v_pages,
+    _compiled(_calls().qk_norm_rope_append, _index(q), stream, q, k, v, positions, inv_freq, q_out, k_pages, v_pages,
               slot_map, q_weight, k_weight, eps, interleaved, rope_scale, k_scale, v_scale, status)
 
 
@@ -281,7 +291,7 @@ def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out
         nbytes = paged_attention_workspace_bytes(T, seq_lens.numel(), Hq, k_pages.shape[2], D, max_q_len, max_seq_len,
                                                  window, sinks)
         workspace = _new_workspace(nbytes, dev, stream)
-    _compiled(_calls.paged_attention, dev, stream, q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len,
+    _compiled(_calls().paged_attention, dev, stream, q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len,
               max_seq_len, scale, causal, window, sinks, idx_map, k_scale, v_scale, lse, workspace)
     return workspace
 
@@ -461,4 +471,4 @@ def lm_head_mxfp4(hidden, lm_head, scales, out, K, stream=None) -> None:
     from tile_lm_head_mxfp4 / quantize_lm_head_mxfp4; out float32 or bf16
     [B, >=K, V] with unit column stride (rows k < K are written).
     """
-    _compiled(_calls.lm_head_mxfp4, _index(hidden), stream, hidden, lm_head, scales, out, K)
+    _compiled(_calls().lm_head_mxfp4, _index(hidden), stream, hidden, lm_head, scales, out, K)

@@ -163,7 +163,7 @@ def test_the_copies_of_a_signature_agree():
 def test_the_compiled_calls_check_their_arguments():
     import torch
     from markov_draft_sampling_amd import _serving
-    calls = _serving._calls
+    calls = _serving._calls()
     x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     for fn, n in ((calls.qk_norm_rope, 12), (calls.qk_norm_rope_append, 18), (calls.paged_attention, 19),
                   (calls.lm_head_mxfp4, 6)):
