@@ -239,8 +239,10 @@ hipError_t launch_lanes(const RopeArgs& a, hipStream_t st) {
     return hipGetLastError();
   };
   // Two heads a lane once the waves fill the CUs: sines, cosines and positions serve two, and twice the bytes are in flight
-  // (32 + 2 x 8 heads of 128, us with one / two / three: 16384 tokens 86 / 76 / 79, 1024 8.4 / 8.3 / 8.7, 256 3.8 / 4.3 / 5.3).
-  if ((long long)a.T * waves > 8192) return launch(rope_kernel<LPH, 2, TO>, 2);
+  // (us with one and two: 32 + 2 x 8 heads of 128, 24576 waves 21.5 and 19.4, 6144 7.5 and 7.5; 16 + 2 x 4 of 256, 6144
+  // 7.9 and 7.7; 8 + 2 x 2 of 128, 4096 5.0 and 5.2; 27 of 64, 4096 4.6 and 4.6, 2048 3.4 and 3.7. With three the
+  // prompt above takes 79 against 76).
+  if ((long long)a.T * waves > 4096) return launch(rope_kernel<LPH, 2, TO>, 2);
   return launch(rope_kernel<LPH, 1, TO>, 1);
 }
 
