@@ -15,8 +15,9 @@
 // border of two codes, the last bit of float32 decides. So that float32 decides
 // alike wherever a key is computed, every factor here is the float32 nearest to
 // its exact value (sine and cosine, 1 / sqrt), products are rounded one by one and
-// squares are summed in the columns' order, fours in turn and then neighbours.
-// (With float32 sines and fused products three codes in a million fell on the
+// squares are summed fours in turn and then neighbours (neighbouring columns,
+// but where only part of a head is turned and that in halves). (Heads of 128:
+// with float32 sines and fused products three codes in a million fell on the
 // other side than by separate operations, now none of 43 million; the prompt
 // below takes 76.1 us and took 75.3.)
 //
