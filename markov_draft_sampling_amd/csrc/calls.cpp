@@ -120,9 +120,14 @@ int small(int64_t n, const char* name) {
 // threads of the interpreter run meanwhile. It touches no Python object.
 template <typename F>
 PyObject* enqueue(const char* what, F call) {
-  PyThreadState* state = PyEval_SaveThread();
-  const int rc = call();
-  PyEval_RestoreThread(state);
+  struct Others {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Others() { PyEval_RestoreThread(state); }
+  };
+  const int rc = [&] {
+    Others run;
+    return call();
+  }();
   if (rc) {
     PyErr_Format(g_error, "%s: %s (%d): %s", what, mds_status_string(rc), rc, mds_last_error());
     return nullptr;

@@ -304,3 +304,41 @@ def test_refusals_of_the_binding():
                 dict(status=torch.zeros(2, device="cuda"))):
         with pytest.raises(mds.MdsError):
             mds.qk_norm_rope_append(**{**ok, **bad})
+
+
+def test_threads_of_the_interpreter():
+    # the calls let other threads run while they enqueue; errors belong to the thread whose call it was
+    import threading
+    import torch
+    import markov_draft_sampling_amd as mds
+    sets = [_inputs(32 + 8 * i, 8, 2, 128, 128, seed=i) for i in range(4)]
+    want = []
+    for s in sets:
+        q, k = torch.empty_like(s["q"]), torch.empty_like(s["k"])
+        mds.qk_norm_rope(s["q"], s["k"], s["pos"], s["freq"], q, k, q_weight=s["qw"], k_weight=s["kw"])
+        want.append((q, k))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        s, st = sets[i], torch.cuda.Stream()
+        q, k = torch.empty_like(s["q"]), torch.empty_like(s["k"])
+        try:
+            for n in range(100):
+                args = dict(q_weight=s["qw"], k_weight=s["kw"], stream=st)
+                if n % 10 == i:
+                    with pytest.raises(mds.MdsError, match="eps" if i % 2 else "rope_scale"):
+                        mds.qk_norm_rope(s["q"], s["k"], s["pos"], s["freq"], q, k, eps=-1.0 if i % 2 else 1e-6,
+                                         rope_scale=1.0 if i % 2 else float("nan"), **args)
+                mds.qk_norm_rope(s["q"], s["k"], s["pos"], s["freq"], q, k, **args)
+            st.synchronize()
+            assert torch.equal(q, want[i][0]) and torch.equal(k, want[i][1])
+        except BaseException as e:  # noqa: BLE001
+            failed.append((i, e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
