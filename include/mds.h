@@ -786,6 +786,14 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
                       void* stream);
 
 /*
+ * mds_debug_lm_head_mxfp4_plan - test hook (pure host function, no GPU needed):
+ * which kernel a call of these sizes takes, out [3]: 1 that for few rows or 0
+ * the wide one; groups of 4 rows (few: 1, 2, 4, 8) or blocks of 16 (wide: 1 to
+ * 7) a work-group; blocks of 16 vocabulary rows a work-group (few) or wave (wide).
+ */
+int mds_debug_lm_head_mxfp4_plan(int B, int K, int V, int H, int32_t* out);
+
+/*
  * mds_call_packed - one of the serving calls from an array of its arguments
  * (all but the stream, in their order, 8 bytes each: integers and pointers as
  * int64, a float as the bits of a double), for bindings in which every argument

@@ -255,4 +255,15 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
   return e == hipSuccess ? abi_ok() : hip_fail(e);
 }
 
+int mds_debug_lm_head_mxfp4_plan(int B, int K, int V, int H, int32_t* out) {
+  int rc, rows;
+  if ((rc = check_lm_head_rows(B, K, &rows)) || (rc = check_lm_head_matrix(V, H))) return rc;
+  if (!out) return abi_fail(MDS_ERR_INVALID_ARG, "out is NULL");
+  const mds::LmHeadMxPlan p = mds::lm_head_mx_plan(rows, V);
+  out[0] = p.few;
+  out[1] = p.height;
+  out[2] = p.nbw;
+  return abi_ok();
+}
+
 }  // extern "C"

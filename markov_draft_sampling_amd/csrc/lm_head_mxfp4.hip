@@ -475,12 +475,13 @@ hipError_t launch_few(const LmHeadMxArgs& a, hipStream_t st) {
 // Vocabulary blocks of a work-group: four, so that the hidden rows are read less often, but fewer where that leaves CUs
 // without one, and for up to 4 rows, which cost little (H = 4096, us with one / two / four: 16 rows, V = 4099 8.5 / 9.6 /
 // 12.0, V = 32000 28 / 22 / 20; H = 2048, 4 rows, V = 151936 33 / 32 / 33, one row 33 / 29 / 32).
+int few_blocks(int VB, int ng) { return VB <= 512 ? 1 : ng == 1 || VB <= 1024 ? 2 : 4; }
 template <int NG>
-hipError_t launch_few_rows(const LmHeadMxArgs& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4;
-  if (VB <= 512) return launch_few<NG, 1>(a, st);
-  if constexpr (NG == 1) return launch_few<NG, 2>(a, st);
-  return VB <= 1024 ? launch_few<NG, 2>(a, st) : launch_few<NG, 4>(a, st);
+hipError_t launch_few_rows(const LmHeadMxArgs& a, int nbw, hipStream_t st) {
+  if (nbw == 1) return launch_few<NG, 1>(a, st);
+  if constexpr (NG > 1)
+    if (nbw == 4) return launch_few<NG, 4>(a, st);
+  return launch_few<NG, 2>(a, st);
 }
 
 template <int MB, int NBW>
@@ -514,46 +515,52 @@ int wide_row_tiles(int VB, int n) {
 }
 
 template <int MB>
-hipError_t launch_rows(const LmHeadMxArgs& a, int mt, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4;
-  const int nbw = wide_blocks(VB, mt, MB), tiles = (VB + 4 * nbw - 1) / (4 * nbw);
+hipError_t launch_rows(const LmHeadMxArgs& a, const LmHeadMxPlan& p, hipStream_t st) {
   if constexpr (MB <= 4) {
-    if (nbw == 6) return launch_wide<MB, 6>(a, tiles, mt, st);
-    if (nbw == 7) return launch_wide<MB, 7>(a, tiles, mt, st);
+    if (p.nbw == 6) return launch_wide<MB, 6>(a, p.v_tiles, p.row_tiles, st);
+    if (p.nbw == 7) return launch_wide<MB, 7>(a, p.v_tiles, p.row_tiles, st);
   }
-  switch (nbw) {
-    case 1: return launch_wide<MB, 1>(a, tiles, mt, st);
-    case 2: return launch_wide<MB, 2>(a, tiles, mt, st);
-    case 3: return launch_wide<MB, 3>(a, tiles, mt, st);
-    case 4: return launch_wide<MB, 4>(a, tiles, mt, st);
-    default: return launch_wide<MB, 5>(a, tiles, mt, st);
+  switch (p.nbw) {
+    case 1: return launch_wide<MB, 1>(a, p.v_tiles, p.row_tiles, st);
+    case 2: return launch_wide<MB, 2>(a, p.v_tiles, p.row_tiles, st);
+    case 3: return launch_wide<MB, 3>(a, p.v_tiles, p.row_tiles, st);
+    case 4: return launch_wide<MB, 4>(a, p.v_tiles, p.row_tiles, st);
+    default: return launch_wide<MB, 5>(a, p.v_tiles, p.row_tiles, st);
   }
 }
 
 }  // namespace
 
-hipError_t launch_lm_head_mx(const LmHeadMxArgs& a, hipStream_t st) {
-  const int VB = (a.V + 15) >> 4, n = (a.M + 15) >> 4;
+LmHeadMxPlan lm_head_mx_plan(int M, int V) {
+  const int VB = (V + 15) >> 4, n = (M + 15) >> 4;
   const int tiles = wide_row_tiles(VB, n), mb = (n + tiles - 1) / tiles, mt = (n + mb - 1) / mb;
+  const int nbw = wide_blocks(VB, mt, mb);
   // Up to 32 rows either kernel: the few rows' takes a start and a time by the vocabulary that grows with the rows, in
   // wide_cost's units (H = 4096, us few / wide: 7 rows, V = 200064 81 / 95, V = 151936 63 / 59; 16 rows, V = 100003 54 / 48,
   // V = 32000 20 / 24; 32 rows, V = 200064 117 / 104, V = 4099 12.5 / 16.7).
-  if (a.M <= 32) {
-    const float few = 0.5f + (a.M <= 4 ? 0.55e-3f : a.M <= 8 ? 0.61e-3f : a.M <= 16 ? 0.71e-3f : 0.88e-3f) * (float)VB;
-    if (few < wide_cost(VB, mt, wide_blocks(VB, mt, mb))) {
-      if (a.M <= 4) return launch_few_rows<1>(a, st);
-      if (a.M <= 8) return launch_few_rows<2>(a, st);
-      return a.M <= 16 ? launch_few_rows<4>(a, st) : launch_few_rows<8>(a, st);
-    }
+  if (M <= 32) {
+    const float few = 0.5f + (M <= 4 ? 0.55e-3f : M <= 8 ? 0.61e-3f : M <= 16 ? 0.71e-3f : 0.88e-3f) * (float)VB;
+    const int ng = M <= 4 ? 1 : M <= 8 ? 2 : M <= 16 ? 4 : 8;
+    if (few < wide_cost(VB, mt, nbw)) return {true, ng, few_blocks(VB, ng), 0, 0};
   }
-  switch (mb) {
-    case 1: return launch_rows<1>(a, mt, st);
-    case 2: return launch_rows<2>(a, mt, st);
-    case 3: return launch_rows<3>(a, mt, st);
-    case 4: return launch_rows<4>(a, mt, st);
-    case 5: return launch_rows<5>(a, mt, st);
-    case 6: return launch_rows<6>(a, mt, st);
-    default: return launch_rows<7>(a, mt, st);
+  return {false, mb, nbw, mt, (VB + 4 * nbw - 1) / (4 * nbw)};
+}
+
+hipError_t launch_lm_head_mx(const LmHeadMxArgs& a, hipStream_t st) {
+  const LmHeadMxPlan p = lm_head_mx_plan(a.M, a.V);
+  if (p.few) {
+    if (p.height == 1) return launch_few_rows<1>(a, p.nbw, st);
+    if (p.height == 2) return launch_few_rows<2>(a, p.nbw, st);
+    return p.height == 4 ? launch_few_rows<4>(a, p.nbw, st) : launch_few_rows<8>(a, p.nbw, st);
+  }
+  switch (p.height) {
+    case 1: return launch_rows<1>(a, p, st);
+    case 2: return launch_rows<2>(a, p, st);
+    case 3: return launch_rows<3>(a, p, st);
+    case 4: return launch_rows<4>(a, p, st);
+    case 5: return launch_rows<5>(a, p, st);
+    case 6: return launch_rows<6>(a, p, st);
+    default: return launch_rows<7>(a, p, st);
   }
 }
 

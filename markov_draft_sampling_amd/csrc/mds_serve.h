@@ -158,6 +158,14 @@ struct LmHeadMxArgs {
   long long out_rs, out_ss;
   int out_bf16, vec_out;
 };
+// Which kernel a call of M rows takes: that for few rows, of height (1, 2, 4, 8) groups of four, or the wide one, of
+// height (1 to 7) 16-row blocks a work-group; nbw: vocabulary blocks of a work-group (few) or of each of its waves; the wide
+// one's tiles.
+struct LmHeadMxPlan {
+  bool few;
+  int height, nbw, row_tiles, v_tiles;
+};
+LmHeadMxPlan lm_head_mx_plan(int M, int V);
 hipError_t launch_lm_head_mx(const LmHeadMxArgs& a, hipStream_t st);
 hipError_t launch_tile_mx(int V, int H, const uint8_t* codes, const uint8_t* scales, uint8_t* tiled, uint8_t* tiled_scales,
                           hipStream_t st);
