@@ -631,6 +631,13 @@ int mds_qk_norm_rope_append(int T, int Hq, int Hkv, int D, int R, const void* q,
                             void* stream);
 
 /*
+ * mds_debug_qk_norm_rope_plan - test hook (pure host function, no GPU needed):
+ * which kernel a call of these sizes takes (append: mds_qk_norm_rope_append),
+ * out [2]: lanes of a head (4, 8, 16), heads a lane takes (1, 2).
+ */
+int mds_debug_qk_norm_rope_plan(int T, int Hq, int Hkv, int D, int append, int32_t* out);
+
+/*
  * mds_paged_attention - attention of every request's new tokens over its cache
  * (the new tokens' own keys and values included: append them first).
  *

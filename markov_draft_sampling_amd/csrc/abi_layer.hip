@@ -27,16 +27,24 @@ int check_out(const void* p, int T, int64_t ts, int H, int64_t hs, int D) {
   return MDS_OK;
 }
 
+// The sizes of both rotations
+int check_rope_sizes(int T, int Hq, int Hk, int D, int per_key_head) {
+  int rc;
+  if (T < 0 || T > (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "T must be in [0, 2^24]");
+  if ((rc = check_heads(Hk, D))) return rc;
+  if (Hq < 1 || Hq > 1024) return abi_fail(MDS_ERR_INVALID_ARG, "query heads must be in [1, 1024]");
+  if (D % 16 || D > 256) return abi_fail(MDS_ERR_UNSUPPORTED, "the head dimension must be a multiple of 16, at most 256");
+  if ((long long)T * (Hq + per_key_head * Hk) >= 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many heads in one call");
+  return MDS_OK;
+}
+
 // What both calls have in common; fills a
 int check_rope(mds::RopeArgs& a, int T, int Hq, int Hk, int D, int R, const void* q, int64_t q_ts, int64_t q_hs,
                const void* k, int64_t k_ts, int64_t k_hs, const int64_t* positions, const double* inv_freq,
                const void* q_weight, const void* k_weight, float eps, double rope_scale, int interleaved, void* q_out,
                int64_t qo_ts, int64_t qo_hs, int per_key_head) {
   int rc;
-  if (T < 0 || T > (1 << 24)) return abi_fail(MDS_ERR_INVALID_ARG, "T must be in [0, 2^24]");
-  if ((rc = check_heads(Hk, D))) return rc;
-  if (Hq < 1 || Hq > 1024) return abi_fail(MDS_ERR_INVALID_ARG, "query heads must be in [1, 1024]");
-  if (D % 16 || D > 256) return abi_fail(MDS_ERR_UNSUPPORTED, "the head dimension must be a multiple of 16, at most 256");
+  if ((rc = check_rope_sizes(T, Hq, Hk, D, per_key_head))) return rc;
   if (R < 0 || R > D) return abi_fail(MDS_ERR_INVALID_ARG, "the rotated part must be in [0, D]");
   if (R % 16) return abi_fail(MDS_ERR_UNSUPPORTED, "the rotated part must be a multiple of 16");
   if ((T && (!q || !k || !q_out || !positions)) || (R && !inv_freq))
@@ -46,7 +54,6 @@ int check_rope(mds::RopeArgs& a, int T, int Hq, int Hk, int D, int R, const void
   if (interleaved != 0 && interleaved != 1) return abi_fail(MDS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8))
     return abi_fail(MDS_ERR_INVALID_ARG, "weights must be 16-byte aligned, positions and frequencies 8-byte aligned");
-  if ((long long)T * (Hq + per_key_head * Hk) >= 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many heads in one call");
   a.q_ts = step(T, q_ts);
   a.q_hs = step(Hq, q_hs);
   a.k_ts = step(T, k_ts);
@@ -164,6 +171,16 @@ int mds_qk_norm_rope_append(int T, int Hq, int Hkv, int D, int R, const void* q,
   a.status = status;
   const hipError_t e = mds::launch_rope(a, (hipStream_t)stream);
   return e == hipSuccess ? abi_ok() : hip_fail(e);
+}
+
+int mds_debug_qk_norm_rope_plan(int T, int Hq, int Hkv, int D, int append, int32_t* out) {
+  int rc;
+  if ((rc = check_rope_sizes(T, Hq, Hkv, D, append ? 2 : 1))) return rc;
+  if (!out) return abi_fail(MDS_ERR_INVALID_ARG, "out is NULL");
+  const mds::RopePlan p = mds::rope_plan(T, Hq + (append ? 2 : 1) * Hkv, D);
+  out[0] = p.lanes;
+  out[1] = p.heads;
+  return abi_ok();
 }
 
 int mds_lm_head_mxfp4_bytes(int V, int H, size_t* code_bytes, size_t* scale_bytes) {

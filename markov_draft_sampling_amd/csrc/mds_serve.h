@@ -74,6 +74,12 @@ struct RopeArgs {
   const float* v_scale;
   uint32_t* status;
 };
+// How the heads (those of queries, keys and, with pages, values) of T tokens are dealt out: lanes of a head, heads a lane
+// takes, waves of a token.
+struct RopePlan {
+  int lanes, heads, per_token;
+};
+RopePlan rope_plan(int T, int heads, int D);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
 
 struct PagedAttnArgs {

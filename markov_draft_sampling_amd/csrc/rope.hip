@@ -228,33 +228,37 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
   }
 }
 
+template <int LPH, int U, int TO>
+hipError_t launch(const RopeArgs& a, const RopePlan& p, hipStream_t st) {
+  const long long n = (long long)a.T * p.per_token;
+  hipLaunchKernelGGL((rope_kernel<LPH, U, TO>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, a, p.per_token);
+  return hipGetLastError();
+}
 template <int LPH, int TO>
-hipError_t launch_lanes(const RopeArgs& a, hipStream_t st) {
-  constexpr int HPW = 64 / LPH;
-  const int heads = a.Hq + (TO == kRows ? a.Hk : 2 * a.Hk);
-  const int waves = (heads + HPW - 1) / HPW;  // of a token, at one head a lane
-  auto launch = [&](auto kernel, int u) {
-    const int per_token = (waves + u - 1) / u;
-    const long long n = (long long)a.T * per_token;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, a, per_token);
-    return hipGetLastError();
-  };
+hipError_t launch_lanes(const RopeArgs& a, const RopePlan& p, hipStream_t st) {
+  return p.heads == 2 ? launch<LPH, 2, TO>(a, p, st) : launch<LPH, 1, TO>(a, p, st);
+}
+template <int TO>
+hipError_t launch_to(const RopeArgs& a, hipStream_t st) {
+  const RopePlan p = rope_plan(a.T, a.Hq + (TO == kRows ? a.Hk : 2 * a.Hk), a.D);
+  if (p.lanes == 4) return launch_lanes<4, TO>(a, p, st);
+  return p.lanes == 8 ? launch_lanes<8, TO>(a, p, st) : launch_lanes<16, TO>(a, p, st);
+}
+
+}  // namespace
+
+RopePlan rope_plan(int T, int heads, int D) {
+  RopePlan p;
+  p.lanes = D <= 64 ? 4 : D <= 128 ? 8 : 16;
+  const int waves = (heads * p.lanes + 63) / 64;  // of a token, at one head a lane
   // Two heads a lane once the waves fill the CUs: sines, cosines and positions serve two, and twice the bytes are in flight
   // (us with one and two: 32 + 2 x 8 heads of 128, 24576 waves 21.5 and 19.4, 6144 7.5 and 7.5; 16 + 2 x 4 of 256, 6144
   // 7.9 and 7.7; 8 + 2 x 2 of 128, 4096 5.0 and 5.2; 27 of 64, 4096 4.6 and 4.6, 2048 3.4 and 3.7. With three the
   // prompt above takes 79 against 76).
-  if ((long long)a.T * waves > 4096) return launch(rope_kernel<LPH, 2, TO>, 2);
-  return launch(rope_kernel<LPH, 1, TO>, 1);
+  p.heads = (long long)T * waves > 4096 ? 2 : 1;
+  p.per_token = (waves + p.heads - 1) / p.heads;
+  return p;
 }
-
-template <int TO>
-hipError_t launch_to(const RopeArgs& a, hipStream_t st) {
-  if (a.D <= 64) return launch_lanes<4, TO>(a, st);
-  if (a.D <= 128) return launch_lanes<8, TO>(a, st);
-  return launch_lanes<16, TO>(a, st);
-}
-
-}  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t st) {
   if (!a.k_pages) return launch_to<kRows>(a, st);

@@ -14,3 +14,17 @@ MXFP4_HEAD = [
     (164003, (9, 17, 33, 50)),
     (200064, (5, 17, 33, 50, 65, 84, 100, 129, 161, 224)),
 ]
+
+# (T, Hq, Hkv, D, R, interleaved, norm, keys to, tokens of a short call): norm and rotation with two heads a lane, and in
+# short calls of the same tokens with one; wave counts of a token that are odd and one, lanes without columns
+ROPE = [
+    (1501, 30, 5, 64, 32, False, True, "rows", 400),
+    (1501, 20, 9, 48, 48, True, True, "bf16", 400),
+    (2101, 7, 5, 64, 64, False, False, "e4m3", 700),
+    (851, 30, 6, 128, 128, False, True, "rows", 300),
+    (1402, 9, 4, 80, 80, True, False, "bf16", 500),
+    (1403, 16, 4, 128, 64, False, True, "e4m3", 500),
+    (1404, 5, 4, 256, 128, True, True, "rows", 500),
+    (1405, 3, 3, 192, 192, False, True, "bf16", 500),
+    (4201, 1, 1, 256, 256, True, True, "e4m3", 2000),
+]

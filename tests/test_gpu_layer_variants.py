@@ -2,10 +2,13 @@
 GPU, at remainders of its tiles (the sizes: layer_cases.py)."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 import layer_cases as lc
 import layer_ref as lr
+import serving_ref as sr
+from test_gpu_rope import _check, _expected, _inputs, _pages
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +62,70 @@ def test_lm_head(V, some):
             tol += 2.0 ** -8 * (z.abs() + tol)
         err = (got[:n].double() - z).abs()
         assert (err <= tol).all(), (float((err / tol).max()), torch.nonzero(~(err <= tol))[:4].tolist())
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,R,interleaved,norm,to,short", lc.ROPE)
+def test_rotation(T, Hq, Hk, D, R, interleaved, norm, to, short):
+    import torch
+    import markov_draft_sampling_amd as mds
+    s = _inputs(T, Hq, Hk, D, R, norm, seed=T)
+    args = dict(q_weight=s["qw"], k_weight=s["kw"], interleaved=interleaved, rope_scale=1.1)
+    (rq, eq), (rk, ek) = _expected(s, 1.1, interleaved)
+    qo = torch.full((T + 2, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    parts = [slice(t, min(t + short, T)) for t in range(0, T, short)]
+    print(f"rotation T {T} heads {Hq}/{Hk} D {D} R {R} to {to}", flush=True)
+    if to == "rows":
+        ko = torch.full((T + 2, Hk, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        mds.qk_norm_rope(s["q"], s["k"], s["pos"], s["freq"], qo[:T], ko[:T], **args)
+        _check(qo[:T], rq, eq)
+        _check(ko[:T], rk, ek)
+        assert (qo[T:] == 7).all() and (ko[T:] == 7).all()
+        q2, k2 = torch.empty_like(s["q"]), torch.empty_like(s["k"])
+        for p in parts:
+            mds.qk_norm_rope(s["q"][p], s["k"][p], s["pos"][p], s["freq"], q2[p], k2[p], **args)
+        assert torch.equal(q2, qo[:T]) and torch.equal(k2, ko[:T])
+        mds.qk_norm_rope(s["q"], s["k"], s["pos"], s["freq"], s["q"], s["k"], **args)  # over its own input
+        assert torch.equal(s["q"], qo[:T]) and torch.equal(s["k"], ko[:T])
+        return
+    rng = np.random.default_rng(T)
+    P, NP = 32, -(-T // 32) + 2
+    slot = rng.permutation(NP * P)[:T].astype(np.int64)
+    slot[5], slot[T - 1], slot[T // 2] = -1, -9, NP * P  # two of padding, one past the cache
+    live = (slot >= 0) & (slot < NP * P)
+    ks = vs = None
+    if to == "e4m3":
+        ks, vs = (torch.tensor(rng.uniform(0.002, 0.03, Hk), dtype=torch.float32).cuda() for _ in range(2))
+    kp, vp = _pages(NP, P, Hk, D, to, "hnd", 1), _pages(NP, P, Hk, D, to, "nhd", 2)
+    k2, v2, q2 = kp.clone(), vp.clone(), torch.empty_like(s["q"])
+    raw = lambda t: t.view(torch.uint8 if to == "e4m3" else torch.int16)  # noqa: E731
+    k0, v0 = raw(kp).cpu().reshape(NP * P, Hk, D), raw(vp).cpu().reshape(NP * P, Hk, D)
+    sl = torch.from_numpy(slot).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mds.qk_norm_rope_append(s["q"], s["k"], s["v"], s["pos"], s["freq"], qo[:T], kp, vp, sl, k_scale=ks, v_scale=vs,
+                            status=status, **args)
+    assert int(status.item()) == mds.STATUS_BAD_PAGE
+    for p in parts:
+        mds.qk_norm_rope_append(s["q"][p], s["k"][p], s["v"][p], s["pos"][p], s["freq"], q2[p], k2, v2, sl[p], k_scale=ks,
+                                v_scale=vs, status=status, **args)
+    assert torch.equal(q2, qo[:T]) and torch.equal(raw(k2), raw(kp)) and torch.equal(raw(v2), raw(vp))
+    _check(qo[:T], rq, eq)  # of every token, those without a slot too
+    assert (qo[T:] == 7).all()
+    rest = np.setdiff1d(np.arange(NP * P), slot[live])
+    assert torch.equal(raw(kp).cpu().reshape(NP * P, Hk, D)[rest], k0[rest])
+    assert torch.equal(raw(vp).cpu().reshape(NP * P, Hk, D)[rest], v0[rest])
+    k, v = (x.float().cpu().reshape(NP * P, Hk, D)[slot[live]] for x in (kp, vp))
+    rk, ek, x = rk[live], ek[live], s["v"].cpu().float()[live]
+    if to == "bf16":
+        _check(k, rk, ek)
+        assert torch.equal(v, x)
+        return
+    # rounded once: half a step of a code (2^-4, or 2^-10 below the normal ones) on what float32 leaves of y / scale,
+    # as in test_gpu_rope.py
+    assert np.array_equal(v.numpy(), sr.e4m3_round((x / vs.cpu()[:, None]).numpy()))
+    sc = ks.cpu().double()[:, None]
+    z, fuzz = (rk / sc).clamp(-448, 448), (ek / sc + 2.0 ** -23 * (rk / sc).abs()) * 1.01
+    tol = torch.maximum(2.0 ** -4 * (z.abs() + fuzz), torch.tensor(2.0 ** -10)) + fuzz
+    assert ((k.double() - z).abs() <= tol).all()
+    lo, hi = sr.e4m3_round((z - fuzz).float().numpy()), sr.e4m3_round((z + fuzz).float().numpy())
+    sure = lo == hi
+    assert sure.mean() > 0.99 and (k.double().numpy()[sure] == lo[sure]).all()
