@@ -713,6 +713,15 @@ int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* 
                               void* stream);
 
 /*
+ * mds_debug_paged_attention_plan - test hook (pure host function, no GPU needed):
+ * how a call of these sizes is cut, out [4]: rows of a tile (16, 32, 64, 128),
+ * key groups of a work-group (1, 2, 4), chunks of keys, keys of a chunk. T and
+ * max_q_len >= 1.
+ */
+int mds_debug_paged_attention_plan(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len, int window,
+                                   int sinks, int cache_dtype, int32_t* out);
+
+/*
  * The LM head from an 8-bit matrix: lm_head [V, H] in MDS_E4M3 with one
  * float32 scale for each block of 128 rows by 128 columns, scales
  * [ceil(V / 128), H / 128] contiguous (weight = code * scale), H a multiple of

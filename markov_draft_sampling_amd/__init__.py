@@ -106,6 +106,7 @@ _SIGS = {
     "mds_quantize_lm_head_mxfp4": ([_c_int, _c_int, _vp, _vp, _c_sz, _vp, _c_sz, _vp], _c_int),
     "mds_unpack_lm_head_mxfp4": ([_c_int, _c_int, _vp, _vp, _vp, _vp], _c_int),
     "mds_lm_head_mxfp4": ([_c_int] * 4 + [_vp, _c_i64, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _vp], _c_int),
+    "mds_debug_paged_attention_plan": ([_c_int] * 6 + [_c_i64] + [_c_int] * 3 + [_vp], _c_int),
     "mds_debug_qk_norm_rope_plan": ([_c_int] * 5 + [_vp], _c_int),
     "mds_debug_lm_head_mxfp4_plan": ([_c_int] * 4 + [_vp], _c_int),
     "mds_call_packed": ([_c_int, ctypes.c_char_p, _c_int, _vp], _c_int),

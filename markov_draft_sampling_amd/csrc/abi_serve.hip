@@ -316,6 +316,23 @@ int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* 
   return e == hipSuccess ? abi_ok() : hip_fail(e);
 }
 
+int mds_debug_paged_attention_plan(int T, int B, int Hq, int Hkv, int D, int max_q_len, int64_t max_seq_len, int window,
+                                   int sinks, int cache_dtype, int32_t* out) {
+  int rc;
+  if ((rc = check_sinks(sinks)) || (rc = check_attention(T, B, Hq, Hkv, D, max_q_len, max_seq_len, window)) ||
+      (rc = check_cache_dtype(cache_dtype)))
+    return rc;
+  if (!out) return abi_fail(MDS_ERR_INVALID_ARG, "out is NULL");
+  if (T == 0 || max_q_len == 0) return abi_fail(MDS_ERR_INVALID_ARG, "a call of no tokens is not cut");
+  const mds::AttnPlan p = mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks),
+                                         window > 0 && sinks > 0, cache_dtype == MDS_E4M3);
+  out[0] = p.rows;
+  out[1] = p.key_groups;
+  out[2] = p.n_chunks;
+  out[3] = p.chunk;
+  return abi_ok();
+}
+
 int mds_paged_attention(int T, int B, int Hq, int Hkv, int D, const void* q, int64_t q_token_stride,
                         int64_t q_head_stride, const void* k_pages, const void* v_pages, int cache_dtype,
                         int page_size, int n_pages, int64_t k_page_stride, int64_t k_slot_stride,

@@ -2,12 +2,15 @@
 GPU, at remainders of its tiles (the sizes: layer_cases.py)."""
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import pytest
 
 import layer_cases as lc
 import layer_ref as lr
 import serving_ref as sr
+from test_gpu_attention_sinks import _case
 from test_gpu_rope import _check, _expected, _inputs, _pages
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +132,58 @@ def test_rotation(T, Hq, Hk, D, R, interleaved, norm, to, short):
     lo, hi = sr.e4m3_round((z - fuzz).float().numpy()), sr.e4m3_round((z + fuzz).float().numpy())
     sure = lo == hi
     assert sure.mean() > 0.99 and (k.double().numpy()[sure] == lo[sure]).all()
+
+
+_ATTENTION = [pytest.param(*c[1:], D, cache, id=f"{c[0][0]}rows-{c[0][1 + (cache == 'e4m3')]}groups-"
+                           f"{'split' if c[0][3] else 'whole'}-{D}-{cache}")
+              for c in lc.ATTENTION_SINKS for D in (64, 128) for cache in ("bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("ctx,chunk,Hq,Hk,P,window,sinks,more,D,cache", _ATTENTION)
+def test_attention(ctx, chunk, Hq, Hk, P, window, sinks, more, D, cache):
+    # against float64, with NaN in every page and behind every end that no row sees
+    _case(ctx, chunk, Hq, Hk, D, P, window, sinks, cache=cache, seed=Hq + D, **more)
+
+
+@pytest.mark.parametrize("ctx,chunk,Hq,Hk,P,window,sinks,more,D,cache", _ATTENTION)
+def test_attention_with_values_that_are_no_numbers(ctx, chunk, Hq, Hk, P, window, sinks, more, D, cache):
+    # of the first key, which all see, of the key in the middle of a request's new tokens, and of one that the window of only
+    # some of its tokens reaches: each reaches the rows that see it, in its own column, and no others
+    import torch
+    import markov_draft_sampling_amd as mds
+    causal = more.get("causal", True)
+    g = torch.Generator().manual_seed(Hq)
+    seq = [a + n for a, n in zip(ctx, chunk)]
+    MP = -(-max(seq) // P)
+    used = sum(-(-x // P) for x in seq)
+    kind = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
+    kp, vp = (torch.randn((used, P, Hk, D), generator=g).to(kind) for _ in range(2))
+    raw = vp.view(torch.uint8 if cache == "e4m3" else torch.int16)
+    nan, inf = (0x7F, 0x7F) if cache == "e4m3" else (0x7FC0, 0x7F80)  # (e4m3 has no infinities)
+    table = torch.full((len(ctx), MP), -1, dtype=torch.int32)
+    expect = torch.zeros((sum(chunk), 3), dtype=torch.bool)
+    at = t0 = 0
+    for b, (c, n) in enumerate(zip(ctx, chunk)):
+        held = -(-seq[b] // P)
+        table[b, :held] = torch.arange(at, at + held, dtype=torch.int32)
+        pos = torch.arange(c, c + n)
+        for i, key in enumerate((0, c + n // 2, max(0, c - window + 1 + n // 2)) if n else ()):
+            seen = (key <= pos) if causal else torch.ones(n, dtype=torch.bool)
+            expect[t0:t0 + n, i] = seen & ((key > pos - window) | (key < sinks))
+            raw[at + key // P, key % P, :, 5 + 20 * i] = inf if i == 1 else nan
+        at, t0 = at + held, t0 + n
+    T = sum(chunk)
+    q = torch.randn((T, Hq, D), generator=g).to(torch.bfloat16).cuda()
+    out = torch.zeros_like(q)
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    starts = t(np.concatenate([[0], np.cumsum(chunk)]).tolist())
+    ws = mds.paged_attention(q, kp.cuda(), vp.cuda(), table.cuda(), starts, t(seq), out, max(chunk), max(seq), window=window,
+                             sinks=sinks, causal=causal)
+    assert mds.workspace_status(ws) == 0
+    o = out.float().cpu()
+    for i in range(3):
+        x, hit = o[:, :, 5 + 20 * i], expect[:, i]
+        assert (x[hit] == math.inf if i == 1 and cache == "bf16" else x[hit].isnan()).all(), i
+        assert x[~hit].isfinite().all(), i
+    rest = [d for d in range(D) if d not in (5, 25, 45)]
+    assert o[:, :, rest].isfinite().all()
