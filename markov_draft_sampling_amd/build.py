@@ -5,10 +5,12 @@
 Each source is compiled by hipcc in parallel, then linked into a shared
 library next to this file. Packed fp32 instructions are disabled for device
 code. The binding's compiled calls (csrc/calls.cpp, against torch's headers)
-become the module _calls beside it.
+become the module _calls beside it; without torch the library is built alone.
+Both are put in place together, once both are built.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -41,16 +43,33 @@ def _hipcc() -> str:
     return exe
 
 
-def _calls_command(out: str):
-    """How the module of the binding's compiled calls is built."""
-    import importlib.util
+def _calls_command(lib: str, out: str):
+    """How the module of the binding's compiled calls is built against the library, or None without torch."""
     import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     include = os.path.join(torch, "include")
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-o", out, os.path.join(CSRC, "calls.cpp"),
+    cxx = ["g++"] if shutil.which("g++") else [_hipcc(), "-x", "c++", "-no-hip-rt"]
+    return [*cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-o", out, os.path.join(CSRC, "calls.cpp"),
             "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
-            "-isystem", sysconfig.get_paths()["include"], "-L", HERE, "-L", os.path.join(torch, "lib"), "-l:libmds.so",
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+            "-isystem", sysconfig.get_paths()["include"], "-L", os.path.dirname(lib), "-L", os.path.join(torch, "lib"),
+            "-l:" + os.path.basename(lib), "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+
+
+def _link(cmd, what: str, verbose: bool):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + r.stdout + r.stderr)
+
+
+def _remove(*paths):
+    for path in paths:
+        if os.path.exists(path):
+            os.remove(path)
 
 
 def build(verbose: bool = False) -> str:
@@ -76,19 +95,22 @@ def build(verbose: bool = False) -> str:
             print(out)
     if errors:
         raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
-    tmp = LIB + ".tmp"
-    cmd = [hipcc, f"--offload-arch={ARCH}", "-shared", "-Wl,--no-undefined", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
-    os.replace(tmp, LIB)
-    cmd = _calls_command(CALLS + ".tmp")
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("building the binding's calls failed:\n" + r.stdout + r.stderr)
-    os.replace(CALLS + ".tmp", CALLS)
+    lib, calls = LIB + ".tmp", CALLS + ".tmp"
+    try:
+        _link([hipcc, f"--offload-arch={ARCH}", "-shared", "-Wl,--no-undefined", "-Wl,-soname,libmds.so", "-o", lib, *objs],
+              "link", verbose)
+        cmd = _calls_command(lib, calls)
+        if cmd:
+            _link(cmd, "building the binding's calls", verbose)
+        else:  # a module of before would call this library by another one's signatures
+            print("torch is not installed: libmds.so is built alone, without the module of the binding's compiled calls",
+                  file=sys.stderr, flush=True)
+            _remove(CALLS)
+        os.replace(lib, LIB)
+        if cmd:
+            os.replace(calls, CALLS)
+    finally:
+        _remove(lib, calls)
     return LIB
 
 
