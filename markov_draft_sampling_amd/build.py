@@ -55,7 +55,7 @@ def _calls_command(lib: str, out: str):
     return [*cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-o", out, os.path.join(CSRC, "calls.cpp"),
             "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], "-L", os.path.dirname(lib), "-L", os.path.join(torch, "lib"),
-            "-l:" + os.path.basename(lib), "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+            "-l:libmds.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
 
 
 def _link(cmd, what: str, verbose: bool):
@@ -95,10 +95,9 @@ def build(verbose: bool = False) -> str:
             print(out)
     if errors:
         raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
-    lib, calls = LIB + ".tmp", CALLS + ".tmp"
+    lib, calls = (os.path.join(BUILD, os.path.basename(path)) for path in (LIB, CALLS))
     try:
-        _link([hipcc, f"--offload-arch={ARCH}", "-shared", "-Wl,--no-undefined", "-Wl,-soname,libmds.so", "-o", lib, *objs],
-              "link", verbose)
+        _link([hipcc, f"--offload-arch={ARCH}", "-shared", "-Wl,--no-undefined", "-o", lib, *objs], "link", verbose)
         cmd = _calls_command(lib, calls)
         if cmd:
             _link(cmd, "building the binding's calls", verbose)

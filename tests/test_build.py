@@ -3,6 +3,8 @@ put in place (no GPU), on sources of a few lines."""
 import glob
 import os
 import shutil
+import subprocess
+import sys
 
 import pytest
 
@@ -45,9 +47,9 @@ def test_both_are_put_in_place(tree, monkeypatch, gxx):
     assert b.build() == b.LIB
     assert not _old(b.LIB) and not _old(b.CALLS)
     assert _left(tree) == sorted(map(os.path.basename, (b.LIB, b.CALLS)))
-    import ctypes
-    import torch  # noqa: F401  (whose libraries the module is linked against)
-    assert ctypes.CDLL(b.CALLS).asked() == 42  # finds the library beside it, by its final name
+    # it finds the library beside it, by its final name (in a process of its own: this one may have loaded the real ones)
+    code = f"import ctypes, torch; assert ctypes.CDLL({b.CALLS!r}).asked() == 42"
+    subprocess.run([sys.executable, "-c", code], check=True)
 
 
 @pytest.mark.parametrize("source", ["lib.hip", "calls.cpp"])
