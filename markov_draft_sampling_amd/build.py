@@ -10,17 +10,19 @@ Both are put in place together, once both are built.
 """
 from __future__ import annotations
 
+import glob
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmds.so")
-CALLS = os.path.join(HERE, "_calls.so")
+CALLS = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))  # (for this interpreter alone)
 SOURCES = ("abi.hip", "abi_layer.hip", "abi_serve.hip", "draft.hip", "draft_wave.hip", "draft_topk.hip", "kv_cache.hip", "lm_head.hip",
            "lm_head_fp8.hip", "lm_head_mxfp4.hip", "paged_attention.hip", "rope.hip", "verify.hip", "topp.hip")
 ARCH = "gfx950"
@@ -45,7 +47,6 @@ def _hipcc() -> str:
 
 def _calls_command(lib: str, out: str):
     """How the module of the binding's compiled calls is built against the library, or None without torch."""
-    import sysconfig
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
@@ -101,10 +102,11 @@ def build(verbose: bool = False) -> str:
         cmd = _calls_command(lib, calls)
         if cmd:
             _link(cmd, "building the binding's calls", verbose)
-        else:  # a module of before would call this library by another one's signatures
+        else:
             print("torch is not installed: libmds.so is built alone, without the module of the binding's compiled calls",
                   file=sys.stderr, flush=True)
-            _remove(CALLS)
+        # modules of before (of other interpreters too) would call this library by another one's signatures
+        _remove(*(set(glob.glob(os.path.join(HERE, "_calls*.so"))) - ({CALLS} if cmd else set())))
         os.replace(lib, LIB)
         if cmd:
             os.replace(calls, CALLS)

@@ -5,8 +5,10 @@
 // the package's function of its name, checked against one device, and the
 // stream as a number; errors are the package's MdsError.
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cmath>
+#include <cstring>
 #include <stdexcept>
 #include <string>
 
@@ -306,9 +308,29 @@ PyMethodDef g_methods[] = {method<qk_norm_rope>("qk_norm_rope"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
+// Whether the library and torch that are loaded are those whose declarations this was compiled with
+bool fits() {
+  if (mds_abi_version() != MDS_ABI_VERSION) {
+    PyErr_Format(PyExc_ImportError, "built for version %d of the library's interface, which is %d", MDS_ABI_VERSION,
+                 mds_abi_version());
+    return false;
+  }
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  const char* v = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const size_t n = sizeof(TORCH_VERSION) - 1;
+  // (2.10.0, and 2.10.0+rocm7.0, but not 2.10.01)
+  const bool same = v && strncmp(v, TORCH_VERSION, n) == 0 && !(v[n] >= '0' && v[n] <= '9');
+  if (v && !same) PyErr_Format(PyExc_ImportError, "built with torch %s, not %s", TORCH_VERSION, v);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return same;
+}
+
 }  // namespace
 
 PyMODINIT_FUNC PyInit__calls() {
+  if (!fits()) return nullptr;
   PyObject* m = PyModule_Create(&g_module);
   if (!m) return nullptr;
   Py_INCREF(PyExc_RuntimeError);
