@@ -6,6 +6,7 @@ functions, which re-exports these.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import struct
 
@@ -20,7 +21,8 @@ _c_sz = ctypes.c_size_t
 # These calls take a few microseconds on the GPU at decoding sizes, so the checks here are kept cheap: a device is
 # compared by its index, pointers are plain integers (0: NULL), the stream is asked for once, and the arguments of the
 # calls of a step go over packed (39 ctypes arguments cost 3.6 us, packed 0.9). Those whose checks would
-# outlast their kernels all the same are checked and called by _calls, which is compiled.
+# outlast their kernels all the same are checked and called by _calls, which is compiled; where it is not built, attention
+# is called from here (10 us of host time instead of 7) and the others raise an error that says so.
 
 
 def _current_stream(index):
@@ -62,11 +64,13 @@ def _packed(what, index, stream, args):
 _CALLS = None
 
 
-def _calls():
-    """The module of the compiled calls."""
+def _calls(needed=True):
+    """The module of the compiled calls; None where there is none for this interpreter and it is not needed."""
     global _CALLS
     if _CALLS is None:
         _lib()
+        if not needed and importlib.util.find_spec("._calls", __package__) is None:
+            return None
         try:
             from . import _calls as m
         except ImportError as e:
@@ -291,9 +295,50 @@ def paged_attention(q, k_pages, v_pages, block_table, query_start, seq_lens, out
         nbytes = paged_attention_workspace_bytes(T, seq_lens.numel(), Hq, k_pages.shape[2], D, max_q_len, max_seq_len,
                                                  window, sinks)
         workspace = _new_workspace(nbytes, dev, stream)
-    _compiled(_calls().paged_attention, dev, stream, q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len,
-              max_seq_len, scale, causal, window, sinks, idx_map, k_scale, v_scale, lse, workspace)
+    args = (q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len, max_seq_len, scale, causal, window,
+            sinks, idx_map, k_scale, v_scale, lse, workspace)
+    calls = _calls(needed=False)
+    if calls is None:
+        _attention(dev, stream, *args)
+    else:
+        _compiled(calls.paged_attention, dev, stream, *args)
     return workspace
+
+
+def _heads(t, shape, index, name):
+    """(pointer, token stride, head stride) of bf16 [T, H, D] with a unit last stride."""
+    st = t.stride()
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or (st[2] != 1 and t.numel()):
+        raise MdsError(f"{name} must be bf16 {list(shape)} with a unit last stride on cuda:{index}")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _attention(dev, stream, q, k_pages, v_pages, block_table, query_start, seq_lens, out, max_q_len, max_seq_len, scale,
+               causal, window, sinks, idx_map, k_scale, v_scale, lse, workspace):
+    """_calls' paged_attention, in Python."""
+    (NP, P, Hk, D), code, kp, vp = _pages(k_pages, v_pages, dev)
+    _need(q.dim() == 3, "q must be bf16 [T, Hq, D]")
+    T, Hq, _ = q.shape
+    B = seq_lens.numel()
+    _need(block_table.dim() == 2, "block_table must be [n_slots, max_pages]")
+    N, MP = block_table.shape
+    _check_workspace(workspace, dev)
+    args = (T, B, Hq, Hk, D, *_heads(q, (T, Hq, D), dev, "q"), k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, *kp[:3],
+            *vp[:3], _vec(block_table, _I32, N * MP, dev, "block_table"), N, MP, _opt(idx_map, _I32, B, dev, "idx_map"),
+            _vec(query_start, _I32, B + 1, dev, "query_start"), _vec(seq_lens, _I32, B, dev, "seq_lens"), max_q_len,
+            max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, sinks,
+            _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
+            *_heads(out, (T, Hq, D), dev, "out"), _opt(lse, _F32, T * Hq, dev, "lse"), workspace.data_ptr(), workspace.numel())
+    try:
+        _ATTENTION.pack(*args)  # (ctypes would cut integers to their types' size)
+    except struct.error as e:
+        raise MdsError(f"paged_attention: an argument is no integer or out of range: {e}") from None
+    _call("paged_attention", _lib().mds_paged_attention_sinks, dev, stream, args)
+
+
+# the types and ranges of mds_paged_attention_sinks' arguments
+_ATTENTION = struct.Struct("=" + "".join({ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "d"}.get(t, "Q")
+                                         for t in _SIGS["mds_paged_attention_sinks"][0][:-1]))
 
 
 def lm_head_fp8_tiled_bytes(V, H) -> int:
