@@ -596,7 +596,9 @@ int mds_kv_append(int T, int Hkv, int D, const void* k, int64_t k_token_stride, 
  * frequencies: linear, by another base, or by parts with rope_scale as its factor
  * on cosine and sine.
  *   q, k          bf16 [T, Hq, D], [T, Hkv, D] (strides as k in mds_kv_append),
- *                 D a multiple of 16, at most 256 (else MDS_ERR_UNSUPPORTED)
+ *                 D a multiple of 16, at most 256 (else MDS_ERR_UNSUPPORTED);
+ *                 T times the heads that the call writes below 2^31, and, D taken as
+ *                 64, 128 or 256, 2^37 columns at most (else MDS_ERR_UNSUPPORTED)
  *   R             a multiple of 16 (else MDS_ERR_UNSUPPORTED), 0 <= R <= D (0: the norm alone)
  *   positions     int64 [T]; inv_freq double [R / 2], radians a position
  *   q_weight, k_weight  bf16 [D], 16-byte aligned, or NULL

@@ -27,6 +27,9 @@ int check_out(const void* p, int T, int64_t ts, int H, int64_t hs, int D) {
   return MDS_OK;
 }
 
+// Work-groups of 256 threads that a launch can have: its threads are counted in 32 bits
+bool launchable(long long groups) { return groups < (1LL << 24); }
+
 // The sizes of both rotations
 int check_rope_sizes(int T, int Hq, int Hk, int D, int per_key_head) {
   int rc;
@@ -34,7 +37,9 @@ int check_rope_sizes(int T, int Hq, int Hk, int D, int per_key_head) {
   if ((rc = check_heads(Hk, D))) return rc;
   if (Hq < 1 || Hq > 1024) return abi_fail(MDS_ERR_INVALID_ARG, "query heads must be in [1, 1024]");
   if (D % 16 || D > 256) return abi_fail(MDS_ERR_UNSUPPORTED, "the head dimension must be a multiple of 16, at most 256");
-  if ((long long)T * (Hq + per_key_head * Hk) >= 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many heads in one call");
+  const int heads = Hq + per_key_head * Hk;
+  if ((long long)T * heads >= 0x7FFFFFFFLL || !launchable(((long long)T * mds::rope_plan(T, heads, D).per_token + 3) / 4))
+    return abi_fail(MDS_ERR_UNSUPPORTED, "too many heads in one call");
   return MDS_OK;
 }
 
