@@ -783,7 +783,8 @@ int mds_lm_head_fp8(int B, int K, int V, int H, const void* hidden, int64_t hidd
  * microscaling formats' rule); 32 columns with an infinity or NaN get s = 255.
  * mds_unpack_lm_head_mxfp4 gives the weights back in bf16 [V, H], which has them
  * exactly. All matrices contiguous, 16-byte aligned and not overlapping (tiled scales
- * 4-byte aligned, row-major ones of any alignment); one launch each.
+ * 4-byte aligned, row-major ones of any alignment); one launch each, for
+ * ceil(V / 16) * ceil(H / 512) below 2^24 (V * H up to 2^37; else MDS_ERR_UNSUPPORTED).
  */
 int mds_lm_head_mxfp4_bytes(int V, int H, size_t* code_bytes, size_t* scale_bytes);
 int mds_tile_lm_head_mxfp4(int V, int H, const void* codes, const void* scales, void* tiled, size_t tiled_bytes,

@@ -89,6 +89,14 @@ int check_rope(mds::RopeArgs& a, int T, int Hq, int Hk, int D, int R, const void
 size_t mx_code_bytes(int V, int H) { return (size_t)((V + 15) / 16) * 8 * H; }
 size_t mx_scale_bytes(int V, int H) { return (size_t)((V + 15) / 16) * 256 * ((H + 511) / 512); }
 
+// A matrix whose tiles are made or read back in one launch: a work-group for 16 rows and 512 columns
+int check_mx_matrix(int V, int H) {
+  const int rc = check_lm_head_matrix(V, H);
+  if (rc) return rc;
+  if (!launchable((long long)((V + 15) / 16) * ((H + 511) / 512))) return abi_fail(MDS_ERR_UNSUPPORTED, "the matrix is too large");
+  return MDS_OK;
+}
+
 int check_mx_tiled(int V, int H, const void* tiled, size_t tiled_bytes, const void* tiled_scales, size_t scale_bytes) {
   if (!tiled || !tiled_scales) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(tiled, 16) || !aligned(tiled_scales, 4))
@@ -200,7 +208,7 @@ int mds_lm_head_mxfp4_bytes(int V, int H, size_t* code_bytes, size_t* scale_byte
 int mds_tile_lm_head_mxfp4(int V, int H, const void* codes, const void* scales, void* tiled, size_t tiled_bytes,
                            void* tiled_scales, size_t tiled_scale_bytes, void* stream) {
   int rc;
-  if ((rc = check_lm_head_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, tiled_bytes, tiled_scales, tiled_scale_bytes)))
+  if ((rc = check_mx_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, tiled_bytes, tiled_scales, tiled_scale_bytes)))
     return rc;
   if (!codes || !scales) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(codes, 16)) return abi_fail(MDS_ERR_INVALID_ARG, "codes must be 16-byte aligned");
@@ -215,7 +223,7 @@ int mds_tile_lm_head_mxfp4(int V, int H, const void* codes, const void* scales, 
 int mds_quantize_lm_head_mxfp4(int V, int H, const void* lm_head, void* tiled, size_t tiled_bytes, void* tiled_scales,
                                size_t tiled_scale_bytes, void* stream) {
   int rc;
-  if ((rc = check_lm_head_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, tiled_bytes, tiled_scales, tiled_scale_bytes)))
+  if ((rc = check_mx_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, tiled_bytes, tiled_scales, tiled_scale_bytes)))
     return rc;
   if (!lm_head) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(lm_head, 16)) return abi_fail(MDS_ERR_INVALID_ARG, "lm_head must be 16-byte aligned");
@@ -228,7 +236,7 @@ int mds_quantize_lm_head_mxfp4(int V, int H, const void* lm_head, void* tiled, s
 
 int mds_unpack_lm_head_mxfp4(int V, int H, const void* tiled, const void* tiled_scales, void* lm_head, void* stream) {
   int rc;
-  if ((rc = check_lm_head_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, mx_code_bytes(V, H), tiled_scales, mx_scale_bytes(V, H))))
+  if ((rc = check_mx_matrix(V, H)) || (rc = check_mx_tiled(V, H, tiled, mx_code_bytes(V, H), tiled_scales, mx_scale_bytes(V, H))))
     return rc;
   if (!lm_head) return abi_fail(MDS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(lm_head, 16)) return abi_fail(MDS_ERR_INVALID_ARG, "lm_head must be 16-byte aligned");
@@ -252,6 +260,9 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
   // (112 rows are addressed with 32-bit offsets)
   if (hidden_row_stride > (1 << 22)) return abi_fail(MDS_ERR_UNSUPPORTED, "hidden_row_stride must be at most 2^22");
   if ((int64_t)((V + 63) / 64) * ((rows + 15) / 16) > (1 << 30)) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
+  const mds::LmHeadMxPlan plan = mds::lm_head_mx_plan(rows, V);
+  if (!plan.few && !launchable((int64_t)(plan.v_tiles + 7) / 8 * 8 * plan.row_tiles))
+    return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   if (!aligned(hidden, 16) || !aligned(lm_head, 16) || !aligned(scales, 4))
     return abi_fail(MDS_ERR_INVALID_ARG, "hidden and lm_head must be 16-byte aligned, scales 4-byte aligned");
   out_req_stride = step(B, out_req_stride);

@@ -20,3 +20,23 @@ def test_rotations_of_too_many_heads():
         assert b"too many heads" in mds._lib().mds_last_error()
         assert _rope(T, max(Hq - Hk, 1), Hk, D, True) == -2, (T, Hq, Hk, D)
         assert b"too many heads" in mds._lib().mds_last_error()
+
+
+def test_matrices_of_too_many_tiles():
+    lib = mds._lib()
+    for V, H in ((1 << 22, 32768), ((1 << 24) - 1, 65536), ((1 << 24) - 1, 8192)):
+        n, m = mds.lm_head_mxfp4_bytes(V, H)
+        codes, scales, tiled, ts = FAKE, FAKE + (1 << 40), FAKE + (1 << 41), FAKE + (1 << 42)
+        assert lib.mds_tile_lm_head_mxfp4(V, H, codes, scales, tiled, n, ts, m, None) == -2
+        assert b"too large" in lib.mds_last_error()
+        assert lib.mds_quantize_lm_head_mxfp4(V, H, codes, tiled, n, ts, m, None) == -2
+        assert b"too large" in lib.mds_last_error()
+        assert lib.mds_unpack_lm_head_mxfp4(V, H, tiled, ts, codes, None) == -2
+        assert b"too large" in lib.mds_last_error()
+
+
+def test_logits_of_too_many_work_groups():
+    lib = mds._lib()
+    B, K, V, H = 65535, 64, 262000, 128
+    assert lib.mds_lm_head_mxfp4(B, K, V, H, FAKE, H, FAKE, FAKE, FAKE, mds.BF16, K * V, V, None) == -2
+    assert b"too many work-groups" in lib.mds_last_error()
