@@ -12,6 +12,9 @@ inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 inline int hip_fail(hipError_t e) { return abi_fail(MDS_ERR_HIP, hipGetErrorString(e)); }
 
+// A launch's threads are counted in 32 bits.
+inline bool launchable(int threads, long long groups) { return groups < ((1LL << 32) + threads - 1) / threads; }
+
 // A dimension of one element is never stepped along: its stride may be anything, and counts as 0.
 inline int64_t step(int64_t n, int64_t stride) { return n <= 1 ? 0 : stride; }
 

@@ -27,9 +27,6 @@ int check_out(const void* p, int T, int64_t ts, int H, int64_t hs, int D) {
   return MDS_OK;
 }
 
-// Work-groups of 256 threads that a launch can have: its threads are counted in 32 bits
-bool launchable(long long groups) { return groups < (1LL << 24); }
-
 // The sizes of both rotations
 int check_rope_sizes(int T, int Hq, int Hk, int D, int per_key_head) {
   int rc;
@@ -38,7 +35,7 @@ int check_rope_sizes(int T, int Hq, int Hk, int D, int per_key_head) {
   if (Hq < 1 || Hq > 1024) return abi_fail(MDS_ERR_INVALID_ARG, "query heads must be in [1, 1024]");
   if (D % 16 || D > 256) return abi_fail(MDS_ERR_UNSUPPORTED, "the head dimension must be a multiple of 16, at most 256");
   const int heads = Hq + per_key_head * Hk;
-  if ((long long)T * heads >= 0x7FFFFFFFLL || !launchable(((long long)T * mds::rope_plan(T, heads, D).per_token + 3) / 4))
+  if ((long long)T * heads >= 0x7FFFFFFFLL || !launchable(256, ((long long)T * mds::rope_plan(T, heads, D).per_token + 3) / 4))
     return abi_fail(MDS_ERR_UNSUPPORTED, "too many heads in one call");
   return MDS_OK;
 }
@@ -93,7 +90,7 @@ size_t mx_scale_bytes(int V, int H) { return (size_t)((V + 15) / 16) * 256 * ((H
 int check_mx_matrix(int V, int H) {
   const int rc = check_lm_head_matrix(V, H);
   if (rc) return rc;
-  if (!launchable((long long)((V + 15) / 16) * ((H + 511) / 512))) return abi_fail(MDS_ERR_UNSUPPORTED, "the matrix is too large");
+  if (!launchable(256, (long long)((V + 15) / 16) * ((H + 511) / 512))) return abi_fail(MDS_ERR_UNSUPPORTED, "the matrix is too large");
   return MDS_OK;
 }
 
@@ -261,7 +258,7 @@ int mds_lm_head_mxfp4(int B, int K, int V, int H, const void* hidden, int64_t hi
   if (hidden_row_stride > (1 << 22)) return abi_fail(MDS_ERR_UNSUPPORTED, "hidden_row_stride must be at most 2^22");
   if ((int64_t)((V + 63) / 64) * ((rows + 15) / 16) > (1 << 30)) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   const mds::LmHeadMxPlan plan = mds::lm_head_mx_plan(rows, V);
-  if (!plan.few && !launchable((int64_t)(plan.v_tiles + 7) / 8 * 8 * plan.row_tiles))
+  if (!plan.few && !launchable(256, (int64_t)(plan.v_tiles + 7) / 8 * 8 * plan.row_tiles))
     return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   if (!aligned(hidden, 16) || !aligned(lm_head, 16) || !aligned(scales, 4))
     return abi_fail(MDS_ERR_INVALID_ARG, "hidden and lm_head must be 16-byte aligned, scales 4-byte aligned");

@@ -269,7 +269,10 @@ int mds_paged_attention_sinks(int T, int B, int Hq, int Hkv, int D, const void* 
   const mds::AttnPlan p = mds::attn_plan(T, B, Hkv, Hq / Hkv, D, max_q_len, max_seq_len, sinks_window(window, sinks),
                                          window > 0 && sinks > 0, a.e4m3);
   if (workspace_bytes < p.total) return abi_fail(MDS_ERR_WORKSPACE, "workspace too small for paged attention");
-  if ((long long)p.tiles * Hkv * p.n_chunks > 0x7FFFFFFFLL) return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
+  const long long groups = (long long)p.tiles * Hkv;
+  if (!launchable(64 * p.key_groups * (p.rows > 32 ? p.rows / 32 : 1), groups * p.n_chunks) ||
+      (p.n_chunks > 1 && !launchable(256, groups)))
+    return abi_fail(MDS_ERR_UNSUPPORTED, "too many work-groups");
   a.T = T;
   a.B = B;
   a.Hq = Hq;

@@ -40,3 +40,16 @@ def test_logits_of_too_many_work_groups():
     B, K, V, H = 65535, 64, 262000, 128
     assert lib.mds_lm_head_mxfp4(B, K, V, H, FAKE, H, FAKE, FAKE, FAKE, mds.BF16, K * V, V, None) == -2
     assert b"too many work-groups" in lib.mds_last_error()
+
+
+def test_attention_of_too_many_work_groups():
+    # (work-groups of four waves: four key groups, or the four row groups of a prompt's tile)
+    lib = mds._lib()
+    for T, B, Hq, Hk, max_q in ((65535, 65535, 1024, 1024, 1), (65535, 65535, 257, 257, 1), (1 << 22, 4, 1024, 1024, 1 << 20)):
+        q, pages = [FAKE, Hq * 64, 64], [16 * Hk * 64, Hk * 64, 64]
+        for window, sinks in ((0, 0), (4096, 4)):
+            rc = lib.mds_paged_attention_sinks(T, B, Hq, Hk, 64, *q, FAKE, FAKE, mds.BF16, 16, 8, *pages, *pages, FAKE, B, 4096,
+                                               None, FAKE, FAKE, max_q, 20000, 0.125, 1, window, sinks, None, None, *q, None, FAKE,
+                                               1 << 50, None)
+            assert rc == -2, (T, Hk, window)
+            assert b"too many work-groups" in lib.mds_last_error()
