@@ -234,8 +234,11 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, train
         _need(trained_len >= 1 and beta_fast > beta_slow > 0, "yarn scaling needs trained_len and beta_fast > beta_slow > 0")
         lo, hi = (rotary_dim * math.log(trained_len / (turns * 2 * math.pi)) / (2 * math.log(base))
                   for turns in (beta_fast, beta_slow))
-        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
-        ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        if hi <= 0:  # even the fastest pair turns beta_slow times at most
+            ramp = torch.ones_like(i)
+        else:
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
+            ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0, 1)
         f, rope_scale = f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
     elif scaling not in ("none", "ntk"):
         raise MdsError(f"unknown scaling {scaling!r}")

@@ -53,3 +53,18 @@ def test_attention_of_too_many_work_groups():
                                                1 << 50, None)
             assert rc == -2, (T, Hk, window)
             assert b"too many work-groups" in lib.mds_last_error()
+
+
+def test_by_parts_frequencies_whose_pairs_are_all_slow_or_all_fast():
+    # pairs that turn less than beta_slow times within the trained positions are divided by factor, the first one too; those
+    # of more than beta_fast are kept
+    import math
+    import numpy as np
+    for dim, base, trained, fast, slow in ((64, 10000.0, 6, 32.0, 1.0), (64, 10000.0, 1, 2.0, 0.5), (128, 5e5, 128, 64.0, 32.0),
+                                           (16, 1.5, 1 << 20, 32.0, 1.0), (2, 10000.0, 3, 32.0, 1.0)):
+        f, _ = mds.rope_frequencies(dim, base=base, device="cpu")
+        g, _ = mds.rope_frequencies(dim, base=base, scaling="yarn", factor=8.0, trained_len=trained, beta_fast=fast,
+                                    beta_slow=slow, device="cpu")
+        turns, ratio = trained * f.numpy() / (2 * math.pi), g.numpy() / f.numpy()
+        assert (turns < slow).all() or (turns > fast).all()
+        assert np.allclose(ratio, 0.125 if turns[0] < slow else 1.0, rtol=1e-12), (dim, trained)
