@@ -48,6 +48,12 @@ __device__ __forceinline__ float scale_of(uint32_t word, int i) { return __uint_
 template <int COLS>
 constexpr int kOutStride = COLS + 4;
 
+// A wave's LDS operations keep their order, and so must the compiler where lanes read what others of the wave wrote.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Where a hidden row's logits start
 __device__ __forceinline__ long long row_at(const LmHeadMxArgs& a, int m) {
   const int b = m / a.K;
@@ -172,6 +178,7 @@ __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
         if (i < n) {
 #pragma unroll
           for (int j = 0; j < NG; ++j) *(u32x4*)(s_x + put[j]) = X[p][j];
+          wave_lds();
           float sc[NBW];
 #pragma unroll
           for (int nb = 0; nb < NBW; ++nb) sc[nb] = scale_of(S[p][nb], i & 3);
@@ -189,6 +196,7 @@ __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
                 acc[nb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, x[mb], acc[nb][mb], 0, 0, 0);
             }
           }
+          wave_lds();
         }
         load(p, i + NP);
       }
@@ -357,12 +365,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb) *(floatx4*)(so + lr * kOut + nb * 16 + lg * 4) = acc[nb][mb];
+    wave_lds();
     store_rows<NBW * 16>(
         a, lane, 64, min(16, a.M - m0 - mb * 16), vb0 * 16, [&](int r) { return s_at[mb * 16 + r]; },
         [&](int r, int c, auto cols) {
           using T = typename std::conditional<decltype(cols)::value == 4, floatx4, float>::type;
           return *(const T*)(so + r * kOut + c);
         });
+    if (mb + 1 < MB) wave_lds();
   }
 }
 
