@@ -13,13 +13,16 @@
 //
 // An e4m3 code is a sixteenth of its value: where the quotient is next to the
 // border of two codes, the last bit of float32 decides. So that float32 decides
-// alike wherever a key is computed, every factor here is the float32 nearest to
-// its exact value (sine and cosine, 1 / sqrt), products are rounded one by one and
-// squares are summed fours in turn and then neighbours (neighbouring columns,
-// but where only part of a head is turned and that in halves). (Heads of 128:
-// with float32 sines and fused products three codes in a million fell on the
-// other side than by separate operations, now none of 43 million; the prompt
-// below takes 76.1 us and took 75.3.)
+// alike wherever a key is computed, sines and cosines here are the float32
+// nearest to those of the float64 angle, at far positions too, and 1 / sqrt that
+// nearest to the root of the float32 mean (but where float64 cannot tell which of
+// two is nearer, some 1 in 10^7), products are rounded one by one and squares are
+// summed fours in turn and then neighbours. (That is the columns' order, except
+// where a part of a head is turned in halves: there a lane's two eights of columns
+// are R / 2 apart, and the sum may differ in its last bits.) (Heads of 128: with
+// float32 sines and fused products three codes in a million fell on the other side
+// than by separate operations, now none of 43 million; the prompt below takes
+// 76.1 us and took 75.3.)
 //
 // A wave takes some heads of one token, LPH lanes a head and 16 columns a lane:
 // two pieces of 16 bytes, which in either layout are whole pairs (columns 8 j
@@ -122,10 +125,14 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int per_token) {
   long long slot = 0;
   if constexpr (TO != kRows) slot = a.slot_map[t];
   for (int i = lane; i < a.R >> 1; i += 64) {
-    // turns of the angle without the whole ones, at most half a turn either way
-    const double turns = pos * a.inv_freq[i] * 0.15915494309189535;
+    // The angle's turns without the whole ones. An angle is rounded once, its turns are not: the product with 1 / (2 pi)
+    // is a sum of two, so that a far position's sine is that of its angle. (Fused, the difference would have the rest already.)
+#pragma clang fp contract(off)
+    constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnRest = -0x1.6b01ec5417056p-57;
+    const double angle = pos * a.inv_freq[i], turns = angle * kTurn;
+    const double rest = __builtin_fma(angle, kTurnRest, __builtin_fma(angle, kTurn, -turns));
     double s, c;
-    sincospi(2.0 * (turns - __builtin_rint(turns)), &s, &c);
+    sincospi(2.0 * ((turns - __builtin_rint(turns)) + rest), &s, &c);
     s_turn[w][i] = make_float2((float)(c * a.rope_scale), (float)(s * a.rope_scale));
   }
   // (a wave's LDS operations keep their order)
