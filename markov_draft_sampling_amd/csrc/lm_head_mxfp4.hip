@@ -15,11 +15,11 @@
 // operands agree: its slice s has columns 32 g + 8 s .. + 7 of each g. Scales of
 // four tiles in a row of tiles are the bytes of a lane's word.
 //
-// Up to some 50 rows the call is bound by the matrix's 17 / 32 V H bytes (H = 4096: one row, V = 200064 73 us and 6.0
-// TB/s; 7 rows, V = 151936 57 us; 32 rows, V = 200064 90 us), above by the matrix cores, the widening and the operand
-// reads from LDS (224 rows: V = 200064 280 us and 1.31 PFLOP/s, V = 151936 221 us). Small vocabularies take a
-// work-group's start and its chain of loads (7 rows, V = 4099 8 us). (Pairs at the rules below are from one run each;
-// cards differ by up to 8%.)
+// Up to some 50 rows the call is bound by the matrix's 17 / 32 V H bytes (H = 4096: one row, V = 200064 72 us and 6.1
+// TB/s; 7 rows, V = 151936 59 us; 32 rows, V = 200064 89 us), above by the matrix cores, the widening and the operand
+// reads from LDS (224 rows: V = 200064 284 us and 1.29 PFLOP/s, V = 151936 227 us). Small vocabularies take a
+// work-group's start and its chain of loads (7 rows, V = 4099 7 us). (Times at the rules below are of this code on one
+// card, the two sides in turn; those of what is not kept are of the build that had it. Cards differ by up to 8%.)
 #include <type_traits>
 
 #include "mds_device.h"
@@ -43,8 +43,8 @@ __device__ __forceinline__ bf16x8 widen(uint32_t codes, float scale) {
 __device__ __forceinline__ float scale_of(uint32_t word, int i) { return __uint_as_float((word >> (8 * i) & 0xFFu) << 23); }
 
 // Logits go out by way of LDS, as rows of consecutive columns (four floats of padding keep rows apart in the banks): a
-// row's run of them in one piece, also where rows are not aligned and every logit is a store of its own (224 rows, V = 100003:
-// 163 us, by stores of a lane's own four logits 201; V = 151936 221 and 228).
+// row's run of them in one piece, also where rows are not aligned and every logit is a store of its own (when it was built: 224
+// rows, V = 100003 163 us, by stores of a lane's own four logits 201; V = 151936 221 and 228).
 template <int COLS>
 constexpr int kOutStride = COLS + 4;
 
@@ -115,7 +115,7 @@ __device__ __forceinline__ void store_rows(const LmHeadMxArgs& a, int i, int n, 
 template <int NG, int NBW>
 __global__ __launch_bounds__(256) void lm_head_mx_kernel(LmHeadMxArgs a) {
   constexpr int MB = (NG + 3) / 4;
-  constexpr int NP = 2;  // (three, four: 16 rows, V = 200064, H = 4096 109 and 107 us against 93: fewer waves a CU)
+  constexpr int NP = 2;  // (three, four: 16 rows, V = 200064, H = 4096 108 and 107 us against 93; V = 32000 22 and 22 against 19: fewer waves a CU)
   constexpr int kOut = kOutStride<NBW * 16>;
   constexpr int kX = NG * 1024, kZ = NG * 4 * kOut * 4;  // a wave's hidden rows of a tile; in the end its sums
   __shared__ __attribute__((aligned(16))) unsigned char s[4 * (kX > kZ ? kX : kZ)];
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr int NW = 4;
   constexpr int kStage = MB * 4096;  // the hidden rows' 128 columns
   // The order within a tile: operand reads one row block ahead, the next slice's widening between this one's products (224
-  // rows, V = 131072, H = 4096: 185 us against 210 as the compiler has it). With five blocks there are no registers for it.
+  // rows, H = 4096: V = 131072 183 us against 196 as the compiler has it, four blocks at V = 200064 288 against 308). With five blocks there are no registers for it.
   constexpr bool kPinned = NBW <= 4;
   constexpr int kOut = kOutStride<NBW * 16>;
   constexpr int kOutWave = 16 * kOut * 4;  // a wave's logits of 16 rows, in the same place in the end
@@ -483,8 +483,8 @@ hipError_t launch_few(const LmHeadMxArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 // Vocabulary blocks of a work-group: four, so that the hidden rows are read less often, but fewer where that leaves CUs
-// without one, and for up to 4 rows, which cost little (H = 4096, us with one / two / four: 16 rows, V = 4099 8.5 / 9.6 /
-// 12.0, V = 32000 28 / 22 / 20; H = 2048, 4 rows, V = 151936 33 / 32 / 33, one row 33 / 29 / 32).
+// without one, and for up to 4 rows, which cost little (us with one / two / four: H = 4096, 16 rows, V = 4099 8.7 / 7.8 / 9.4,
+// V = 32000 28 / 22 / 19; H = 2048, 4 rows, V = 151936 34 / 33 / 36, one row 30 / 29 / 35).
 int few_blocks(int VB, int ng) { return VB <= 512 ? 1 : ng == 1 || VB <= 1024 ? 2 : 4; }
 template <int NG>
 hipError_t launch_few_rows(const LmHeadMxArgs& a, int nbw, hipStream_t st) {
@@ -504,9 +504,10 @@ hipError_t launch_wide(const LmHeadMxArgs& a, int tiles, int mt, hipStream_t st)
 // What a launch of the wide kernel takes, in units that a pass over a row of the matrix with one more block would add: the
 // CUs take 512 work-groups a round, each of a time that grows with its blocks of the vocabulary beside what a tile of the
 // hidden rows costs (as much as one of them); 256 or fewer at the end have a CU each and take about 0.7 of it.
-// (H = 4096, us with 1 / 2 / 3 / 4 / 5 blocks a wave, the rule's choice last: 112 rows, V = 100003 144 / 118 / 126 / 104 / 124,
-// 4; 32 rows, V = 151936 105 / 83 / 75 / 92 / 65, 5; V = 200064 143 / 110 / 107 / 104 / 106, and 90 with the rule's 7; 112
-// rows, V = 32000 41 / 39 / 44 / 54 / 66, 1; 224 rows, V = 200064 455 / 332 / 312 / 297 / 289, 5.)
+// (H = 4096, us with 1 / 2 / 3 / 4 / 5 blocks a wave, and 6 / 7 up to 64 rows; the rule's choice: 32 rows, V = 151936
+// 104 / 83 / 75 / 90 / 65 / 67 / 72, 5; 32 rows, V = 200064 144 / 110 / 108 / 103 / 106 / 113 / 88, 7; 112 rows, V = 32000
+// 41 / 41 / 45 / 54 / 67, 1; 112 rows, V = 100003 143 / 108 / 119 / 92 / 117, 4; 224 rows, V = 200064 440 / 329 / 303 / 289 /
+// 285, 5.)
 float wide_cost(int VB, int mt, int nbw) {
   const int wgs = (VB + 4 * nbw - 1) / (4 * nbw) * mt, rest = wgs % 512;
   return (float)(wgs / 512) * (float)(1 + nbw) + (rest == 0 ? 0.0f : rest <= 256 ? 0.7f : 1.0f) * (float)(1 + nbw);
@@ -518,7 +519,7 @@ int wide_blocks(int VB, int mt, int mb) {
   return best;
 }
 // Row tiles of at most 7 blocks, all of one height; lower ones while every work-group keeps a CU to itself (112 rows,
-// V = 4099, H = 4096: 28 us in one tile, three of 3 blocks 19 us).
+// V = 4099, H = 4096: 29 us in one tile, three of 3 blocks 19 us; seven of one, which share CUs, would take 15.5).
 int wide_row_tiles(int VB, int n) {
   const int least = (n + 6) / 7, alone = 256 / ((VB + 3) / 4);
   return alone > n ? n : alone > least ? alone : least;
@@ -546,8 +547,10 @@ LmHeadMxPlan lm_head_mx_plan(int M, int V) {
   const int tiles = wide_row_tiles(VB, n), mb = (n + tiles - 1) / tiles, mt = (n + mb - 1) / mb;
   const int nbw = wide_blocks(VB, mt, mb);
   // Up to 32 rows either kernel: the few rows' takes a start and a time by the vocabulary that grows with the rows, in
-  // wide_cost's units (H = 4096, us few / wide: 7 rows, V = 200064 81 / 95, V = 151936 63 / 59; 16 rows, V = 100003 54 / 48,
-  // V = 32000 20 / 24; 32 rows, V = 200064 117 / 104, V = 4099 12.5 / 16.7).
+  // wide_cost's units (H = 4096, us few / wide, the rule's choice: 7 rows, V = 151936 61 / 59, wide, V = 200064 79 / 79, wide;
+  // 16 rows, V = 32000 19 / 24, few, V = 100003 51 / 48, few; 32 rows, V = 4099 12 / 15, few, V = 32000 23.5 / 24.9, wide,
+  // V = 200064 112 / 89, wide. It misses by up to 15% where the wide one's work-groups just fill a round and the bytes bound
+  // it: 8 rows, V = 128256 52 / 60, wide).
   if (M <= 32) {
     const float few = 0.5f + (M <= 4 ? 0.55e-3f : M <= 8 ? 0.61e-3f : M <= 16 ? 0.71e-3f : 0.88e-3f) * (float)VB;
     const int ng = M <= 4 ? 1 : M <= 8 ? 2 : M <= 16 ? 4 : 8;

@@ -818,9 +818,11 @@ hipError_t launch_shape(const PagedAttnArgs& a, hipStream_t st) {
 }
 
 // With first tokens, up to 32 rows over an 8-bit cache: half the LDS and two work-groups to a CU, since a block is half as
-// long in bytes and its chain of LDS reads, widening, exponentials and products is not (8 key heads, windows over twice
-// their keys at most, against one work-group to a CU: 128 requests of one token, window 2000 58 us to 82 us, 4000 129 to
-// 146; 32 requests of 8 tokens, 4000 47 to 53; the other way 32 requests of one token, 8000 72 to 61).
+// long in bytes and its chain of LDS reads, widening, exponentials and products is not (8 key heads of 128, sequences of up
+// to twice the window; us with two work-groups to a CU / with one: 128 requests of one token, window 300 26 / 35, 2000
+// 91 / 117, 4000 168 / 187; 64 requests, 1000 28 / 39; 32 requests, 8000 98 / 105; 32 of 8 tokens, 4000 51 / 58; 8 of one
+// token, whose keys are split, 8000 27 / 29. Heads of 64: 24 / 31, 76 / 93, 135 / 148; 28 / 34; 71 / 72; 43 / 43; 27 / 27).
+// Calls without first tokens, windowed or not, keep one.
 template <int D, bool E4M3, bool SINKS>
 hipError_t launch_d(const PagedAttnArgs& a, int rows, int key_groups, hipStream_t st) {
   if constexpr (E4M3 && SINKS) {
@@ -898,8 +900,11 @@ AttnPlan attn_plan(int T, int B, int Hkv, int G, int D, int max_q_len, long long
     if (span <= 1024 && wgs > 512) p.key_groups = 1;
     if (span <= 512 && wgs > 256 && wgs <= 512) p.key_groups = 2;
   }
-  // With first tokens beside a window all sequences beyond it are as long, so the places beside a work-group matter up
-  // to longer ones (one token, 8 key heads, a window over twice its keys at most; us with one / two / four key groups:
+  // Sequences beyond a window all have as many keys to read, so the places beside a work-group matter up to longer ones.
+  // That is so of any window; it is looked at for calls with first tokens only, and a window without them keeps the rule
+  // above (128 requests of one token over an 8-bit cache, 8 key heads, window 2000, up to twice as many keys: 91 us with
+  // first tokens and 114 us without; 64 over a bf16 cache, window 512: 28 and 34). (One token, 8 key heads, sequences of up to
+  // twice the window; us with one / two / four key groups:
   // 64 requests, window 300 30 / 22 / 27, 1000 57 / 42 / 48, 4000 172 / 162 / 163; 128 requests, 300 35 / 39 / 59,
   // 2000 165 / 164 / 166, 4000 293 / 301 / 287; over 8-bit caches, whose work-groups are two to a CU already, 128
   // requests with two / four, 300 25 / 31, 1000 48 / 48, 2000 108 / 101).

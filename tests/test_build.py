@@ -89,6 +89,8 @@ def test_the_module_refuses_another_library_or_torch(tmp_path, abi, torch_versio
     # the real module beside a library that has its entry points and some version
     import torch
     import markov_draft_sampling_amd as mds
+    if not os.path.exists(b.CALLS):
+        b.build()
     version = mds.abi_version() + abi
     (tmp_path / "lib.cpp").write_text("".join(f'extern "C" int {n}() {{ return 0; }}\n' for n in _ENTRIES)
                                       + f'extern "C" int mds_abi_version() {{ return {version}; }}\n')
