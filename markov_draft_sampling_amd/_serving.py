@@ -22,7 +22,7 @@ _c_sz = ctypes.c_size_t
 # compared by its index, pointers are plain integers (0: NULL), the stream is asked for once, and the arguments of the
 # calls of a step go over packed (39 ctypes arguments cost 3.6 us, packed 0.9). Those whose checks would
 # outlast their kernels all the same are checked and called by _calls, which is compiled; where it is not built, attention
-# is called from here (10 us of host time instead of 7) and the others raise an error that says so.
+# is called from here (11 to 13 us of host time for one token instead of 8) and the others raise an error that says so.
 
 
 def _current_stream(index):
@@ -48,7 +48,7 @@ def _call(what, fn, index, stream, args):
 
 # mds_call_packed's numbers and the arguments' layout: 8 bytes each, floats as doubles
 _PACKED = {name: (i, struct.Struct("".join("d" if t is ctypes.c_float else "q" for t in _SIGS["mds_" + name][0][:-1])))
-           for i, name in ((0, "kv_page_tables"), (1, "kv_append"), (3, "lm_head_fp8"))}
+           for i, name in ((0, "kv_page_tables"), (1, "kv_append"), (2, "paged_attention"), (3, "lm_head_fp8"))}
 
 
 def _packed(what, index, stream, args):
@@ -61,24 +61,27 @@ def _packed(what, index, stream, args):
     _call(what, _lib().mds_call_packed, index, stream, (call, data, len(args)))
 
 
-_CALLS = None
+_CALLS = None  # the module of the compiled calls, once it is loaded; False: there is none for this interpreter
 
 
 def _calls(needed=True):
-    """The module of the compiled calls; None where there is none for this interpreter and it is not needed."""
+    """The module of the compiled calls; None where there is none and it is not needed."""
     global _CALLS
+    how = "build them with `python -m markov_draft_sampling_amd.build`"
     if _CALLS is None:
         _lib()
-        if not needed and importlib.util.find_spec("._calls", __package__) is None:
-            return None
-        try:
-            from . import _calls as m
-        except ImportError as e:
-            raise MdsError(f"the compiled calls do not load ({e}): build them with "
-                           "`python -m markov_draft_sampling_amd.build`") from None
-        m.set_error(MdsError)
-        _CALLS = m
-    return _CALLS
+        if importlib.util.find_spec("._calls", __package__) is None:
+            _CALLS = False
+        else:
+            try:
+                from . import _calls as m
+            except ImportError as e:
+                raise MdsError(f"the compiled calls do not load ({e}): {how}") from None
+            m.set_error(MdsError)
+            _CALLS = m
+    if needed and not _CALLS:
+        raise MdsError(f"there are no compiled calls for this interpreter: {how}")
+    return _CALLS or None
 
 
 def _compiled(fn, index, stream, *args):
@@ -329,9 +332,13 @@ def _attention(dev, stream, q, k_pages, v_pages, block_table, query_start, seq_l
     args = (T, B, Hq, Hk, D, *_heads(q, (T, Hq, D), dev, "q"), k_pages.data_ptr(), v_pages.data_ptr(), code, P, NP, *kp[:3],
             *vp[:3], _vec(block_table, _I32, N * MP, dev, "block_table"), N, MP, _opt(idx_map, _I32, B, dev, "idx_map"),
             _vec(query_start, _I32, B + 1, dev, "query_start"), _vec(seq_lens, _I32, B, dev, "seq_lens"), max_q_len,
-            max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, sinks,
+            max_seq_len, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0,
+            *((window, sinks) if sinks else (window,)),
             _opt(k_scale, _F32, Hk, dev, "k_scale"), _opt(v_scale, _F32, Hk, dev, "v_scale"),
             *_heads(out, (T, Hq, D), dev, "out"), _opt(lse, _F32, T * Hq, dev, "lse"), workspace.data_ptr(), workspace.numel())
+    if not sinks:
+        _packed("paged_attention", dev, stream, args)
+        return
     try:
         _ATTENTION.pack(*args)  # (ctypes would cut integers to their types' size)
     except struct.error as e:

@@ -22,6 +22,8 @@ def test_a_package_without_the_module(tmp_path):
 import torch, markov_draft_sampling_amd as mds
 from markov_draft_sampling_amd import _serving
 assert mds.abi_version() == 2 and _serving._calls(needed=False) is None
+_serving.importlib.util.find_spec = None  # (looked for once)
+assert _serving._calls(needed=False) is None
 x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
 for call in (lambda: mds.qk_norm_rope(x, x, x, None, x, x), lambda: mds.lm_head_mxfp4(x[0], x, x, x, 1)):
     try:
@@ -64,13 +66,17 @@ def test_its_arguments_reach_the_library(monkeypatch):
     _serving._attention(-1, None, *_args(q=torch.zeros((0, 4, 64), dtype=torch.bfloat16), lse=None, idx_map=torch.zeros(
         2, dtype=torch.int32), out=torch.zeros((0, 4, 64), dtype=torch.bfloat16)).values())
     assert got.pop() == 0  # nothing to do
+    _serving._attention(-1, None, *_args(max_seq_len=100000, window=0, sinks=0).values())
+    assert got.pop() == -3
     for bad, rc in ((dict(window=-1), -1), (dict(sinks=-1), -1), (dict(max_seq_len=-1), -1), (dict(scale=-1.0), -1),
+                    (dict(sinks=0, max_q_len=1 << 32), -1),
                     (dict(k_scale=torch.ones(2)), -1)):
         _serving._attention(-1, None, *_args(**bad).values())
         assert got.pop() == rc, bad
 
 
 @pytest.mark.parametrize("bad", [dict(max_q_len=1 << 32), dict(max_seq_len=1 << 70), dict(window=2.5), dict(sinks=1 << 31),
+                                 dict(sinks=0, window=2.5),
                                  dict(scale="x"), "q", "out", "block_table", "query_start", "seq_lens", "workspace", "lse",
                                  "k_pages", "v_pages"])
 def test_its_refusals(monkeypatch, bad):
