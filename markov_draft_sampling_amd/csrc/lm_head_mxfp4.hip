@@ -509,7 +509,7 @@ hipError_t launch_wide(const LmHeadMxArgs& a, int tiles, int mt, hipStream_t st)
 // 41 / 41 / 45 / 54 / 67, 1; 112 rows, V = 100003 143 / 108 / 119 / 92 / 117, 4; 224 rows, V = 200064 440 / 329 / 303 / 289 /
 // 285, 5.)
 float wide_cost(int VB, int mt, int nbw) {
-  const int wgs = (VB + 4 * nbw - 1) / (4 * nbw) * mt, rest = wgs % 512;
+  const long long wgs = (long long)((VB + 4 * nbw - 1) / (4 * nbw)) * mt, rest = wgs % 512;
   return (float)(wgs / 512) * (float)(1 + nbw) + (rest == 0 ? 0.0f : rest <= 256 ? 0.7f : 1.0f) * (float)(1 + nbw);
 }
 int wide_blocks(int VB, int mt, int mb) {

@@ -29,6 +29,7 @@ def test_lm_head_plan_refusals():
     assert f(1, 1, 1000, 200, out) == -2
     with pytest.raises(ctypes.ArgumentError):
         f(1, 1, 1000, "128", out)
+    assert f(65535, 64, (1 << 24) - 1, 128, out) == 0 and tuple(out) == (0, 7, 5)  # (work-groups counted in 64 bits)
 
 
 def test_every_rotation_variant_has_a_case():
